@@ -1,0 +1,323 @@
+// Causal attention over packed prompts (awq_attn_prompt in awq_block.h).
+//
+// One pass over the keys with a running maximum and sum per row (float32, base 2). A
+// workgroup owns 128 query rows of one head (four wavefronts of 32) and walks over the keys
+// in tiles of 64 that all four share through LDS.
+//
+// Both products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with the 32 x 32 x 16
+// matrix instruction: lane l then holds scores of one query (column l % 32) for 16 keys per
+// tile, so the softmax statistics are per lane (one exchange with lane l ^ 32), the factor
+// that rescales O is one register, and P never changes lanes: the keys a lane holds after
+// S^T, in order, are the contraction slots it feeds to O^T, and the V^T operand is read
+// from LDS in that order with the transposing 16-bit read.
+//
+// The K and V tiles go from memory straight into LDS (16 bytes per lane, no registers), two
+// tiles deep, one barrier per tile. Rows are 2 D bytes without padding; the 16-byte chunks
+// of a row are permuted (below) so that the rows one LDS access touches fall into different
+// banks. Elements past D and rows past the sequence read as 0.
+#include "block_internal.hpp"
+
+namespace awq {
+namespace {
+
+constexpr int kBQ = 128;  // query rows per workgroup
+constexpr int kBK = 64;   // keys per tile
+
+struct PromptArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  const int32_t* cu;
+  int64_t q_token, k_token, v_token, o_token, q_head, k_head, v_head, o_head;
+  int32_t tokens, seqs, tiles, q_heads, group, head_dim;
+  float c;  // scale * log2(e)
+};
+
+// chunk position of chunk c of row r in LDS. K is read 16 rows at one chunk, V 4 rows x 64
+// bytes; with 128-byte rows (DP = 64) two rows share a 256-byte line.
+template <int DP>
+__device__ __forceinline__ int k_pos(int r, int c) {
+  return DP == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
+}
+template <int DP>
+__device__ __forceinline__ int v_pos(int r, int c) {
+  return DP == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
+}
+
+// Finds the sequence of query tile `tile` (tiles are numbered sequence by sequence): 64
+// sequences at a time, one per lane. Returns false past the last tile.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int& start, int& len, int& in_seq) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
+    const int b = b0 + lane;
+    int s = 0, n = 0;
+    if (b < a.seqs) {
+      s = min(max(a.cu[b], 0), a.tokens);
+      n = max(min(a.cu[b + 1], a.tokens) - s, 0);
+    }
+    const int mine = (n + kBQ - 1) / kBQ;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int other = __shfl_up(upto, d);
+      if (lane >= d) upto += other;
+    }
+    const uint64_t past = __ballot(before + upto > tile);
+    if (past != 0) {
+      const int w = __builtin_ctzll(past);
+      start = __builtin_amdgcn_readlane(s, w);
+      len = __builtin_amdgcn_readlane(n, w);
+      in_seq = tile - before - __builtin_amdgcn_readlane(upto - mine, w);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
+  constexpr int RB = DP * 2;            // bytes of a row in LDS
+  constexpr int RC = DP / 8;            // 16-byte chunks of a row
+  constexpr int TILE = kBK * RB;        // bytes of a K or V tile
+  constexpr int ROWS = 1024 / RB;       // rows one load instruction of a wavefront fills
+  constexpr int LOADS = kBK / ROWS / 4;  // load instructions per wavefront and tile
+  constexpr int NC = DP / 16, ND = DP / 32;
+  typedef typename T::v8 v8;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [2][K tile, V tile]
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 31, h = lane >> 5;
+
+  const int head = blockIdx.x % a.q_heads;
+  int start, len, in_seq;
+  if (!find_tile(a, a.tiles - 1 - static_cast<int>(blockIdx.x / a.q_heads), start, len, in_seq)) return;
+  start = __builtin_amdgcn_readfirstlane(start);
+  len = __builtin_amdgcn_readfirstlane(len);
+  const int q0 = __builtin_amdgcn_readfirstlane(in_seq) * kBQ;
+  const int kv_head = head / a.group;
+  const int wq0 = q0 + 32 * wave;    // this wavefront's first row
+  const int row = wq0 + col;         // this lane's row
+
+  const uint16_t* kbase = a.k + start * a.k_token + kv_head * a.k_head;
+  const uint16_t* vbase = a.v + start * a.v_token + kv_head * a.v_head;
+
+  // tile loads: instruction j of wavefront w fills rows ROWS (LOADS w + j).., lane l row
+  // l / RC of them, chunk position l % RC
+  uint32_t k_off[LOADS], v_off[LOADS];
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int r = ROWS * (LOADS * wave + j) + lane / RC;
+    const int ck = k_pos<DP>(r, lane % RC), cv = v_pos<DP>(r, lane % RC);
+    k_off[j] = 8 * ck < a.head_dim ? static_cast<uint32_t>(r * a.k_token + 8 * ck) * 2 : kNoLoad;
+    v_off[j] = 8 * cv < a.head_dim ? static_cast<uint32_t>(r * a.v_token + 8 * cv) * 2 : kNoLoad;
+  }
+  auto load_tile = [&](int kv0, int buf) {
+    const int rows = min(kBK, len - kv0);
+    const __amdgpu_buffer_rsrc_t rk =
+        make_rsrc(kbase + kv0 * a.k_token, static_cast<uint32_t>((rows - 1) * a.k_token + a.head_dim) * 2);
+    const __amdgpu_buffer_rsrc_t rv =
+        make_rsrc(vbase + kv0 * a.v_token, static_cast<uint32_t>((rows - 1) * a.v_token + a.head_dim) * 2);
+    unsigned char* dst = smem + buf * 2 * TILE + LOADS * wave * 1024;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void*)(dst + j * 1024), 16,
+                                               static_cast<int>(k_off[j]), 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void*)(dst + TILE + j * 1024), 16,
+                                               static_cast<int>(v_off[j]), 0, 0, 0);
+  };
+
+  const int kv_end = min(len, q0 + kBQ);  // keys this workgroup needs
+  load_tile(0, 0);
+
+  // Q^T operand: column l % 32, channels 16 c + 8 h .. + 7 (rows past the sequence: 0)
+  v8 qf[NC];
+  {
+    const int rows = min(kBQ, len - q0);
+    const __amdgpu_buffer_rsrc_t rq =
+        make_rsrc(a.q + (start + q0) * a.q_token + head * a.q_head,
+                  static_cast<uint32_t>((rows - 1) * a.q_token + a.head_dim) * 2);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int d = 16 * c + 8 * h;
+      const uint32_t off =
+          d < a.head_dim ? static_cast<uint32_t>((32 * wave + col) * a.q_token + d) * 2 : kNoLoad;
+      qf[c] = __builtin_bit_cast(v8, buf_load16(rq, off, 0));
+    }
+  }
+
+  float16_t acc[ND];
+#pragma unroll
+  for (int t = 0; t < ND; ++t)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
+  // P carries a factor 2^kShift: with the maximum at most kSlack above the one in use,
+  // binary16 holds it, and probabilities down to 2^-21 of the maximum keep their digits
+  constexpr float kShift = 7.0f, kSlack = 8.0f;
+  float m = kNegInf;  // maximum in use, in units of scores * c
+  float l = 0.0f;     // this lane's part of the sum
+
+  // LDS read positions
+  const int tr_row = 4 * h + ((lane & 15) >> 2);                       // + 16 cc + 32 s (+ 8)
+  const int tr_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);      // + 4 dt
+  const int tr_byte = 8 * (lane & 1);
+
+  int buf = 0;
+  for (int kv0 = 0; kv0 < kv_end; kv0 += kBK, buf ^= 1) {
+    __builtin_amdgcn_s_waitcnt(0);  // this wavefront's loads of the tile have landed
+    __syncthreads();                // everyone's have, and the other buffer is free
+    if (kv0 + kBK < kv_end) load_tile(kv0 + kBK, buf ^ 1);
+    if (kv0 > wq0 + 31) continue;   // above the diagonal for this wavefront
+    const unsigned char* ks = smem + buf * 2 * TILE;
+    const unsigned char* vs = ks + TILE;
+
+    float16_t s[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int r = 32 * t + col;
+        const v8 kf = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 2 * c + h));
+        s[t] = T::mfma32(kf, qf[c], s[t]);
+      }
+    }
+    if (kv0 + kBK - 1 > wq0) {  // the tile reaches past some row of the wavefront
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = kv0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
+          s[t][i] = key <= row ? s[t][i] : kNegInf;
+        }
+    }
+    float top = kNegInf;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+    top = xor32_max(top) * a.c;
+    // rescale only when some row's maximum grew by more than the slack
+    if (__ballot(top > m + kSlack) != 0) {
+      const float m_new = fmaxf(m, top);
+      const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= keep;
+#pragma unroll
+      for (int t = 0; t < ND; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[t][i] *= keep;
+    }
+    const float off = m == kNegInf ? 0.0f : kShift - m;
+    u32x4 p[4];  // P^T operands of the four 16-key steps
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], a.c, off));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i + 1], a.c, off));
+        l += e0 + e1;
+        p[2 * t + (i >> 3)][(i >> 1) & 3] = T::pack2(e0, e1);
+      }
+#pragma unroll
+    for (int cc = 0; cc < 4; ++cc) {
+      const v8 pf = __builtin_bit_cast(v8, p[cc]);
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt) {
+        const int r0 = 16 * cc + tr_row, r1 = r0 + 8;
+        const int ch = 4 * dt + tr_chunk;
+        const short4_t lo = lds_read_tr(vs + r0 * RB + 16 * v_pos<DP>(r0, ch) + tr_byte);
+        const short4_t hi = lds_read_tr(vs + r1 * RB + 16 * v_pos<DP>(r1, ch) + tr_byte);
+        acc[dt] = T::mfma32(join8<v8>(lo, hi), pf, acc[dt]);
+      }
+    }
+  }
+
+  l = xor32_add(l);
+  const float inv = inv_sum(l);
+  bool broken = false;
+  uint16_t* o = a.out + (start + row) * a.o_token + head * a.o_head;
+#pragma unroll
+  for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      float v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = acc[dt][i + e] * inv;
+        broken |= v[e] != v[e];
+      }
+      const int d = 32 * dt + 2 * i + 4 * h;
+      if (row < len && d < a.head_dim)
+        *reinterpret_cast<uint2*>(o + d) = make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
+    }
+  // rows that came out NaN: again, key by key (a masked infinity or NaN may be the cause)
+  uint64_t again = __ballot(broken && row < len);
+  again = (again | (again >> 32)) & 0xFFFFFFFFu;
+  while (again != 0) {
+    const int i = __builtin_ctzll(again);
+    again &= again - 1;
+    const int t = wq0 + i;
+    float mr, lr;
+    float2_t orow;
+    attend_row<T>(a.q + (start + t) * a.q_token + head * a.q_head, a.head_dim, a.c, 0, t + 1,
+                  [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
+                    kr = kbase + j * a.k_token;
+                    vr = vbase + j * a.v_token;
+                    return true;
+                  },
+                  mr, lr, orow);
+    if (2 * lane < a.head_dim)
+      *reinterpret_cast<uint32_t*>(a.out + (start + t) * a.o_token + head * a.o_head + 2 * lane) =
+          T::pack2(orow.x * inv_sum(lr), orow.y * inv_sum(lr));
+  }
+}
+
+template <typename T, int DP>
+hipError_t launch_dp(const PromptArgs& a, int64_t blocks, hipStream_t st) {
+  constexpr int lds = 4 * kBK * DP * 2;
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t e =
+      ensure_lds_limit(reinterpret_cast<const void*>(&attn_prompt_kernel<T, DP>), lds, lds_done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_prompt_kernel<T, DP>), dim3(static_cast<unsigned>(blocks)), dim3(256), lds, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_prompt(const awq_attn_prompt_args& g, hipStream_t st) {
+  PromptArgs a;
+  a.q = static_cast<const uint16_t*>(g.q);
+  a.k = static_cast<const uint16_t*>(g.k);
+  a.v = static_cast<const uint16_t*>(g.v);
+  a.out = static_cast<uint16_t*>(g.out);
+  a.cu = g.cu;
+  a.q_token = g.q_token;
+  a.k_token = g.k_token;
+  a.v_token = g.v_token;
+  a.o_token = g.o_token;
+  a.q_head = g.q_head;
+  a.k_head = g.k_head;
+  a.v_head = g.v_head;
+  a.o_head = g.o_head;
+  a.tokens = static_cast<int32_t>(g.tokens);
+  a.seqs = static_cast<int32_t>(g.seqs);
+  // at most this many tiles for any lengths: sum of ceil(n / kBQ)
+  const int64_t tiles = g.tokens / kBQ + (g.seqs < g.tokens ? g.seqs : g.tokens);
+  a.tiles = static_cast<int32_t>(tiles);
+  a.q_heads = g.q_heads;
+  a.group = g.q_heads / g.kv_heads;
+  a.head_dim = g.head_dim;
+  a.c = g.scale * kLog2e;
+  const int64_t blocks = tiles * g.q_heads;
+  if (g.dtype == AWQ_DT_F16)
+    return g.head_dim <= 64 ? launch_dp<F16, 64>(a, blocks, st) : launch_dp<F16, 128>(a, blocks, st);
+  return g.head_dim <= 64 ? launch_dp<BF16, 64>(a, blocks, st) : launch_dp<BF16, 128>(a, blocks, st);
+}
+
+}  // namespace awq

@@ -1,0 +1,476 @@
+// Attention of the last (new or drafted) tokens of each sequence over its paged cache
+// (awq_attn_tree in awq_block.h). A handful of query rows read every cached key and value
+// once: the kernel is bound by streaming the cache from memory.
+//
+// The query rows that share a key / value head (tokens x heads of the group) are handled
+// together, 16 NT rows per workgroup, so the cache is read once for all of them. The
+// context is split over workgroups, and inside a workgroup over its four wavefronts: each
+// takes every fourth step of 32 positions and runs alone, with a running maximum and sum of
+// its own, its own LDS ring and no barriers, until the four results are merged through LDS.
+// With more than one split the merged result is a partial one (float32 maximum, sum and
+// unnormalised row) in the workspace, and a second launch adds the splits in their order.
+//
+// A step's keys and values go from memory straight into LDS (16 bytes per lane, no
+// registers), kStages steps ahead. Both products are formed transposed, S^T = K Q^T and
+// O^T = V^T P^T (16 x 16 x 32 matrix instruction): lane l holds the scores of one query
+// (column l % 16), the positions it holds after S^T are the contraction slots it feeds to
+// O^T, and V^T is read from LDS in that order with the transposing 16-bit read.
+#include "block_internal.hpp"
+
+namespace awq {
+namespace {
+
+constexpr int kStep = 32;        // positions per wavefront and step
+constexpr int kWaves = 4;
+constexpr int kStages = 2;
+constexpr int kMinChunk = kStep * kWaves;  // positions per split: a multiple of this
+constexpr int kTableEntries = 1024;        // page numbers of a split staged in LDS
+constexpr int kMaxSplits = 64;
+
+struct TreeArgs {
+  const uint16_t *q, *k, *v;
+  uint16_t* out;
+  const int32_t *table, *ctx, *cu;
+  const uint64_t* mask;
+  float* part;  // [tokens * q_heads][splits][head_dim], then [..][splits][2]; NULL: one split
+  int64_t q_token, q_head, o_token, o_head, cache_page, cache_head, cache_slot;
+  int64_t max_len;  // table_width * page_size
+  int32_t tokens, seqs, table_width, pages, page_size, max_q, q_heads, kv_heads, group, head_dim;
+  int32_t splits, row_blocks;
+  float c;  // scale * log2(e)
+};
+
+// A sequence's tokens, context and length, clamped to what the buffers hold
+struct Seq {
+  int first, count, ctx, len;
+};
+__device__ __forceinline__ Seq sequence(const TreeArgs& a, int b) {
+  Seq s;
+  s.first = min(max(a.cu[b], 0), a.tokens);
+  s.count = min(max(min(a.cu[b + 1], a.tokens) - s.first, 0), a.max_q);
+  const int64_t ctx = max(a.ctx[b], 0);
+  s.ctx = static_cast<int>(ctx < a.max_len ? ctx : a.max_len);
+  const int64_t len = ctx + s.count;
+  s.len = static_cast<int>(len < a.max_len ? len : a.max_len);
+  return s;
+}
+// Positions per split of a sequence: the same for every workgroup of it
+__device__ __forceinline__ int chunk_of(int len, int splits) {
+  const int per = (len + splits - 1) / splits;
+  return max((per + kMinChunk - 1) / kMinChunk, 1) * kMinChunk;
+}
+
+// Which of a step's 32 positions a row sees, as bits: `back` is the step's first position less
+// the context (bit j of `mask` is new token j), `left` the positions up to the split's end.
+__device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
+  const int k = min(max(-back, 0), 31);  // positions of the step that are context (< 32 here)
+  const uint32_t bits = (static_cast<uint32_t>(mask >> (max(back, 0) & 63)) << k) | ((1u << k) - 1u);
+  return left < 32 ? bits & ((1u << left) - 1u) : bits;
+}
+
+// The factor that brings a partial result with maximum m and sum l to the maximum top. A
+// part that saw no finite score (m = -inf) has l = 0, or NaN if it saw a NaN, and passes
+// that on.
+__device__ __forceinline__ float scale_of(float m, float l, float top) {
+  return m == kNegInf ? l : __builtin_amdgcn_exp2f(m - top);
+}
+
+template <int DP>
+__device__ __forceinline__ int k_pos(int r, int c) {
+  return DP == 128 ? c ^ (r & 15) : c ^ ((r >> 1) & 7);
+}
+template <int DP>
+__device__ __forceinline__ int v_pos(int r, int c) {
+  return DP == 128 ? c ^ ((r & 7) << 1) : c ^ (((r >> 1) & 3) << 1);
+}
+
+// LDS bytes of a workgroup: the rings (later the four float32 results), Q, the page numbers
+template <int DP, int NT>
+struct Lds {
+  static constexpr int kRow = DP * 2;
+  static constexpr int kTile = kStep * kRow;
+  static constexpr int kRing = kWaves * kStages * 2 * kTile;
+  static constexpr int kSumStride = DP + 4;  // floats: rows 4 banks apart
+  static constexpr int kSums = kWaves * 16 * NT * kSumStride * 4;
+  static constexpr int kBig = kRing > kSums ? kRing : kSums;
+  static constexpr int kQ = 16 * NT * kRow;
+  static constexpr int kStats = kWaves * 16 * NT * 2 * 4;
+  static constexpr int kTotal = kBig + kQ + kStats + kTableEntries * 4;
+};
+
+// PAD: head_dim < DP
+template <typename T, int DP, int NT, bool PAD>
+__global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
+  typedef typename T::v8 v8;
+  typedef Lds<DP, NT> L;
+  constexpr int RB = L::kRow, RC = DP / 8, TILE = L::kTile;
+  constexpr int ROWS = 1024 / RB;        // positions one load instruction fills
+  constexpr int LOADS = kStep / ROWS;
+  constexpr int NC = DP / 32, ND = DP / 16;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];
+  unsigned char* q_lds = smem + L::kBig;
+  float* stats = reinterpret_cast<float*>(q_lds + L::kQ);
+  int* pages = reinterpret_cast<int*>(q_lds + L::kQ + L::kStats);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
+  const int kv_head = blockIdx.y, b = blockIdx.z;
+  const Seq s = sequence(a, b);
+  const int r0 = rb * 16 * NT, rows = min(s.count * a.group - r0, 16 * NT);
+  if (rows <= 0) return;
+  const int chunk = chunk_of(s.len, a.splits);
+  const int p0 = split * chunk, p1 = min(s.len, p0 + chunk);
+  if (p0 >= p1 && a.part != nullptr) return;  // the second launch knows that it is empty
+
+  // page numbers of the split, clamped to the cache
+  const int t0 = p0 / a.page_size;
+  const int n_pages = p1 > p0 ? (p1 - 1) / a.page_size - t0 + 1 : 0;
+  for (int i = threadIdx.x; i < n_pages; i += 256)
+    pages[i] = min(max(a.table[static_cast<int64_t>(b) * a.table_width + t0 + i], 0), a.pages - 1);
+  // Q rows (row r: token r / group, head r % group of the key head), 0 past the last
+  for (int i = threadIdx.x; i < 16 * NT * RC; i += 256) {
+    const int r = i / RC, ch = i % RC;
+    u32x4 x = {0, 0, 0, 0};
+    if (r < rows && 8 * ch < a.head_dim) {
+      const int t = (r0 + r) / a.group, hq = kv_head * a.group + (r0 + r) % a.group;
+      x = *reinterpret_cast<const u32x4*>(a.q + (s.first + t) * a.q_token + hq * a.q_head + 8 * ch);
+    }
+    *reinterpret_cast<u32x4*>(q_lds + r * RB + 16 * k_pos<DP>(r, ch)) = x;
+  }
+  unsigned char* ring = smem + wave * kStages * 2 * TILE;
+  if constexpr (PAD) {  // chunks past D are never loaded: they stay 0
+    for (int i = lane; i < kStages * 2 * TILE / 16; i += 64)
+      *reinterpret_cast<u32x4*>(ring + 16 * i) = u32x4{0, 0, 0, 0};
+    __builtin_amdgcn_s_waitcnt(0);
+  }
+  uint64_t sees[NT];  // this lane's rows' masks over the new tokens
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = 16 * n + col;
+    const int t = min((r0 + r) / a.group, max(s.count - 1, 0));
+    sees[n] = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
+  }
+  __syncthreads();
+
+  const uint16_t* kbase = a.k + kv_head * a.cache_head;
+  const uint16_t* vbase = a.v + kv_head * a.cache_head;
+  auto offset_of = [&](int pos) -> int64_t {
+    const int page = pos / a.page_size;
+    return pages[page - t0] * a.cache_page + (pos - page * a.page_size) * a.cache_slot;
+  };
+  // loads of the step at position s0; positions past the split repeat its last one (their
+  // scores are masked and their V rows cleared below)
+  auto load_step = [&](int s0, int stage) {
+    const int64_t off = offset_of(min(s0 + (lane & 31), p1 - 1));
+    const int off_lo = static_cast<int>(off), off_hi = static_cast<int>(off >> 32);
+    unsigned char* dst = ring + stage * 2 * TILE;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int r = ROWS * j + lane / RC;
+      const uint32_t lo = __shfl(off_lo, r), hi = __shfl(off_hi, r);
+      const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+      const int ck = 8 * k_pos<DP>(r, lane % RC), cv = 8 * v_pos<DP>(r, lane % RC);
+      if (!PAD || ck < a.head_dim)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(kbase + at + ck),
+            (lds_void*)(dst + j * 1024), 16, 0, 0);
+      if (!PAD || cv < a.head_dim)
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)(vbase + at + cv),
+            (lds_void*)(dst + TILE + j * 1024), 16, 0, 0);
+    }
+  };
+
+  float4_t acc[NT][ND];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    m[n] = kNegInf;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  // P carries 2^kShift (see kSlack: the maximum in use may be that much too small)
+  constexpr float kShift = 7.0f, kSlack = 8.0f;
+
+  const int first = p0 + kStep * wave;
+  constexpr int kStride = kStep * kWaves;
+  if (first < p1) load_step(first, 0);
+  int stage = 0;
+  for (int s0 = first; s0 < p1; s0 += kStride, stage ^= 1) {
+    __builtin_amdgcn_s_waitcnt(0);  // the step has landed
+    asm volatile("" ::: "memory");
+    if (s0 + kStride < p1) load_step(s0 + kStride, stage ^ 1);
+    const unsigned char* ks = ring + stage * 2 * TILE;
+    unsigned char* vs = ring + stage * 2 * TILE + TILE;
+    if (s0 + kStep > p1) {  // V rows past the split: 0
+      for (int i = lane; i < (s0 + kStep - p1) * RC; i += 64)
+        *reinterpret_cast<u32x4*>(vs + (p1 - s0) * RB + 16 * i) = u32x4{0, 0, 0, 0};
+    }
+    v8 kf[2][NC];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int r = 16 * t + col;
+        kf[t][c] = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
+      }
+    u32x4 p[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float4_t sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int r = 16 * n + col;
+        const v8 qf = *reinterpret_cast<const v8*>(q_lds + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
+        sc[0] = T::mfma16(kf[0][c], qf, sc[0]);
+        sc[1] = T::mfma16(kf[1][c], qf, sc[1]);
+      }
+      if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
+        const uint32_t bits = visible(sees[n], s0 - s.ctx, p1 - s0) >> (4 * g);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][i] = (bits & (1u << (16 * t + i))) != 0 ? sc[t][i] : kNegInf;
+      }
+      float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                        fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * a.c;
+      if (__ballot(top > m[n] + kSlack) != 0) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float m_new = fmaxf(m[n], top);
+        const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - m_new);
+        m[n] = m_new;
+        l[n] *= keep;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[n][d] *= keep;
+      }
+      const float off = m[n] == kNegInf ? 0.0f : kShift - m[n];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.c, off));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i + 1], a.c, off));
+          l[n] += e0 + e1;
+          p[n][2 * t + (i >> 1)] = T::pack2(e0, e1);
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const int ra = 4 * g + (col >> 2), rb2 = ra + 16;
+      const int ch = 2 * d + ((col & 3) >> 1), byte = 8 * (col & 1);
+      const short4_t lo = lds_read_tr(vs + ra * RB + 16 * v_pos<DP>(ra, ch) + byte);
+      const short4_t hi = lds_read_tr(vs + rb2 * RB + 16 * v_pos<DP>(rb2, ch) + byte);
+      const v8 vf = join8<v8>(lo, hi);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n][d] = T::mfma16(vf, __builtin_bit_cast(v8, p[n]), acc[n][d]);
+    }
+    asm volatile("" ::: "memory");
+  }
+
+  // merge the four wavefronts: maxima, then the rows brought to the common maximum
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    l[n] += __shfl_xor(l[n], 16);
+    l[n] += __shfl_xor(l[n], 32);
+    if (g == 0) {
+      stats[(wave * 16 * NT + 16 * n + col) * 2] = m[n];
+      stats[(wave * 16 * NT + 16 * n + col) * 2 + 1] = l[n];
+    }
+  }
+  __syncthreads();  // also: every ring is done with
+  float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int r = 16 * n + col;
+    float top = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 * NT + r) * 2]);
+    const float f = scale_of(m[n], l[n], top);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+      *reinterpret_cast<float4_t*>(sums + (wave * 16 * NT + r) * L::kSumStride + 16 * d + 4 * g) = acc[n][d] * f;
+  }
+  __syncthreads();
+  // one wavefront per row: lane i has d = 2 i, 2 i + 1
+  for (int r = wave; r < rows; r += kWaves) {
+    float top = kNegInf, sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 * NT + r) * 2]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float mw = stats[(w * 16 * NT + r) * 2], lw = stats[(w * 16 * NT + r) * 2 + 1];
+      sum += lw * scale_of(mw, lw, top);
+    }
+    float2_t o = {0.0f, 0.0f};
+    if (2 * lane < DP) {
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w)
+        o += *reinterpret_cast<const float2_t*>(sums + (w * 16 * NT + r) * L::kSumStride + 2 * lane);
+    }
+    const int t = (r0 + r) / a.group, hq = kv_head * a.group + (r0 + r) % a.group;
+    // a row that came out NaN: again, key by key (a masked infinity or NaN may be the cause)
+    if (__ballot(o.x != o.x || o.y != o.y) != 0) {
+      const uint64_t bits = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
+      attend_row<T>(a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, p0, p1,
+                    [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
+                      const int64_t at = offset_of(static_cast<int>(j));
+                      kr = kbase + at;
+                      vr = vbase + at;
+                      const int64_t back = j - s.ctx;
+                      return back < 0 || ((bits >> (back & 63)) & 1) != 0;
+                    },
+                    top, sum, o);
+    }
+    if (2 * lane >= a.head_dim) continue;
+    if (a.part != nullptr) {
+      const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits + split;
+      *reinterpret_cast<float2_t*>(a.part + at * a.head_dim + 2 * lane) = o;
+      if (lane == 0) {
+        float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim + 2 * at;
+        ml[0] = top;
+        ml[1] = sum;
+      }
+    } else {
+      const float inv = inv_sum(sum);
+      *reinterpret_cast<uint32_t*>(a.out + (s.first + t) * a.o_token + hq * a.o_head + 2 * lane) =
+          T::pack2(o.x * inv, o.y * inv);
+    }
+  }
+}
+
+// Adds the splits of a row in their order: one wavefront per token and head, lane i has
+// d = 2 i, 2 i + 1.
+template <typename T>
+__global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int b = blockIdx.y;
+  const Seq s = sequence(a, b);
+  const int i = blockIdx.x * 4 + wave;
+  const int t = i / a.q_heads, hq = i - t * a.q_heads;
+  if (t >= s.count) return;
+  const int chunk = chunk_of(s.len, a.splits);
+  const int n = (s.len + chunk - 1) / chunk;
+  const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits;
+  const float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim + 2 * at;
+  float top = kNegInf;
+  for (int w = lane; w < n; w += 64) top = fmaxf(top, ml[2 * w]);
+  top = wave_max(top);
+  float sum = 0.0f;
+  float2_t o = {0.0f, 0.0f};
+  for (int w = 0; w < n; ++w) {
+    const float f = scale_of(ml[2 * w], ml[2 * w + 1], top);
+    sum += ml[2 * w + 1] * f;
+    if (2 * lane < a.head_dim)
+      o += *reinterpret_cast<const float2_t*>(a.part + (at + w) * a.head_dim + 2 * lane) * f;
+  }
+  const float inv = inv_sum(sum);
+  if (2 * lane < a.head_dim)
+    *reinterpret_cast<uint32_t*>(a.out + (s.first + t) * a.o_token + hq * a.o_head + 2 * lane) =
+        T::pack2(o.x * inv, o.y * inv);
+}
+
+// Rows per workgroup: 16, 32 or 64, the least that hold a sequence's, 64 at most.
+int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// Splits of the longest context the table holds: about 1024 workgroups, each at least 128
+// positions, and at most the page numbers that a workgroup stages.
+int pick_splits(int64_t seqs, int64_t max_len, int32_t page_size, int64_t rows, int32_t kv_heads) {
+  const int64_t row_blocks = (rows + 16 * row_tiles(rows) - 1) / (16 * row_tiles(rows));
+  const int64_t wgs = seqs * kv_heads * row_blocks;
+  int64_t s = (1024 + wgs - 1) / wgs;
+  const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
+  s = s < most ? s : most;
+  s = s < kMaxSplits ? s : kMaxSplits;
+  // a split of `chunk` positions touches at most chunk / page_size + 1 pages
+  const int64_t limit = static_cast<int64_t>(kTableEntries - 1) * page_size / kMinChunk * kMinChunk;
+  const int64_t least = (max_len + limit - 1) / limit;
+  s = s > least ? s : least;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+template <typename T, int DP, int NT, bool PAD>
+hipError_t launch_nt(const TreeArgs& a, hipStream_t st) {
+  static std::atomic<uint64_t> lds_done{0};
+  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attn_tree_kernel<T, DP, NT, PAD>),
+                                        Lds<DP, NT>::kTotal, lds_done);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((attn_tree_kernel<T, DP, NT, PAD>),
+                     dim3(static_cast<unsigned>(a.row_blocks) * a.splits, a.kv_heads, a.seqs), dim3(256),
+                     (Lds<DP, NT>::kTotal), st, a);
+  const hipError_t e2 = hipGetLastError();
+  if (e2 != hipSuccess || a.part == nullptr) return e2;
+  hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3((a.max_q * a.q_heads + 3) / 4, a.seqs), dim3(256), 0,
+                     st, a);
+  return hipGetLastError();
+}
+
+template <typename T, int DP>
+hipError_t launch_dp(const TreeArgs& a, int nt, hipStream_t st) {
+  if (a.head_dim < DP) {
+    if (nt == 1) return launch_nt<T, DP, 1, true>(a, st);
+    if (nt == 2) return launch_nt<T, DP, 2, true>(a, st);
+    return launch_nt<T, DP, 4, true>(a, st);
+  }
+  if (nt == 1) return launch_nt<T, DP, 1, false>(a, st);
+  if (nt == 2) return launch_nt<T, DP, 2, false>(a, st);
+  return launch_nt<T, DP, 4, false>(a, st);
+}
+
+}  // namespace
+
+int attn_tree_splits(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
+                     int32_t kv_heads) {
+  return pick_splits(seqs, table_width * page_size, page_size,
+                     static_cast<int64_t>(max_q) * (q_heads / kv_heads), kv_heads);
+}
+
+size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size,
+                                 int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  const int s = attn_tree_splits(seqs, table_width, page_size, max_q, q_heads, kv_heads);
+  return s > 1 ? static_cast<size_t>(tokens) * q_heads * s * (head_dim + 2) * 4 : 0;
+}
+
+hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
+  TreeArgs a;
+  a.q = static_cast<const uint16_t*>(g.q);
+  a.k = static_cast<const uint16_t*>(g.k_cache);
+  a.v = static_cast<const uint16_t*>(g.v_cache);
+  a.out = static_cast<uint16_t*>(g.out);
+  a.table = g.block_table;
+  a.ctx = g.ctx_lens;
+  a.cu = g.cu_q;
+  a.mask = g.mask;
+  a.q_token = g.q_token;
+  a.q_head = g.q_head;
+  a.o_token = g.o_token;
+  a.o_head = g.o_head;
+  a.cache_page = g.cache_page;
+  a.cache_head = g.cache_head;
+  a.cache_slot = g.cache_slot;
+  a.max_len = g.table_width * g.page_size;
+  a.tokens = static_cast<int32_t>(g.tokens);
+  a.seqs = static_cast<int32_t>(g.seqs);
+  a.table_width = static_cast<int32_t>(g.table_width);
+  a.pages = static_cast<int32_t>(g.pages);
+  a.page_size = g.page_size;
+  a.max_q = g.max_q;
+  a.q_heads = g.q_heads;
+  a.kv_heads = g.kv_heads;
+  a.group = g.q_heads / g.kv_heads;
+  a.head_dim = g.head_dim;
+  a.c = g.scale * kLog2e;
+  const int64_t rows = static_cast<int64_t>(g.max_q) * a.group;
+  const int nt = row_tiles(rows);
+  a.row_blocks = static_cast<int32_t>((rows + 16 * nt - 1) / (16 * nt));
+  a.splits = attn_tree_splits(g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads);
+  a.part = a.splits > 1 ? static_cast<float*>(g.ws) : nullptr;
+  if (g.dtype == AWQ_DT_F16)
+    return g.head_dim <= 64 ? launch_dp<F16, 64>(a, nt, st) : launch_dp<F16, 128>(a, nt, st);
+  return g.head_dim <= 64 ? launch_dp<BF16, 64>(a, nt, st) : launch_dp<BF16, 128>(a, nt, st);
+}
+
+}  // namespace awq

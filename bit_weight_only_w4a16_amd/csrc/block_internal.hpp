@@ -1,0 +1,147 @@
+// Internal declarations and device helpers of the decoder-block operators (awq_block.h).
+#pragma once
+
+#include "../../include/awq_block.h"
+#include "awq_internal.hpp"
+
+namespace awq {
+
+hipError_t launch_rope(const awq_rope_args& a, hipStream_t st);
+hipError_t launch_attn_prompt(const awq_attn_prompt_args& a, hipStream_t st);
+int attn_tree_splits(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
+                     int32_t kv_heads);
+size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size,
+                                 int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+hipError_t launch_attn_tree(const awq_attn_tree_args& a, hipStream_t st);
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+
+typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef float float2_t __attribute__((ext_vector_type(2)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// The two element types: conversions round to nearest even.
+struct F16 {
+  typedef half8_t v8;
+  static __device__ __forceinline__ float to_float(uint16_t b) {
+    return static_cast<float>(__builtin_bit_cast(_Float16, b));
+  }
+  static __device__ __forceinline__ uint16_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(f));
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, half2_t));
+  }
+  static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float4_t mfma16(v8 a, v8 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+};
+struct BF16 {
+  typedef bf8_t v8;
+  static __device__ __forceinline__ float to_float(uint16_t b) {
+    return __builtin_bit_cast(float, static_cast<uint32_t>(b) << 16);
+  }
+  static __device__ __forceinline__ uint16_t bits(float f) {
+    return __builtin_bit_cast(uint16_t, static_cast<__bf16>(f));
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf2_t));
+  }
+  static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float4_t mfma16(v8 a, v8 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(3))) short4_t lds_short4;
+
+// Transposed LDS read of 16-bit elements: lane i of each group of 16 lanes gets element
+// i % 4 of the 8 bytes that lane 4 r + i / 4 of its group points at, for r = 0 .. 3. With
+// lane j pointing at row j / 4, columns 4 (j % 4).. of a 4 x 16 block, lane i gets column i.
+__device__ __forceinline__ short4_t lds_read_tr(const unsigned char* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4*)(p));
+}
+template <typename V8>
+__device__ __forceinline__ V8 join8(short4_t a, short4_t b) {
+  typedef short short8_t __attribute__((ext_vector_type(8)));
+  return __builtin_bit_cast(V8, short8_t{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
+}
+
+// v from the lane 32 (16) lanes away, combined by maximum / sum
+__device__ __forceinline__ float xor32_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
+__device__ __forceinline__ float xor32_add(float v) { return v + __shfl_xor(v, 32); }
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
+  return v;
+}
+
+// 1 / sum of a row's probabilities; 0 for a row that saw nothing
+__device__ __forceinline__ float inv_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+
+// One row of attention by one wavefront, key by key, in float32: the running maximum m and
+// sum l (base 2, of exponents q.k * c) and, in lane i, o for d = 2 i, 2 i + 1. Keys that the
+// row does not see are skipped, not multiplied by zero, so nothing in them reaches the row.
+// The matrix kernels multiply masked probabilities of exactly 0 with whatever the masked
+// value row holds; where that is an infinity or NaN the row comes out NaN, and the kernels
+// take this path for rows that came out NaN. key(j, k, v) gives key j's rows and whether the
+// row sees it.
+template <typename T, typename Key>
+__device__ __forceinline__ void attend_row(const uint16_t* q, int head_dim, float c, int64_t first,
+                                        int64_t end, Key key, float& m_out, float& l_out,
+                                        float2_t& o_out) {
+  const int lane = threadIdx.x & 63;
+  float m = kNegInf, l = 0.0f;
+  float2_t o = {0.0f, 0.0f};
+  for (int64_t j0 = first; j0 < end; j0 += 64) {
+    const int64_t j = j0 + lane;
+    const uint16_t *k = nullptr, *v = nullptr;
+    const bool sees = j < end && key(j, k, v);
+    float s = kNegInf;
+    if (sees) {
+      float dot = 0.0f;
+      for (int d = 0; d < head_dim; ++d) dot = __builtin_fmaf(T::to_float(q[d]), T::to_float(k[d]), dot);
+      s = dot * c;
+    }
+    const float m_new = fmaxf(m, wave_max(s));
+    const float base = m_new == kNegInf ? 0.0f : m_new;
+    const float p = sees ? __builtin_amdgcn_exp2f(s - base) : 0.0f;
+    const float keep = __builtin_amdgcn_exp2f(m - base);
+    l = l * keep + wave_sum(p);
+    o *= keep;
+    m = m_new;
+    uint64_t left = __ballot(sees);
+    while (left != 0) {
+      const int i = __builtin_ctzll(left);
+      left &= left - 1;
+      const float pi = __shfl(p, i);
+      const uint64_t va = reinterpret_cast<uint64_t>(v);
+      const uint32_t lo = __shfl(static_cast<int>(va), i), hi = __shfl(static_cast<int>(va >> 32), i);
+      const uint16_t* vi = reinterpret_cast<const uint16_t*>((static_cast<uint64_t>(hi) << 32) | lo);
+      if (2 * lane < head_dim) {
+        o.x = __builtin_fmaf(pi, T::to_float(vi[2 * lane]), o.x);
+        o.y = __builtin_fmaf(pi, T::to_float(vi[2 * lane + 1]), o.y);
+      }
+    }
+  }
+  m_out = m;
+  l_out = l;
+  o_out = o;
+}
+
+}  // namespace awq
