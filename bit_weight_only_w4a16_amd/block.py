@@ -16,6 +16,7 @@ import torch
 from . import awq
 
 DT = {torch.float16: 0, torch.bfloat16: 1}
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 TREE_MAX_TOKENS = 64
 
 _vp = ctypes.c_void_p
@@ -56,7 +57,14 @@ class AttnTreeArgs(ctypes.Structure):
                 + [("scale", _f32), ("reserved", _i32)])
 
 
+class Epilogue(ctypes.Structure):
+    """awq_epilogue of awq_block.h."""
+    _fields_ = [("bias", _vp), ("mul", _vp), ("residual", _vp), ("act", _i32), ("reserved", _i32)]
+
+
 _SIGNATURES = {
+    "awq_gemm_fused": (ctypes.c_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp, _vp, ctypes.c_size_t,
+                                      _vp]),
     "awq_rope": (ctypes.c_int, [_vp, _vp]),
     "awq_attn_prompt": (ctypes.c_int, [_vp, _vp]),
     "awq_attn_tree_workspace_bytes": (ctypes.c_size_t, [_i64, _i64, _i64, _i32, _i32, _i32, _i32, _i32]),
@@ -125,6 +133,35 @@ def _like(out, name: str, ref: torch.Tensor) -> torch.Tensor:
     awq._shape(out, name, ref.shape)
     awq._same_device(ref, **{name: out})
     return out
+
+
+def awq_gemm_fused(x, inv_s_c, packed, n: int, k: int, group: int = awq.GROUP, fmt: int = awq.FMT_ASYM, *,
+                   bias=None, act: str = "none", mul=None, residual=None, y=None, ws=None) -> torch.Tensor:
+    """awq_gemm with an element-wise tail, y = act(x . W^T + bias) * mul + residual, rounded
+    once: bias fp16 [N], mul and residual fp16 [M, N], act one of ACTS. y may be mul or
+    residual itself."""
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {tuple(ACTS)}")
+    if x.dim() != 2 or x.shape[1] != k:
+        raise ValueError("x must be [M, K]")
+    m = x.shape[0]
+    if y is None:
+        y = torch.empty((m, n), dtype=torch.float16, device=x.device)
+    awq._shape(y, "y", (m, n))
+    awq._shape(inv_s_c, "inv_s_c", (k,))
+    awq._shape(bias, "bias", (n,))
+    awq._shape(mul, "mul", (m, n))
+    awq._shape(residual, "residual", (m, n))
+    awq._at_least(packed, "packed", awq.awq_repacked_bytes(n, k, group, fmt))
+    awq._same_device(x, inv_s_c=inv_s_c, packed=packed, bias=bias, mul=mul, residual=residual, y=y, ws=ws)
+    f16 = torch.float16
+    tail = Epilogue(awq._opt(bias, "bias", f16), awq._opt(mul, "mul", f16), awq._opt(residual, "residual", f16),
+                    ACTS[act], 0)
+    awq._check(lib().awq_gemm_fused(awq._dev(x, "x", f16), awq._opt(inv_s_c, "inv_s_c", f16),
+                                    awq._dev(packed, "packed", torch.uint8), m, n, k, group, fmt,
+                                    ctypes.byref(tail), awq._dev(y, "y", f16), awq._opt(ws, "ws", torch.uint8),
+                                    0 if ws is None else ws.numel(), awq._stream(x.device)), "awq_gemm_fused")
+    return y
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,

@@ -1,6 +1,7 @@
 // C ABI entry points of the decoder-block operators (awq_block.h): argument checks (all
 // before any launch), then the launchers.
 #include "block_internal.hpp"
+#include "epilogue.hpp"
 
 #include <math.h>
 
@@ -51,6 +52,20 @@ int check_cache(int64_t page, int64_t head, int64_t slot, int64_t pages, int32_t
 }  // namespace
 
 extern "C" {
+
+int awq_gemm_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M, int64_t N,
+                   int64_t K, int32_t group, int32_t fmt, const awq_epilogue* epilogue, uint16_t* y,
+                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  AWQ_TRY(awq::check_product(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes));
+  if (epilogue == nullptr || epilogue->reserved != 0) return AWQ_ERR_INVALID_ARG;
+  if (epilogue->act < AWQ_ACT_NONE || epilogue->act > AWQ_ACT_SILU) return AWQ_ERR_INVALID_ARG;
+  if (!aligned16(epilogue->bias) || !aligned16(epilogue->mul) || !aligned16(epilogue->residual))
+    return AWQ_ERR_MISALIGNED;
+  if (M == 0) return AWQ_OK;
+  const awq::Epilogue e = {epilogue->bias, epilogue->mul, epilogue->residual, epilogue->act};
+  return hip_status(
+      awq::launch_gemm_fused(x, inv_s_c, packed, M, N, K, group, fmt, e, y, ws, ws_bytes, stream));
+}
 
 int awq_rope(const awq_rope_args* a, hipStream_t stream) {
   if (a == nullptr || a->reserved != 0 || a->tokens < 0) return AWQ_ERR_INVALID_ARG;

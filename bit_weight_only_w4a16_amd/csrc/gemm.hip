@@ -33,6 +33,7 @@
 //  * Workgroups are numbered so that the ones a given XCD (L2 slice) runs are
 //    neighbours along M: they share the same weight columns in that L2.
 #include "awq_internal.hpp"
+#include "epilogue.hpp"
 
 #include <stdio.h>
 #include <stdlib.h>
@@ -61,11 +62,12 @@ struct GemmArgs {
 // The arguments are thirteen scalar dwords (the rest of the layout is derived from
 // them), which the compiler preloads into SGPRs at wavefront launch: no wait for the
 // argument block before the first load. `out` is y (binary16) or, with K split, the
-// float32 partial sums.
-template <int WAVES_M, int WM, int WN, int SCHED, bool ASYM, int KS>
+// float32 partial sums. E: nothing, or the Epilogue of the sums, which then are not split
+// across workgroups.
+template <int WAVES_M, int WM, int WN, int SCHED, bool ASYM, int KS, typename... E>
 __global__ void __launch_bounds__(kGThreads * KS)
     gemm_kernel(const uint16_t* x, const uint16_t* inv, const uint8_t* packed, void* out, int M,
-                int N, int K, int splits, int sets) {
+                int N, int K, int splits, int sets, E... epi) {
   constexpr int WAVES_N = 4 / WAVES_M;
   constexpr int BM = WAVES_M * WM * 16, BN = WAVES_N * WN * 16;
   const PackedLayout L = make_layout_sets(N, K, sets, ASYM);
@@ -305,7 +307,8 @@ __global__ void __launch_bounds__(kGThreads * KS)
           if (part) {
             part[o] = acc[ms][j][q];
           } else {
-            a.y[o] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(acc[ms][j][q]));
+            const float v = apply_epilogue(acc[ms][j][q], n, o, epi...);
+            a.y[o] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
           }
         }
       }
@@ -313,13 +316,22 @@ __global__ void __launch_bounds__(kGThreads * KS)
   }
 }
 
+// the Epilogue on four outputs of one row of N
+__device__ __forceinline__ void apply_row(float4_t&, int64_t) {}
+__device__ __forceinline__ void apply_row(float4_t& v, int64_t i, int N, const Epilogue& e) {
+  const int n = static_cast<int>(i % N);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) v[q] = apply_epilogue(v[q], n + q, i + q, e);
+}
+
 // y = binary16(sum over the splits of the partial sums, in split order): deterministic.
 // Four outputs per thread; M * N is a multiple of 8. The split count is a template
 // argument so that all S loads are in flight before the first add (with a run-time
 // count the loop waited one memory round trip per split).
-template <int S>
-__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* part, int64_t mn,
-                                                            uint16_t* y) {
+// E: nothing, or the row length and the Epilogue of the sums.
+template <int S, typename... E>
+__global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* part, int64_t mn, uint16_t* y,
+                                                            E... epi) {
   const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
   if (i >= mn) return;
   float4_t p[S];
@@ -328,6 +340,7 @@ __global__ void __launch_bounds__(256) splitk_reduce_kernel(const float* part, i
   float4_t v = p[0];
 #pragma unroll
   for (int s = 1; s < S; ++s) v += p[s];
+  apply_row(v, i, epi...);
   const half2_t lo = {static_cast<_Float16>(v[0]), static_cast<_Float16>(v[1])};
   const half2_t hi = {static_cast<_Float16>(v[2]), static_cast<_Float16>(v[3])};
   *reinterpret_cast<uint2*>(y + i) = make_uint2(as_u32(lo), as_u32(hi));
@@ -347,27 +360,40 @@ int pick_splits(int64_t blocks, int64_t M, int64_t N, int64_t K, int n_groups) {
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-template <int WAVES_M, int WM, int WN, int SCHED, bool ASYM, int KS>
-hipError_t launch_tiles_fmt(GemmArgs a, hipStream_t st) {
+hipError_t reduce_splits(const GemmArgs& a, hipStream_t st) {
+  return launch_splitk_reduce(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.y, st);
+}
+hipError_t reduce_splits(const GemmArgs& a, hipStream_t st, const Epilogue& e) {
+  return launch_splitk_reduce_fused(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.N, e, a.y, st);
+}
+
+template <int WAVES_M, int WM, int WN, int SCHED, bool ASYM, int KS, typename... E>
+hipError_t launch_tiles_kernel(GemmArgs a, hipStream_t st, E... epi) {
   constexpr int BM = WAVES_M * WM * 16, BN = (4 / WAVES_M) * WN * 16;
   constexpr size_t lds_x = 2ull * KS * BM * kLdsStride * sizeof(_Float16);
   constexpr size_t lds_red = (KS - 1) * 4ull * WM * WN * 64 * 16;
   const size_t lds = lds_x > lds_red ? lds_x : lds_red;
   static std::atomic<uint64_t> lds_done{0};
   const hipError_t ea = ensure_lds_limit(
-      reinterpret_cast<const void*>(&gemm_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS>), static_cast<int>(lds),
+      reinterpret_cast<const void*>(&gemm_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS, E...>), static_cast<int>(lds),
       lds_done);
   if (ea != hipSuccess) return ea;
   a.n_blocks_m = (a.M + BM - 1) / BM;
   a.n_blocks_n = (a.N + BN - 1) / BN;
   const unsigned blocks = static_cast<unsigned>(a.n_blocks_m) * static_cast<unsigned>(a.n_blocks_n);
   void* out = a.splits > 1 ? static_cast<void*>(a.part) : static_cast<void*>(a.y);
-  hipLaunchKernelGGL((gemm_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS>), dim3(blocks, a.splits),
+  hipLaunchKernelGGL((gemm_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS, E...>), dim3(blocks, a.splits),
                      dim3(kGThreads * KS), lds, st, a.x, a.inv, a.packed, out, a.M, a.N, a.K, a.splits,
-                     a.sets);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  return launch_splitk_reduce(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.y, st);
+                     a.sets, epi...);
+  return hipGetLastError();
+}
+
+// Sums split across workgroups leave the Epilogue to the launch that adds them.
+template <int WAVES_M, int WM, int WN, int SCHED, bool ASYM, int KS, typename... E>
+hipError_t launch_tiles_fmt(const GemmArgs& a, hipStream_t st, E... epi) {
+  if (a.splits == 1) return launch_tiles_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS>(a, st, epi...);
+  const hipError_t e = launch_tiles_kernel<WAVES_M, WM, WN, SCHED, ASYM, KS>(a, st);
+  return e != hipSuccess ? e : reduce_splits(a, st, epi...);
 }
 
 // How the narrow tiles split K (from sweeps on MI355X at M = 8 .. 64 on the 7B and 70B
@@ -411,54 +437,63 @@ int64_t default_blocks(int64_t M, int64_t N, int64_t K) {
   return blocks_of<1, 4, 4>(M, N);
 }
 
-template <int WAVES_M, int WM, int WN, int SCHED = 0, int KS = 1>
-hipError_t launch_tiles(GemmArgs a, hipStream_t st) {
-  if (a.zeros_off >= 0) return launch_tiles_fmt<WAVES_M, WM, WN, SCHED, true, KS>(a, st);
-  return launch_tiles_fmt<WAVES_M, WM, WN, SCHED, false, KS>(a, st);
+template <int WAVES_M, int WM, int WN, int SCHED = 0, int KS = 1, typename... E>
+hipError_t launch_tiles(GemmArgs a, hipStream_t st, E... epi) {
+  if (a.zeros_off >= 0) return launch_tiles_fmt<WAVES_M, WM, WN, SCHED, true, KS>(a, st, epi...);
+  return launch_tiles_fmt<WAVES_M, WM, WN, SCHED, false, KS>(a, st, epi...);
 }
 
 // the small-M tilings with K also split inside the workgroup (KS slices of four wavefronts)
-template <int WAVES_M, int WM, int WN>
-hipError_t launch_tiles_ks(GemmArgs a, int ks, hipStream_t st) {
+template <int WAVES_M, int WM, int WN, typename... E>
+hipError_t launch_tiles_ks(GemmArgs a, int ks, hipStream_t st, E... epi) {
   // four slices (1024 threads, 128 VGPRs per lane) only for wavefront tiles of at most
   // four matrix-core tiles: larger ones would spill
   if constexpr (WM * WN <= 4) {
-    if (ks == 4) return launch_tiles<WAVES_M, WM, WN, 0, 4>(a, st);
+    if (ks == 4) return launch_tiles<WAVES_M, WM, WN, 0, 4>(a, st, epi...);
   }
-  if (ks >= 2) return launch_tiles<WAVES_M, WM, WN, 0, 2>(a, st);
-  return launch_tiles<WAVES_M, WM, WN, 0, 1>(a, st);
+  if (ks >= 2) return launch_tiles<WAVES_M, WM, WN, 0, 2>(a, st, epi...);
+  return launch_tiles<WAVES_M, WM, WN, 0, 1>(a, st, epi...);
 }
 
-template <int S>
-hipError_t launch_reduce_s(const float* part, int64_t mn, uint16_t* y, hipStream_t st) {
-  hipLaunchKernelGGL(splitk_reduce_kernel<S>, dim3(static_cast<unsigned>((mn / 4 + 255) / 256)),
-                     dim3(256), 0, st, part, mn, y);
+template <int S, typename... E>
+hipError_t launch_reduce_s(const float* part, int64_t mn, uint16_t* y, hipStream_t st, E... epi) {
+  hipLaunchKernelGGL((splitk_reduce_kernel<S, E...>), dim3(static_cast<unsigned>((mn / 4 + 255) / 256)),
+                     dim3(256), 0, st, part, mn, y, epi...);
   return hipGetLastError();
+}
+
+// splits in [2, 16] (every K split the launchers pick or accept)
+template <typename... E>
+hipError_t dispatch_reduce(const float* part, int splits, int64_t mn, uint16_t* y, hipStream_t st, E... epi) {
+  switch (splits) {
+    case 2: return launch_reduce_s<2>(part, mn, y, st, epi...);
+    case 3: return launch_reduce_s<3>(part, mn, y, st, epi...);
+    case 4: return launch_reduce_s<4>(part, mn, y, st, epi...);
+    case 5: return launch_reduce_s<5>(part, mn, y, st, epi...);
+    case 6: return launch_reduce_s<6>(part, mn, y, st, epi...);
+    case 7: return launch_reduce_s<7>(part, mn, y, st, epi...);
+    case 8: return launch_reduce_s<8>(part, mn, y, st, epi...);
+    case 9: return launch_reduce_s<9>(part, mn, y, st, epi...);
+    case 10: return launch_reduce_s<10>(part, mn, y, st, epi...);
+    case 11: return launch_reduce_s<11>(part, mn, y, st, epi...);
+    case 12: return launch_reduce_s<12>(part, mn, y, st, epi...);
+    case 13: return launch_reduce_s<13>(part, mn, y, st, epi...);
+    case 14: return launch_reduce_s<14>(part, mn, y, st, epi...);
+    case 15: return launch_reduce_s<15>(part, mn, y, st, epi...);
+    case 16: return launch_reduce_s<16>(part, mn, y, st, epi...);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace
 
-// splits in [2, 16] (every K split the launchers pick or accept)
 hipError_t launch_splitk_reduce(const float* part, int splits, int64_t mn, uint16_t* y,
                                 hipStream_t st) {
-  switch (splits) {
-    case 2: return launch_reduce_s<2>(part, mn, y, st);
-    case 3: return launch_reduce_s<3>(part, mn, y, st);
-    case 4: return launch_reduce_s<4>(part, mn, y, st);
-    case 5: return launch_reduce_s<5>(part, mn, y, st);
-    case 6: return launch_reduce_s<6>(part, mn, y, st);
-    case 7: return launch_reduce_s<7>(part, mn, y, st);
-    case 8: return launch_reduce_s<8>(part, mn, y, st);
-    case 9: return launch_reduce_s<9>(part, mn, y, st);
-    case 10: return launch_reduce_s<10>(part, mn, y, st);
-    case 11: return launch_reduce_s<11>(part, mn, y, st);
-    case 12: return launch_reduce_s<12>(part, mn, y, st);
-    case 13: return launch_reduce_s<13>(part, mn, y, st);
-    case 14: return launch_reduce_s<14>(part, mn, y, st);
-    case 15: return launch_reduce_s<15>(part, mn, y, st);
-    case 16: return launch_reduce_s<16>(part, mn, y, st);
-    default: return hipErrorInvalidValue;
-  }
+  return dispatch_reduce(part, splits, mn, y, st);
+}
+hipError_t launch_splitk_reduce_fused(const float* part, int splits, int64_t mn, int64_t N,
+                                      const Epilogue& e, uint16_t* y, hipStream_t st) {
+  return dispatch_reduce(part, splits, mn, y, st, static_cast<int>(N), e);
 }
 
 // Where the decode kernel (whole 16-row tiles and all of K per workgroup: no split, no
@@ -503,9 +538,11 @@ size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
   return s > 1 ? static_cast<size_t>(s) * M * N * sizeof(float) : 0;
 }
 
-hipError_t launch_gemm(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
-                       int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt, uint16_t* y,
-                       void* ws, size_t ws_bytes, hipStream_t st) {
+// awq_gemm's choice of kernel, with or without an Epilogue.
+template <typename... E>
+static hipError_t gemm_impl(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
+                            int64_t N, int64_t K, int32_t group, int32_t fmt, uint16_t* y, void* ws,
+                            size_t ws_bytes, hipStream_t st, E... epi) {
   // large M: wide wavefront tiles, X' from the workspace (or pre-scaled by the caller).
   // Tuning overrides for sweeps (libraries built for tuning): AWQ_GEMM_WIDE = "0" keeps the
   // narrow kernel, "[splits]<column tiles><K split>" (41, 42, 31, 32, 21, 22, 442, ...)
@@ -515,12 +552,20 @@ hipError_t launch_gemm(const uint16_t* x, const uint16_t* inv_s_c, const void* p
   const bool wide_ok =
       inv_s_c == nullptr || (ws != nullptr && ws_bytes >= static_cast<size_t>(M) * K * 2);
   if (M >= kWideMinM && wide_ok && wide_env != 0) {
-    const int cfg = wide_env > 0 ? wide_env : 0;
-    return launch_gemm_wide(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, cfg, st);
+    if constexpr (sizeof...(E) == 0) {
+      const int cfg = wide_env > 0 ? wide_env : 0;
+      return launch_gemm_wide(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, cfg, st);
+    } else {
+      return launch_gemm_wide_fused(x, inv_s_c, packed, M, N, K, group, fmt, epi..., y, ws, ws_bytes, st);
+    }
   }
   const PackedLayout L = make_layout(N, K, group, fmt);
   if (small_m_takes_decode_kernel(M, N, K)) {
-    return launch_gemv(x, inv_s_c, packed, M, N, K, group, fmt, y, nullptr, 0, st);
+    if constexpr (sizeof...(E) == 0) {
+      return launch_gemv(x, inv_s_c, packed, M, N, K, group, fmt, y, nullptr, 0, st);
+    } else {
+      return launch_gemv_fused(x, inv_s_c, packed, M, N, K, group, fmt, epi..., y, st);
+    }
   }
   GemmArgs a;
   a.x = x;
@@ -566,34 +611,36 @@ hipError_t launch_gemm(const uint16_t* x, const uint16_t* inv_s_c, const void* p
     a.splits = want;
     a.part = static_cast<float*>(ws);
   }
-  // AWQ_GEMM_TILE = "waves_m,wm,wn,sched" selects another tiling (tuning sweeps)
-  struct TileEnv {
-    int wv = 0, wm = 0, wn = 0, sc = 0;
-    bool set = false;
-  };
-  TileEnv tile_env;
-  if (const char* env = tuning_env("AWQ_GEMM_TILE")) {
-    tile_env.set = sscanf(env, "%d,%d,%d,%d", &tile_env.wv, &tile_env.wm, &tile_env.wn, &tile_env.sc) == 4;
-  }
-  if (tile_env.set) {
-    const int wv = tile_env.wv, wm = tile_env.wm, wn = tile_env.wn, sc = tile_env.sc;
-    if (wv == 1 && wm == 4 && wn == 4 && sc == 0) return launch_tiles<1, 4, 4, 0>(a, st);
-    if (wv == 1 && wm == 4 && wn == 4 && sc == 2) return launch_tiles<1, 4, 4, 2>(a, st);
-    if (wv == 1 && wm == 4 && wn == 4 && sc == 3) return launch_tiles<1, 4, 4, 3>(a, st);
-    if (wv == 1 && wm == 4 && wn == 4 && sc == 4) return launch_tiles<1, 4, 4, 4>(a, st);
-    if (wv == 1 && wm == 8 && wn == 4 && sc == 0) return launch_tiles<1, 8, 4, 0>(a, st);
-    if (wv == 1 && wm == 8 && wn == 4 && sc == 2) return launch_tiles<1, 8, 4, 2>(a, st);
-    if (wv == 1 && wm == 8 && wn == 2 && sc == 0) return launch_tiles<1, 8, 2, 0>(a, st);
-    if (wv == 1 && wm == 8 && wn == 2 && sc == 3) return launch_tiles<1, 8, 2, 3>(a, st);
-    if (wv == 1 && wm == 4 && wn == 2 && sc == 0) return launch_tiles<1, 4, 2, 0>(a, st);
-    if (wv == 1 && wm == 4 && wn == 8 && sc == 0) return launch_tiles<1, 4, 8, 0>(a, st);
-    if (wv == 2 && wm == 4 && wn == 4 && sc == 0) return launch_tiles<2, 4, 4, 0>(a, st);
-    if (wv == 1 && wm == 2 && wn == 4 && sc == 0) return launch_tiles<1, 2, 4, 0>(a, st);
-    if (wv == 1 && wm == 1 && wn == 4 && sc == 0) return launch_tiles<1, 1, 4, 0>(a, st);
-    if (wv == 1 && wm == 1 && wn == 2 && sc == 0) return launch_tiles<1, 1, 2, 0>(a, st);
-    if (wv == 1 && wm == 1 && wn == 1 && sc == 0) return launch_tiles<1, 1, 1, 0>(a, st);
-    if (wv == 1 && wm == 2 && wn == 1 && sc == 0) return launch_tiles<1, 2, 1, 0>(a, st);
-    if (wv == 1 && wm == 2 && wn == 2 && sc == 0) return launch_tiles<1, 2, 2, 0>(a, st);
+  if constexpr (sizeof...(E) == 0) {
+    // AWQ_GEMM_TILE = "waves_m,wm,wn,sched" selects another tiling (tuning sweeps)
+    struct TileEnv {
+      int wv = 0, wm = 0, wn = 0, sc = 0;
+      bool set = false;
+    };
+    TileEnv tile_env;
+    if (const char* env = tuning_env("AWQ_GEMM_TILE")) {
+      tile_env.set = sscanf(env, "%d,%d,%d,%d", &tile_env.wv, &tile_env.wm, &tile_env.wn, &tile_env.sc) == 4;
+    }
+    if (tile_env.set) {
+      const int wv = tile_env.wv, wm = tile_env.wm, wn = tile_env.wn, sc = tile_env.sc;
+      if (wv == 1 && wm == 4 && wn == 4 && sc == 0) return launch_tiles<1, 4, 4, 0>(a, st);
+      if (wv == 1 && wm == 4 && wn == 4 && sc == 2) return launch_tiles<1, 4, 4, 2>(a, st);
+      if (wv == 1 && wm == 4 && wn == 4 && sc == 3) return launch_tiles<1, 4, 4, 3>(a, st);
+      if (wv == 1 && wm == 4 && wn == 4 && sc == 4) return launch_tiles<1, 4, 4, 4>(a, st);
+      if (wv == 1 && wm == 8 && wn == 4 && sc == 0) return launch_tiles<1, 8, 4, 0>(a, st);
+      if (wv == 1 && wm == 8 && wn == 4 && sc == 2) return launch_tiles<1, 8, 4, 2>(a, st);
+      if (wv == 1 && wm == 8 && wn == 2 && sc == 0) return launch_tiles<1, 8, 2, 0>(a, st);
+      if (wv == 1 && wm == 8 && wn == 2 && sc == 3) return launch_tiles<1, 8, 2, 3>(a, st);
+      if (wv == 1 && wm == 4 && wn == 2 && sc == 0) return launch_tiles<1, 4, 2, 0>(a, st);
+      if (wv == 1 && wm == 4 && wn == 8 && sc == 0) return launch_tiles<1, 4, 8, 0>(a, st);
+      if (wv == 2 && wm == 4 && wn == 4 && sc == 0) return launch_tiles<2, 4, 4, 0>(a, st);
+      if (wv == 1 && wm == 2 && wn == 4 && sc == 0) return launch_tiles<1, 2, 4, 0>(a, st);
+      if (wv == 1 && wm == 1 && wn == 4 && sc == 0) return launch_tiles<1, 1, 4, 0>(a, st);
+      if (wv == 1 && wm == 1 && wn == 2 && sc == 0) return launch_tiles<1, 1, 2, 0>(a, st);
+      if (wv == 1 && wm == 1 && wn == 1 && sc == 0) return launch_tiles<1, 1, 1, 0>(a, st);
+      if (wv == 1 && wm == 2 && wn == 1 && sc == 0) return launch_tiles<1, 2, 1, 0>(a, st);
+      if (wv == 1 && wm == 2 && wn == 2 && sc == 0) return launch_tiles<1, 2, 2, 0>(a, st);
+    }
   }
   // Defaults from sweeps on MI355X: at M <= 64 the product is bound by streaming the
   // weights, and narrow workgroup tiles give the most workgroups (16 x 64 up to M = 16 for
@@ -604,14 +651,26 @@ hipError_t launch_gemm(const uint16_t* x, const uint16_t* inv_s_c, const void* p
   // the workgroups cover the CUs about 2.5 times; at larger M a 64 x 256 tile (each wavefront
   // 64 x 64) runs best, or for long K or wide N a 128 x 128 tile (each wavefront 128 x
   // 32), which dequantizes each weight fragment for 8 row tiles.
-  if (M <= 16 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 1, 1>(a, ks, st);
-  if (M <= 16) return launch_tiles_ks<1, 1, 2>(a, ks, st);
-  if (M <= 32 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 2, 1>(a, ks, st);
-  if (M <= 32) return launch_tiles_ks<1, 2, 2>(a, ks, st);
-  if (M <= 64 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 2, 2>(a, ks, st);
-  if (M <= 64) return launch_tiles_ks<1, 4, 2>(a, ks, st);
-  if (K >= 8192 || N >= 16384) return launch_tiles<1, 8, 2>(a, st);
-  return launch_tiles<1, 4, 4>(a, st);
+  if (M <= 16 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 1, 1>(a, ks, st, epi...);
+  if (M <= 16) return launch_tiles_ks<1, 1, 2>(a, ks, st, epi...);
+  if (M <= 32 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 2, 1>(a, ks, st, epi...);
+  if (M <= 32) return launch_tiles_ks<1, 2, 2>(a, ks, st, epi...);
+  if (M <= 64 && N * K <= (int64_t{1} << 26)) return launch_tiles_ks<1, 2, 2>(a, ks, st, epi...);
+  if (M <= 64) return launch_tiles_ks<1, 4, 2>(a, ks, st, epi...);
+  if (K >= 8192 || N >= 16384) return launch_tiles<1, 8, 2>(a, st, epi...);
+  return launch_tiles<1, 4, 4>(a, st, epi...);
+}
+
+hipError_t launch_gemm(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
+                       int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt, uint16_t* y,
+                       void* ws, size_t ws_bytes, hipStream_t st) {
+  return gemm_impl(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, st);
+}
+
+hipError_t launch_gemm_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
+                             int64_t N, int64_t K, int32_t group, int32_t fmt, const Epilogue& e,
+                             uint16_t* y, void* ws, size_t ws_bytes, hipStream_t st) {
+  return gemm_impl(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, st, e);
 }
 
 }  // namespace awq

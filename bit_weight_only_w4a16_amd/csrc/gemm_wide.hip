@@ -27,6 +27,7 @@
 //    128 x 192 / 128 x 128 with three / two column tiles per wavefront); accumulators in
 //    VGPRs. With few output blocks, eight wavefronts split K in two (see KS below).
 #include "awq_internal.hpp"
+#include "epilogue.hpp"
 
 namespace awq {
 namespace {
@@ -60,8 +61,9 @@ __global__ void __launch_bounds__(256) prescale_kernel(const uint16_t* x, const 
 // groups with their own pair of LDS buffers, and add their sums to those of wavefronts
 // 0..3 through LDS at the end (in a fixed order), which gives two wavefronts per SIMD
 // when there are too few output blocks to fill the CUs twice.
-template <int WN, int KS, bool ASYM>
-__global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a) {
+// E: nothing, or the Epilogue of the sums, which then are not split across workgroups.
+template <int WN, int KS, bool ASYM, typename... E>
+__global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a, E... epi) {
   constexpr int WM = 8;
   constexpr int BN = 4 * WN * 16;
   extern __shared__ __attribute__((aligned(1024))) unsigned char smem_all[];  // [KS][2][kBM][256 B]
@@ -276,6 +278,60 @@ __global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a) {
     __syncthreads();
   }
 
+  if constexpr (sizeof...(E) > 0) {
+    // Unsplit sums with an Epilogue go through LDS, so that a lane gets eight consecutive
+    // outputs of a row and the tail's operands and y move in 16-byte accesses instead of
+    // 2-byte ones. Column tile j of row tile ms of the wavefront has the 1 KiB at
+    // ((ms WN + j) 4 + wave) KiB: for KS = 2 (128 KiB of LDS) where the second half's sums of
+    // that tile, read just before, were; for KS = 1 (64 KiB) four row tiles at a time.
+    constexpr int PASSES = KS == 2 ? 1 : 2, MSP = WM / PASSES;
+    float4_t* red = reinterpret_cast<float4_t*>(smem_all);
+    if constexpr (KS == 2) {
+      if (half == 1) {
+#pragma unroll
+        for (int ms = 0; ms < WM; ++ms)
+#pragma unroll
+          for (int j = 0; j < WN; ++j) red[((ms * WN + j) * 4 + wave) * 64 + lane] = acc[ms][j];
+      }
+      __syncthreads();
+      if (half == 1) return;
+    }
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass) {
+#pragma unroll
+      for (int ms = 0; ms < MSP; ++ms) {
+#pragma unroll
+        for (int j = 0; j < WN; ++j) {
+          const int slot = (ms * WN + j) * 4 + wave;
+          float4_t v = acc[pass * MSP + ms][j];
+          if constexpr (KS == 2) {
+            v += red[slot * 64 + lane];
+            wave_lds_fence();  // the slot is read before it is written again
+          }
+          float* tile = reinterpret_cast<float*>(smem_all) + slot * 256;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tile[(4 * p + q) * 16 + r] = v[q];
+        }
+      }
+      wave_lds_fence();
+#pragma unroll 1
+      for (int at = lane; at < MSP * 32 * WN; at += 64) {  // eight outputs each
+        const int ms = at / (32 * WN), row = at / (2 * WN) % 16, oct = at % (2 * WN);
+        const int m = m_blk + (pass * MSP + ms) * 16 + row, n = n_blk + wave * WN * 16 + 8 * oct;
+        if (m < a.M && n < a.N) {
+          const float* src = reinterpret_cast<const float*>(smem_all) +
+                             ((ms * WN + (oct >> 1)) * 4 + wave) * 256 + row * 16 + 8 * (oct & 1);
+          const float4_t lo = *reinterpret_cast<const float4_t*>(src);
+          const float4_t hi = *reinterpret_cast<const float4_t*>(src + 4);
+          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+          apply_epilogue8(v, n, static_cast<int64_t>(m) * a.N + n, epi..., a.y);
+        }
+      }
+      wave_lds_fence();
+    }
+    return;
+  }
+
   if constexpr (KS == 2) {
     // the second half's sums through LDS (its buffers are free now): float4 i of lane l
     // of column slot w at [i][w][l], so that consecutive lanes write consecutive 16 bytes
@@ -319,27 +375,41 @@ __global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a) {
   }
 }
 
-template <int WN, int KS, bool ASYM>
-hipError_t launch_wide_fmt(WideArgs a, hipStream_t st) {
+hipError_t reduce_splits(const WideArgs& a, hipStream_t st) {
+  return launch_splitk_reduce(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.y, st);
+}
+hipError_t reduce_splits(const WideArgs& a, hipStream_t st, const Epilogue& e) {
+  return launch_splitk_reduce_fused(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.N, e, a.y, st);
+}
+
+template <int WN, int KS, bool ASYM, typename... E>
+hipError_t launch_wide_kernel(WideArgs a, hipStream_t st, E... epi) {
   constexpr int BN = 4 * WN * 16;
   const size_t lds = 2ull * KS * kTileBytes;
   static std::atomic<uint64_t> lds_done{0};
-  const hipError_t ea = ensure_lds_limit(reinterpret_cast<const void*>(&gemm_wide_kernel<WN, KS, ASYM>),
+  const hipError_t ea = ensure_lds_limit(reinterpret_cast<const void*>(&gemm_wide_kernel<WN, KS, ASYM, E...>),
                                          static_cast<int>(lds), lds_done);
   if (ea != hipSuccess) return ea;
   a.n_blocks_m = (a.M + kBM - 1) / kBM;
   a.n_blocks_n = (a.N + BN - 1) / BN;
   const unsigned blocks = static_cast<unsigned>(a.n_blocks_m) * static_cast<unsigned>(a.n_blocks_n);
-  hipLaunchKernelGGL((gemm_wide_kernel<WN, KS, ASYM>), dim3(blocks, a.splits), dim3(256 * KS),
-                     lds, st, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.splits == 1) return e;
-  return launch_splitk_reduce(a.part, a.splits, static_cast<int64_t>(a.M) * a.N, a.y, st);
+  hipLaunchKernelGGL((gemm_wide_kernel<WN, KS, ASYM, E...>), dim3(blocks, a.splits), dim3(256 * KS),
+                     lds, st, a, epi...);
+  return hipGetLastError();
 }
 
-template <int WN, int KS>
-hipError_t launch_wide(const WideArgs& a, hipStream_t st) {
-  return a.zeros_off >= 0 ? launch_wide_fmt<WN, KS, true>(a, st) : launch_wide_fmt<WN, KS, false>(a, st);
+// Sums split across workgroups leave the Epilogue to the launch that adds them.
+template <int WN, int KS, bool ASYM, typename... E>
+hipError_t launch_wide_fmt(const WideArgs& a, hipStream_t st, E... epi) {
+  if (a.splits == 1) return launch_wide_kernel<WN, KS, ASYM>(a, st, epi...);
+  const hipError_t e = launch_wide_kernel<WN, KS, ASYM>(a, st);
+  return e != hipSuccess ? e : reduce_splits(a, st, epi...);
+}
+
+template <int WN, int KS, typename... E>
+hipError_t launch_wide(const WideArgs& a, hipStream_t st, E... epi) {
+  return a.zeros_off >= 0 ? launch_wide_fmt<WN, KS, true>(a, st, epi...)
+                          : launch_wide_fmt<WN, KS, false>(a, st, epi...);
 }
 
 // Column tiles per wavefront and K split for an M x N product, aiming at two workgroups
@@ -388,9 +458,10 @@ size_t gemm_wide_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 // workgroups only when the workspace (ws_bytes) holds its partial sums as well.
 // cfg = 100 * splits + 10 * column tiles per wavefront + K split in the workgroup, or 0
 // for the default choice.
-hipError_t launch_gemm_wide(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
-                            int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt,
-                            uint16_t* y, void* ws, size_t ws_bytes, int cfg, hipStream_t st) {
+template <typename... E>
+static hipError_t wide_impl(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
+                            int64_t N, int64_t K, int32_t group, int32_t fmt, uint16_t* y, void* ws,
+                            size_t ws_bytes, int cfg, hipStream_t st, E... epi) {
   const PackedLayout L = make_layout(N, K, group, fmt);
   const uint16_t* xs = x;
   if (inv_s_c != nullptr) {
@@ -424,13 +495,27 @@ hipError_t launch_gemm_wide(const uint16_t* x, const uint16_t* inv_s_c, const vo
     a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + part_off);
   }
   const int wn = w.wn, ks = w.ks;
-  if (wn == 4 && ks == 1) return launch_wide<4, 1>(a, st);
-  if (wn == 4 && ks == 2) return launch_wide<4, 2>(a, st);
-  if (wn == 3 && ks == 1) return launch_wide<3, 1>(a, st);
-  if (wn == 3 && ks == 2) return launch_wide<3, 2>(a, st);
-  if (wn == 2 && ks == 1) return launch_wide<2, 1>(a, st);
-  if (wn == 2 && ks == 2) return launch_wide<2, 2>(a, st);
+  if (wn == 4 && ks == 1) return launch_wide<4, 1>(a, st, epi...);
+  if (wn == 4 && ks == 2) return launch_wide<4, 2>(a, st, epi...);
+  if (wn == 3 && ks == 1) return launch_wide<3, 1>(a, st, epi...);
+  if (wn == 3 && ks == 2) return launch_wide<3, 2>(a, st, epi...);
+  if constexpr (sizeof...(E) == 0) {  // by `cfg` only
+    if (wn == 2 && ks == 1) return launch_wide<2, 1>(a, st);
+    if (wn == 2 && ks == 2) return launch_wide<2, 2>(a, st);
+  }
   return hipErrorInvalidValue;
+}
+
+hipError_t launch_gemm_wide(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
+                            int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt,
+                            uint16_t* y, void* ws, size_t ws_bytes, int cfg, hipStream_t st) {
+  return wide_impl(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, cfg, st);
+}
+
+hipError_t launch_gemm_wide_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
+                                  int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt,
+                                  const Epilogue& e, uint16_t* y, void* ws, size_t ws_bytes, hipStream_t st) {
+  return wide_impl(x, inv_s_c, packed, M, N, K, group, fmt, y, ws, ws_bytes, 0, st, e);
 }
 
 }  // namespace awq

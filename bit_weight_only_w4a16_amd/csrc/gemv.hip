@@ -36,6 +36,7 @@
 // The A operand of lane l is X' row l % 16; lanes of rows >= M repeat row M - 1, whose
 // results are dropped. Lane (r, p) holds D rows 4 p .. 4 p + 3 for weight row r.
 #include "awq_internal.hpp"
+#include "epilogue.hpp"
 
 #include <stdio.h>
 #include <stdlib.h>
@@ -102,10 +103,12 @@ struct XPass {
 // compiler marks them for kernarg preloading: the command processor writes them into
 // SGPRs when it launches a wavefront, and the kernel starts without waiting for a load
 // of its argument block (0.3-0.4 us of a 4-7 us decode launch on MI355X).
-template <int M, int WAVES, int BATCH, bool ASYM, bool EXACT, int T>
+// E: nothing, or the Epilogue applied to each sum before it is rounded.
+template <int M, int WAVES, int BATCH, bool ASYM, bool EXACT, int T, typename... E>
 __global__ void __launch_bounds__(WAVES * 64)
     gemv_kernel(const uint16_t* x, const uint16_t* inv, const uint8_t* packed, uint16_t* y,
-                uint32_t scales_off, uint32_t zeros_off, int N, int K, int phase_groups, int n_sets) {
+                uint32_t scales_off, uint32_t zeros_off, int N, int K, int phase_groups, int n_sets,
+                E... epi) {
   MvArgs a;
   a.x = x;
   a.inv = inv;
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(WAVES * 64)
     for (int w = 1; w < WAVES; ++w) v += red[(w * M + m) * TN + c];
     const int n = t0 * kTileN + c;
     if (n < a.N) {
+      if constexpr (sizeof...(E) > 0) v = apply_epilogue(v, n, static_cast<int64_t>(m) * a.N + n, epi...);
       a.y[static_cast<int64_t>(m) * a.N + n] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
     }
   }
@@ -359,33 +363,33 @@ size_t smem_bytes(int M, int phase_groups, int waves, int T) {
          4ull * waves * M * kTileN * T;
 }
 
-template <int M, int WAVES, int BATCH, bool ASYM, bool EXACT, int T>
-hipError_t launch_fmt(const MvArgs& a, int64_t n_tiles, hipStream_t st) {
+template <int M, int WAVES, int BATCH, bool ASYM, bool EXACT, int T, typename... E>
+hipError_t launch_fmt(const MvArgs& a, int64_t n_tiles, hipStream_t st, E... epi) {
   const size_t lds = smem_bytes(M, a.phase_groups, WAVES, T);
   static std::atomic<uint64_t> lds_done{0};
   const hipError_t ea = ensure_lds_limit(
-      reinterpret_cast<const void*>(&gemv_kernel<M, WAVES, BATCH, ASYM, EXACT, T>), 163840, lds_done);
+      reinterpret_cast<const void*>(&gemv_kernel<M, WAVES, BATCH, ASYM, EXACT, T, E...>), 163840, lds_done);
   if (ea != hipSuccess) return ea;
-  hipLaunchKernelGGL((gemv_kernel<M, WAVES, BATCH, ASYM, EXACT, T>),
+  hipLaunchKernelGGL((gemv_kernel<M, WAVES, BATCH, ASYM, EXACT, T, E...>),
                      dim3(static_cast<unsigned>((n_tiles + T - 1) / T)), dim3(WAVES * 64), lds, st,
                      a.x, a.inv, a.packed, a.y, static_cast<uint32_t>(a.scales_off),
-                     static_cast<uint32_t>(ASYM ? a.zeros_off : 0), a.N, a.K, a.phase_groups, a.sets);
+                     static_cast<uint32_t>(ASYM ? a.zeros_off : 0), a.N, a.K, a.phase_groups, a.sets, epi...);
   return hipGetLastError();
 }
 
 // The per-group correction needs the activation sums O and S of every row: from five
 // rows on, staging them costs more than dequantizing each weight exactly, so M > 4 (and
 // groups of 32 or 64) take the exact form.
-template <int M, int WAVES, int BATCH, int T = 1>
-hipError_t launch_cfg(const MvArgs& a, int64_t n_tiles, hipStream_t st) {
+template <int M, int WAVES, int BATCH, int T = 1, typename... E>
+hipError_t launch_cfg(const MvArgs& a, int64_t n_tiles, hipStream_t st, E... epi) {
   const bool asym = a.zeros_off >= 0;
   if (M > 4 || a.sets > 1) {
-    return asym ? launch_fmt<M, WAVES, BATCH, true, true, T>(a, n_tiles, st)
-                : launch_fmt<M, WAVES, BATCH, false, true, T>(a, n_tiles, st);
+    return asym ? launch_fmt<M, WAVES, BATCH, true, true, T>(a, n_tiles, st, epi...)
+                : launch_fmt<M, WAVES, BATCH, false, true, T>(a, n_tiles, st, epi...);
   }
   if constexpr (M <= 4) {
-    return asym ? launch_fmt<M, WAVES, BATCH, true, false, T>(a, n_tiles, st)
-                : launch_fmt<M, WAVES, BATCH, false, false, T>(a, n_tiles, st);
+    return asym ? launch_fmt<M, WAVES, BATCH, true, false, T>(a, n_tiles, st, epi...)
+                : launch_fmt<M, WAVES, BATCH, false, false, T>(a, n_tiles, st, epi...);
   }
   return hipErrorInvalidValue;
 }
@@ -419,15 +423,15 @@ int waves_for(int M, int n_groups, int64_t n_tiles) {
   return M <= 4 && n_groups >= 64 && n_tiles <= 512 ? 16 : 8;
 }
 
-template <int M>
-hipError_t launch_m(const MvArgs& a, int64_t n_tiles, int T, hipStream_t st) {
+template <int M, typename... E>
+hipError_t launch_m(const MvArgs& a, int64_t n_tiles, int T, hipStream_t st, E... epi) {
   if constexpr (M <= 4) {
-    if (waves_for(M, a.n_groups, n_tiles) == 16) return launch_cfg<M, 16, 1>(a, n_tiles, st);
+    if (waves_for(M, a.n_groups, n_tiles) == 16) return launch_cfg<M, 16, 1>(a, n_tiles, st, epi...);
   }
-  if (T == 4) return launch_cfg<M, 8, 1, 4>(a, n_tiles, st);
-  if (T == 3) return launch_cfg<M, 8, 1, 3>(a, n_tiles, st);
-  if (T == 2) return launch_cfg<M, 8, 1, 2>(a, n_tiles, st);
-  return launch_cfg<M, 8, 1>(a, n_tiles, st);
+  if (T == 4) return launch_cfg<M, 8, 1, 4>(a, n_tiles, st, epi...);
+  if (T == 3) return launch_cfg<M, 8, 1, 3>(a, n_tiles, st, epi...);
+  if (T == 2) return launch_cfg<M, 8, 1, 2>(a, n_tiles, st, epi...);
+  return launch_cfg<M, 8, 1>(a, n_tiles, st, epi...);
 }
 
 // Tuning override for sweeps (M = 1 only, libraries built for tuning): AWQ_GEMV_CFG =
@@ -447,6 +451,57 @@ hipError_t launch_m1(const MvArgs& a, int64_t n_tiles, int T, hipStream_t st) {
     case 161: return launch_cfg<1, 16, 1>(a, n_tiles, st);
     case 162: return launch_cfg<1, 16, 2>(a, n_tiles, st);
     default: return launch_m<1>(a, n_tiles, T, st);
+  }
+}
+
+// The kernel's arguments and row tiles per workgroup for an M x N x K product.
+MvArgs product_args(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M, int64_t N,
+                    int64_t K, int32_t group, int32_t fmt, uint16_t* y, int64_t& n_tiles, int& T) {
+  const PackedLayout L = make_layout(N, K, group, fmt);
+  MvArgs a;
+  a.x = x;
+  a.inv = inv_s_c;
+  a.packed = static_cast<const uint8_t*>(packed);
+  a.y = y;
+  a.scales_off = L.scales_off;
+  a.zeros_off = L.zeros_off;
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.n_groups = static_cast<int>(L.n_groups);
+  a.sets = static_cast<int>(L.sets);
+  n_tiles = L.n_tiles;
+  T = tiles_per_wg(static_cast<int>(M), L.n_tiles);
+  a.phase_groups = phase_groups_for(static_cast<int>(M), a.n_groups, L.n_tiles, T,
+                                    T == 1 ? waves_for(static_cast<int>(M), a.n_groups, L.n_tiles) : 8);
+  return a;
+}
+
+template <typename... E>
+hipError_t dispatch_m(const MvArgs& a, int64_t M, int64_t n_tiles, int T, hipStream_t st, E... epi) {
+  switch (M) {
+    case 1:
+      // the tuning configurations exist for the plain product only
+      if constexpr (sizeof...(E) == 0) {
+        return launch_m1(a, n_tiles, T, st);
+      } else {
+        return launch_m<1>(a, n_tiles, T, st, epi...);
+      }
+    case 2: return launch_m<2>(a, n_tiles, T, st, epi...);
+    case 3: return launch_m<3>(a, n_tiles, T, st, epi...);
+    case 4: return launch_m<4>(a, n_tiles, T, st, epi...);
+    case 5: return launch_m<5>(a, n_tiles, T, st, epi...);
+    case 6: return launch_m<6>(a, n_tiles, T, st, epi...);
+    case 7: return launch_m<7>(a, n_tiles, T, st, epi...);
+    case 8: return launch_m<8>(a, n_tiles, T, st, epi...);
+    case 9: return launch_m<9>(a, n_tiles, T, st, epi...);
+    case 10: return launch_m<10>(a, n_tiles, T, st, epi...);
+    case 11: return launch_m<11>(a, n_tiles, T, st, epi...);
+    case 12: return launch_m<12>(a, n_tiles, T, st, epi...);
+    case 13: return launch_m<13>(a, n_tiles, T, st, epi...);
+    case 14: return launch_m<14>(a, n_tiles, T, st, epi...);
+    case 15: return launch_m<15>(a, n_tiles, T, st, epi...);
+    case 16: return launch_m<16>(a, n_tiles, T, st, epi...);
+    default: return hipErrorInvalidValue;
   }
 }
 
@@ -470,40 +525,19 @@ int gemv_phases(int64_t M, int64_t N, int64_t K) {
 hipError_t launch_gemv(const uint16_t* x, const uint16_t* inv_s_c, const void* packed,
                        int64_t M, int64_t N, int64_t K, int32_t group, int32_t fmt, uint16_t* y,
                        void*, size_t, hipStream_t st) {
-  const PackedLayout L = make_layout(N, K, group, fmt);
-  MvArgs a;
-  a.x = x;
-  a.inv = inv_s_c;
-  a.packed = static_cast<const uint8_t*>(packed);
-  a.y = y;
-  a.scales_off = L.scales_off;
-  a.zeros_off = L.zeros_off;
-  a.N = static_cast<int>(N);
-  a.K = static_cast<int>(K);
-  a.n_groups = static_cast<int>(L.n_groups);
-  a.sets = static_cast<int>(L.sets);
-  const int T = tiles_per_wg(static_cast<int>(M), L.n_tiles);
-  a.phase_groups = phase_groups_for(static_cast<int>(M), a.n_groups, L.n_tiles, T,
-                                    T == 1 ? waves_for(static_cast<int>(M), a.n_groups, L.n_tiles) : 8);
-  switch (M) {
-    case 1: return launch_m1(a, L.n_tiles, T, st);
-    case 2: return launch_m<2>(a, L.n_tiles, T, st);
-    case 3: return launch_m<3>(a, L.n_tiles, T, st);
-    case 4: return launch_m<4>(a, L.n_tiles, T, st);
-    case 5: return launch_m<5>(a, L.n_tiles, T, st);
-    case 6: return launch_m<6>(a, L.n_tiles, T, st);
-    case 7: return launch_m<7>(a, L.n_tiles, T, st);
-    case 8: return launch_m<8>(a, L.n_tiles, T, st);
-    case 9: return launch_m<9>(a, L.n_tiles, T, st);
-    case 10: return launch_m<10>(a, L.n_tiles, T, st);
-    case 11: return launch_m<11>(a, L.n_tiles, T, st);
-    case 12: return launch_m<12>(a, L.n_tiles, T, st);
-    case 13: return launch_m<13>(a, L.n_tiles, T, st);
-    case 14: return launch_m<14>(a, L.n_tiles, T, st);
-    case 15: return launch_m<15>(a, L.n_tiles, T, st);
-    case 16: return launch_m<16>(a, L.n_tiles, T, st);
-    default: return hipErrorInvalidValue;
-  }
+  int64_t n_tiles;
+  int T;
+  const MvArgs a = product_args(x, inv_s_c, packed, M, N, K, group, fmt, y, n_tiles, T);
+  return dispatch_m(a, M, n_tiles, T, st);
+}
+
+hipError_t launch_gemv_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
+                             int64_t N, int64_t K, int32_t group, int32_t fmt, const Epilogue& e,
+                             uint16_t* y, hipStream_t st) {
+  int64_t n_tiles;
+  int T;
+  const MvArgs a = product_args(x, inv_s_c, packed, M, N, K, group, fmt, y, n_tiles, T);
+  return dispatch_m(a, M, n_tiles, T, st, e);
 }
 
 }  // namespace awq

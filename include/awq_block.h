@@ -33,6 +33,33 @@ extern "C" {
 #define AWQ_DT_F16 0
 #define AWQ_DT_BF16 1
 
+#define AWQ_ACT_NONE 0
+#define AWQ_ACT_RELU 1
+#define AWQ_ACT_GELU 2      /* v (1 + erf(v / sqrt 2)) / 2                          */
+#define AWQ_ACT_GELU_TANH 3 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2   */
+#define AWQ_ACT_SILU 4      /* v / (1 + exp(-v))                                    */
+
+/* What awq_gemm_fused does with a sum v of output n, row m; each pointer may be NULL. */
+typedef struct awq_epilogue {
+  const uint16_t* bias;     /* device, [N] binary16                                 */
+  const uint16_t* mul;      /* device, [M][N] binary16 (a gated activation's factor) */
+  const uint16_t* residual; /* device, [M][N] binary16                              */
+  int32_t act;              /* AWQ_ACT_*                                            */
+  int32_t reserved;         /* 0                                                    */
+} awq_epilogue;
+
+/*
+ * awq_gemm_fused - awq_gemm with the element-wise tail of a decoder's projections:
+ *   y[m][n] = binary16( act(v + bias[n]) * mul[m][n] + residual[m][n] ),
+ * v the float32 sum that awq_gemm would round. Any M; the arguments, kernels, choice by
+ * shape and workspace (awq_workspace_bytes) are awq_gemm's. mul and residual may be y
+ * itself (each element is read by the thread that then writes it).
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, HIP.
+ */
+int awq_gemm_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
+                   int64_t N, int64_t K, int32_t group, int32_t fmt, const awq_epilogue* epilogue,
+                   uint16_t* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /*
  * awq_rope - rotary positions for q and k, and the write of k and v into a paged cache.
  * For pair i < rot_dim / 2 of a head, with angle = positions[t] * inv_freq[i]:
