@@ -9,6 +9,7 @@ kernels; there is no fallback. If the library is missing, the first call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -127,6 +128,10 @@ def _same_device(ref: torch.Tensor, **named) -> None:
 
 
 def _stream(device=None) -> int:
+    """The current stream's handle; for a device number without forming a Stream object,
+    which costs more than a microsecond of a decode call's host time."""
+    if isinstance(device, int):
+        return torch._C._cuda_getCurrentRawStream(device)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -169,6 +174,7 @@ def awq_pack(w: torch.Tensor, s_c: torch.Tensor | None = None, group: int = GROU
     return qweight, scales, qzeros
 
 
+@functools.lru_cache(maxsize=None)
 def awq_repacked_bytes(n: int, k: int, group: int = GROUP, fmt: int = FMT_ASYM) -> int:
     return int(lib().awq_repacked_bytes(n, k, group, fmt))
 
@@ -211,6 +217,7 @@ def awq_dequant(w, scales, qzeros, layout: int, n: int, k: int, group: int = GRO
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def awq_workspace_bytes(m: int, n: int, k: int, group: int = GROUP) -> int:
     return int(lib().awq_workspace_bytes(m, n, k, group))
 
@@ -372,7 +379,7 @@ def workspace(m: int, n: int, k: int, device, group: int = GROUP) -> torch.Tenso
         return None
     dev = torch.device(device)
     index = dev.index if dev.index is not None else torch.cuda.current_device()
-    key = (dev.type, index, torch.cuda.current_stream(index).cuda_stream)
+    key = (dev.type, index, _stream(index))
     cur = _WS.get(key)
     if cur is None or cur.numel() < need:
         cur = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)

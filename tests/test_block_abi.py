@@ -56,6 +56,15 @@ def test_structures_match_the_header(tmp_path):
             assert int(got[f"{c}.{f[0]}"]) == getattr(py, f[0]).offset, f"{c}.{f[0]}"
 
 
+def test_packed_arguments_have_the_structures_layout():
+    for packed, py in ((block._ROPE, block.RopeArgs), (block._PROMPT, block.AttnPromptArgs),
+                       (block._TREE, block.AttnTreeArgs), (block._EPILOGUE, block.Epilogue)):
+        assert packed.size == ctypes.sizeof(py)
+        values = list(range(1, len(py._fields_) + 1))
+        got = py.from_buffer_copy(packed.pack(*values))
+        assert [int(getattr(got, f[0])) for f in py._fields_] == values
+
+
 def call(fn, args):
     return fn(ctypes.byref(args), None)
 
