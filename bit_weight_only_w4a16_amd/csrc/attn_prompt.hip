@@ -240,24 +240,26 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   l = xor32_add(l);
   const float inv = inv_sum(l);
   bool broken = false;
-  uint16_t* o = a.out + (start + row) * a.o_token + head * a.o_head;
 #pragma unroll
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = acc[dt][i + e] * inv;
-        broken |= v[e] != v[e];
-      }
-      const int d = 32 * dt + 2 * i + 4 * h;
-      if (row < len && d < a.head_dim)
-        *reinterpret_cast<uint2*>(o + d) = make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
-    }
-  // rows that came out NaN: again, key by key (a masked infinity or NaN may be the cause)
+    for (int i = 0; i < 16; ++i) broken |= acc[dt][i] != acc[dt][i];
+  broken |= inv != inv;
+  // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
   uint64_t again = __ballot(broken && row < len);
   again = (again | (again >> 32)) & 0xFFFFFFFFu;
+  if (row < len && ((again >> col) & 1) == 0) {
+    uint16_t* o = a.out + (start + row) * a.o_token + head * a.o_head;
+#pragma unroll
+    for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const int d = 32 * dt + 2 * i + 4 * h;
+        if (d < a.head_dim)
+          *reinterpret_cast<uint2*>(o + d) = make_uint2(T::pack2(acc[dt][i] * inv, acc[dt][i + 1] * inv),
+                                                        T::pack2(acc[dt][i + 2] * inv, acc[dt][i + 3] * inv));
+      }
+  }
   while (again != 0) {
     const int i = __builtin_ctzll(again);
     again &= again - 1;

@@ -17,6 +17,9 @@
 // O^T, and V^T is read from LDS in that order with the transposing 16-bit read.
 #include "block_internal.hpp"
 
+#include <math.h>
+#include <stdlib.h>
+
 namespace awq {
 namespace {
 
@@ -26,6 +29,9 @@ constexpr int kStages = 2;
 constexpr int kMinChunk = kStep * kWaves;  // positions per split: a multiple of this
 constexpr int kTableEntries = 1024;        // page numbers of a split staged in LDS
 constexpr int kMaxSplits = 64;
+// P carries a factor 2^kShift: with the maximum in use at most kSlack below the true one,
+// binary16 holds it, and probabilities down to 2^-21 of the maximum keep their digits
+constexpr float kShift = 7.0f, kSlack = 8.0f;
 
 struct TreeArgs {
   const uint16_t *q, *k, *v;
@@ -37,8 +43,15 @@ struct TreeArgs {
   int64_t max_len;  // table_width * page_size
   int32_t tokens, seqs, table_width, pages, page_size, max_q, q_heads, kv_heads, group, head_dim;
   int32_t splits, row_blocks;
+  uint32_t page_mul, page_shift;  // pos / page_size = pos * page_mul >> page_shift
   float c;  // scale * log2(e)
 };
+
+// pos / page_size for 0 <= pos < 2^31 (page_mul = floor(2^page_shift / page_size) + 1 with
+// page_shift = 31 + ceil(log2 page_size): the excess stays below one part in 2^31).
+__device__ __forceinline__ int page_of(const TreeArgs& a, int pos) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * a.page_mul) >> a.page_shift);
+}
 
 // A sequence's tokens, context and length, clamped to what the buffers hold
 struct Seq {
@@ -68,6 +81,27 @@ __device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
   return left < 32 ? bits & ((1u << left) - 1u) : bits;
 }
 
+// Waits until at most N of this wavefront's memory loads are on their way (they land in
+// order). Every load instruction of a step counts: each row's lanes cover all its chunks, so
+// with D < DP some lane takes part in each.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  // vmcnt in bits 0..3 and 14..15, the other counters at their largest: not waited for
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only
+  asm volatile("" ::: "memory");
+}
+// A barrier for LDS alone: loads into LDS that are on their way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // The factor that brings a partial result with maximum m and sum l to the maximum top. A
 // part that saw no finite score (m = -inf) has l = 0, or NaN if it saw a NaN, and passes
 // that on.
@@ -82,6 +116,27 @@ __device__ __forceinline__ int k_pos(int r, int c) {
 template <int DP>
 __device__ __forceinline__ int v_pos(int r, int c) {
   return DP == 128 ? c ^ ((r & 7) << 1) : c ^ (((r >> 1) & 3) << 1);
+}
+
+// One wavefront writes a row's result (lane i has d = 2 i, 2 i + 1): the output, or the
+// split's partial result.
+template <typename T>
+__device__ __forceinline__ void store_row(const TreeArgs& a, int token, int hq, int split, float m, float l,
+                                          float2_t o) {
+  const int lane = threadIdx.x & 63;
+  if (2 * lane >= a.head_dim) return;
+  if (a.part != nullptr) {
+    const int64_t at = (static_cast<int64_t>(token) * a.q_heads + hq) * a.splits + split;
+    *reinterpret_cast<float2_t*>(a.part + at * a.head_dim + 2 * lane) = o;
+    if (lane == 0) {
+      float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
+      *reinterpret_cast<float2_t*>(ml + 2 * at) = float2_t{m, l};
+    }
+  } else {
+    const float inv = inv_sum(l);
+    *reinterpret_cast<uint32_t*>(a.out + token * a.o_token + hq * a.o_head + 2 * lane) =
+        T::pack2(o.x * inv, o.y * inv);
+  }
 }
 
 // LDS bytes of a workgroup: the rings (later the four float32 results), Q, the page numbers
@@ -125,8 +180,8 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   if (p0 >= p1 && a.part != nullptr) return;  // the second launch knows that it is empty
 
   // page numbers of the split, clamped to the cache
-  const int t0 = p0 / a.page_size;
-  const int n_pages = p1 > p0 ? (p1 - 1) / a.page_size - t0 + 1 : 0;
+  const int t0 = page_of(a, p0);
+  const int n_pages = p1 > p0 ? page_of(a, p1 - 1) - t0 + 1 : 0;
   for (int i = threadIdx.x; i < n_pages; i += 256)
     pages[i] = min(max(a.table[static_cast<int64_t>(b) * a.table_width + t0 + i], 0), a.pages - 1);
   // Q rows (row r: token r / group, head r % group of the key head), 0 past the last
@@ -157,28 +212,34 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   const uint16_t* kbase = a.k + kv_head * a.cache_head;
   const uint16_t* vbase = a.v + kv_head * a.cache_head;
   auto offset_of = [&](int pos) -> int64_t {
-    const int page = pos / a.page_size;
+    const int page = page_of(a, pos);
     return pages[page - t0] * a.cache_page + (pos - page * a.page_size) * a.cache_slot;
   };
-  // loads of the step at position s0; positions past the split repeat its last one (their
-  // scores are masked and their V rows cleared below)
-  auto load_step = [&](int s0, int stage) {
+  // where this lane loads from in the step at position s0: load j takes position ROWS j + l / RC
+  // (positions past the split repeat its last one: their scores are masked and their V rows
+  // cleared below)
+  auto find_step = [&](int s0, int64_t at[LOADS]) {
     const int64_t off = offset_of(min(s0 + (lane & 31), p1 - 1));
     const int off_lo = static_cast<int>(off), off_hi = static_cast<int>(off >> 32);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const uint32_t lo = __shfl(off_lo, ROWS * j + lane / RC), hi = __shfl(off_hi, ROWS * j + lane / RC);
+      at[j] = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
+    }
+  };
+  auto load_step = [&](const int64_t at[LOADS], int stage) {
     unsigned char* dst = ring + stage * 2 * TILE;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       const int r = ROWS * j + lane / RC;
-      const uint32_t lo = __shfl(off_lo, r), hi = __shfl(off_hi, r);
-      const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(hi) << 32) | lo);
       const int ck = 8 * k_pos<DP>(r, lane % RC), cv = 8 * v_pos<DP>(r, lane % RC);
       if (!PAD || ck < a.head_dim)
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(kbase + at + ck),
+            (const __attribute__((address_space(1))) void*)(kbase + at[j] + ck),
             (lds_void*)(dst + j * 1024), 16, 0, 0);
       if (!PAD || cv < a.head_dim)
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(vbase + at + cv),
+            (const __attribute__((address_space(1))) void*)(vbase + at[j] + cv),
             (lds_void*)(dst + TILE + j * 1024), 16, 0, 0);
     }
   };
@@ -192,17 +253,27 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
-  // P carries 2^kShift (see kSlack: the maximum in use may be that much too small)
-  constexpr float kShift = 7.0f, kSlack = 8.0f;
 
+  // One step is used while the next is on its way, and the addresses of the one after that
+  // are found meanwhile.
   const int first = p0 + kStep * wave;
   constexpr int kStride = kStep * kWaves;
-  if (first < p1) load_step(first, 0);
+  int64_t at[LOADS];
+  if (first < p1) {
+    find_step(first, at);
+    load_step(at, 0);
+    if (first + kStride < p1) find_step(first + kStride, at);
+  }
   int stage = 0;
   for (int s0 = first; s0 < p1; s0 += kStride, stage ^= 1) {
-    __builtin_amdgcn_s_waitcnt(0);  // the step has landed
-    asm volatile("" ::: "memory");
-    if (s0 + kStride < p1) load_step(s0 + kStride, stage ^ 1);
+    if (s0 + kStride < p1) {
+      wait_lds();  // the last step's reads of this stage are done
+      load_step(at, stage ^ 1);
+      wait_loads<2 * LOADS>();  // the step has landed
+      if (s0 + 2 * kStride < p1) find_step(s0 + 2 * kStride, at);
+    } else {
+      wait_loads<0>();
+    }
     const unsigned char* ks = ring + stage * 2 * TILE;
     unsigned char* vs = ring + stage * 2 * TILE + TILE;
     if (s0 + kStep > p1) {  // V rows past the split: 0
@@ -325,25 +396,230 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
                     },
                     top, sum, o);
     }
-    if (2 * lane >= a.head_dim) continue;
-    if (a.part != nullptr) {
-      const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits + split;
-      *reinterpret_cast<float2_t*>(a.part + at * a.head_dim + 2 * lane) = o;
-      if (lane == 0) {
-        float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim + 2 * at;
-        ml[0] = top;
-        ml[1] = sum;
-      }
-    } else {
-      const float inv = inv_sum(sum);
-      *reinterpret_cast<uint32_t*>(a.out + (s.first + t) * a.o_token + hq * a.o_head + 2 * lane) =
-          T::pack2(o.x * inv, o.y * inv);
+    store_row<T>(a, s.first + t, hq, split, top, sum, o);
+  }
+}
+
+// The same for many query rows (more than 32 of a key / value head): here the wavefronts split
+// the rows, 16 each, and share the keys and values, 32 positions at a time, in a ring of
+// four steps, three of them on their way while one is used. A wavefront keeps its Q
+// operands in registers, needs no merge at the end, and the workgroup needs half the LDS,
+// so two of them share a CU.
+#ifndef KRING
+#define KRING 4
+#endif
+constexpr int kRing = KRING;
+
+template <typename T, int DP, bool PAD>
+__global__ void __launch_bounds__(256, KRING == 2 ? 4 : KRING == 3 ? 3 : 2) attn_tree_rows_kernel(TreeArgs a) {
+  typedef typename T::v8 v8;
+  constexpr int RB = DP * 2, RC = DP / 8, TILE = kStep * RB;
+  constexpr int ROWS = 1024 / RB;               // positions one load instruction fills
+  constexpr int OWN = kStep / kWaves;           // positions a wavefront loads
+  constexpr int LOADS = OWN / ROWS;             // its load instructions per step, for K and for V
+  constexpr int NC = DP / 32, ND = DP / 16;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [kRing][K tile, V tile], pages
+  int* pages = reinterpret_cast<int*>(smem + kRing * 2 * TILE);
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int col = lane & 15, g = lane >> 4;
+  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
+  const int kv_head = blockIdx.y, b = blockIdx.z;
+  const Seq s = sequence(a, b);
+  const int rows = s.count * a.group;
+  if (rb * 16 * kWaves >= rows) return;
+  const int chunk = chunk_of(s.len, a.splits);
+  const int p0 = split * chunk, p1 = min(s.len, p0 + chunk);
+  if (p0 >= p1 && a.part != nullptr) return;  // the second launch knows that it is empty
+
+  const int t0 = page_of(a, p0);
+  const int n_pages = p1 > p0 ? page_of(a, p1 - 1) - t0 + 1 : 0;
+  for (int i = threadIdx.x; i < n_pages; i += 256)
+    pages[i] = min(max(a.table[static_cast<int64_t>(b) * a.table_width + t0 + i], 0), a.pages - 1);
+  if constexpr (PAD) {  // chunks past D are never loaded: they stay 0
+    for (int i = threadIdx.x; i < kRing * 2 * TILE / 16; i += 256)
+      *reinterpret_cast<u32x4*>(smem + 16 * i) = u32x4{0, 0, 0, 0};
+  }
+  // this lane's row, its mask and its Q operands (rows past the last repeat it)
+  const int row = (rb * kWaves + wave) * 16 + col;
+  const int t = min(row, rows - 1) / a.group, hq = kv_head * a.group + min(row, rows - 1) % a.group;
+  const uint64_t sees = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
+  const uint16_t* q = a.q + (s.first + t) * a.q_token + hq * a.q_head;
+  v8 qf[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int d = 32 * c + 8 * g;
+    u32x4 x = {0, 0, 0, 0};
+    if (!PAD || d < a.head_dim) x = *reinterpret_cast<const u32x4*>(q + d);
+    qf[c] = __builtin_bit_cast(v8, x);
+  }
+  wait_loads<0>();  // Q and the mask: or the compiler waits for all loads at their use in the loop
+  __syncthreads();
+
+  const uint16_t* kbase = a.k + kv_head * a.cache_head;
+  const uint16_t* vbase = a.v + kv_head * a.cache_head;
+  auto offset_of = [&](int pos) -> int64_t {
+    const int page = page_of(a, pos);
+    return pages[page - t0] * a.cache_page + (pos - page * a.page_size) * a.cache_slot;
+  };
+  auto find_step = [&](int s0, int64_t at[LOADS]) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) at[j] = offset_of(min(s0 + OWN * wave + ROWS * j + lane / RC, p1 - 1));
+  };
+  auto load_step = [&](const int64_t at[LOADS], int stage) {
+    unsigned char* dst = smem + stage * 2 * TILE + OWN * wave * RB;
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int r = OWN * wave + ROWS * j + lane / RC;
+      const int ck = 8 * k_pos<DP>(r, lane % RC), cv = 8 * v_pos<DP>(r, lane % RC);
+      if (!PAD || ck < a.head_dim)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kbase + at[j] + ck),
+                                         (lds_void*)(dst + j * 1024), 16, 0, 0);
+      if (!PAD || cv < a.head_dim)
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(vbase + at[j] + cv),
+                                         (lds_void*)(dst + TILE + j * 1024), 16, 0, 0);
     }
+  };
+
+  float4_t acc[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d) acc[d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = kNegInf, l = 0.0f;
+  const int steps = (p1 - p0 + kStep - 1) / kStep;  // <= 0: nothing
+  int64_t at[LOADS];
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i)
+    if (i < steps) {
+      find_step(p0 + i * kStep, at);
+      load_step(at, i);
+    }
+  if (kRing - 1 < steps) find_step(p0 + (kRing - 1) * kStep, at);
+  for (int i = 0; i < steps; ++i) {
+    const int s0 = p0 + i * kStep, stage = i % kRing;
+    unsigned char* ks = smem + stage * 2 * TILE;
+    unsigned char* vs = ks + TILE;
+    // this wavefront's loads of the step have landed (those after it may be on their way)
+    if (i + kRing - 2 < steps) {
+      wait_loads<2 * LOADS * (kRing - 2)>();
+    } else {
+      wait_loads<0>();
+    }
+    // V rows past the split: 0, each wavefront among those it loaded
+    const int own = s0 + OWN * wave;
+    if (own + OWN > p1) {
+      const int from = max(p1 - own, 0);
+      for (int j = lane; j < (OWN - from) * RC; j += 64)
+        *reinterpret_cast<u32x4*>(vs + (OWN * wave + from) * RB + 16 * j) = u32x4{0, 0, 0, 0};
+    }
+    lds_barrier();  // the step is whole, and the step before it is done with
+    if (i + kRing - 1 < steps) load_step(at, (i + kRing - 1) % kRing);
+    if (i + kRing < steps) find_step(s0 + kRing * kStep, at);
+
+    float4_t sc[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      sc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int r = 16 * j + col;
+        const v8 kf = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
+        sc[j] = T::mfma16(kf, qf[c], sc[j]);
+      }
+    }
+    if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
+      const uint32_t bits = visible(sees, s0 - s.ctx, p1 - s0) >> (4 * g);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[j][e] = (bits & (1u << (16 * j + e))) != 0 ? sc[j][e] : kNegInf;
+    }
+    float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                      fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * a.c;
+    if (__ballot(top > m + kSlack) != 0) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m_new = fmaxf(m, top);
+      const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[d] *= keep;
+    }
+    const float off = m == kNegInf ? 0.0f : kShift - m;
+    u32x4 p;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][e], a.c, off));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][e + 1], a.c, off));
+        l += e0 + e1;
+        p[2 * j + (e >> 1)] = T::pack2(e0, e1);
+      }
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const int ra = 4 * g + (col >> 2), rb2 = ra + 16;
+      const int ch = 2 * d + ((col & 3) >> 1), byte = 8 * (col & 1);
+      const short4_t lo = lds_read_tr(vs + ra * RB + 16 * v_pos<DP>(ra, ch) + byte);
+      const short4_t hi = lds_read_tr(vs + rb2 * RB + 16 * v_pos<DP>(rb2, ch) + byte);
+      acc[d] = T::mfma16(join8<v8>(lo, hi), __builtin_bit_cast(v8, p), acc[d]);
+    }
+    asm volatile("" ::: "memory");
+  }
+
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  bool broken = false;
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) broken |= acc[d][i] != acc[d][i];
+  // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
+  uint64_t again = __ballot(broken && row < rows);
+  again = (again | (again >> 16) | (again >> 32) | (again >> 48)) & 0xFFFFu;
+  if (row < rows && ((again >> col) & 1) == 0) {
+    float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
+    const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits + split;
+    const float inv = inv_sum(l);
+    uint16_t* o = a.out + (s.first + t) * a.o_token + hq * a.o_head;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+      const int e = 16 * d + 4 * g;
+      if (PAD && e >= a.head_dim) continue;
+      if (a.part != nullptr) {
+        *reinterpret_cast<float4_t*>(a.part + at * a.head_dim + e) = acc[d];
+      } else {
+        *reinterpret_cast<uint2*>(o + e) =
+            make_uint2(T::pack2(acc[d][0] * inv, acc[d][1] * inv), T::pack2(acc[d][2] * inv, acc[d][3] * inv));
+      }
+    }
+    if (a.part != nullptr && g == 0) *reinterpret_cast<float2_t*>(ml + 2 * at) = float2_t{m, l};
+  }
+  while (again != 0) {
+    const int i = __builtin_ctzll(again);
+    again &= again - 1;
+    const int r = (rb * kWaves + wave) * 16 + i, tr = r / a.group, hr = kv_head * a.group + r % a.group;
+    const uint64_t bits = a.mask != nullptr ? a.mask[s.first + tr] : (2ull << tr) - 1;
+    float top, sum;
+    float2_t o;
+    attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1,
+                  [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
+                    const int64_t at = offset_of(static_cast<int>(j));
+                    kr = kbase + at;
+                    vr = vbase + at;
+                    const int64_t back = j - s.ctx;
+                    return back < 0 || ((bits >> (back & 63)) & 1) != 0;
+                  },
+                  top, sum, o);
+    store_row<T>(a, s.first + tr, hr, split, top, sum, o);
   }
 }
 
 // Adds the splits of a row in their order: one wavefront per token and head, lane i has
 // d = 2 i, 2 i + 1.
+constexpr int kMergeLoads = 8;
+
 template <typename T>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -361,11 +637,24 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
   top = wave_max(top);
   float sum = 0.0f;
   float2_t o = {0.0f, 0.0f};
-  for (int w = 0; w < n; ++w) {
-    const float f = scale_of(ml[2 * w], ml[2 * w + 1], top);
-    sum += ml[2 * w + 1] * f;
-    if (2 * lane < a.head_dim)
-      o += *reinterpret_cast<const float2_t*>(a.part + (at + w) * a.head_dim + 2 * lane) * f;
+  const float* part = a.part + at * a.head_dim + min(2 * lane, a.head_dim - 2);
+  for (int w0 = 0; w0 < n; w0 += 64) {  // 64 splits' factors, one per lane
+    const int w = w0 + lane;
+    const float l = w < n ? ml[2 * w + 1] : 0.0f;
+    const float f = w < n ? scale_of(ml[2 * w], l, top) : 0.0f;
+    sum += wave_sum(l * f);
+    const int here = min(64, n - w0);
+    for (int i = 0; i < here; i += kMergeLoads) {  // that many rows in flight
+      float2_t x[kMergeLoads];
+#pragma unroll
+      for (int j = 0; j < kMergeLoads; ++j)
+        x[j] = *reinterpret_cast<const float2_t*>(part + static_cast<int64_t>(min(w0 + i + j, n - 1)) * a.head_dim);
+#pragma unroll
+      for (int j = 0; j < kMergeLoads; ++j) {
+        const float fj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (i + j) & 63));
+        if (i + j < here) o += x[j] * fj;
+      }
+    }
   }
   const float inv = inv_sum(sum);
   if (2 * lane < a.head_dim)
@@ -373,15 +662,29 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
         T::pack2(o.x * inv, o.y * inv);
 }
 
-// Rows per workgroup: 16, 32 or 64, the least that hold a sequence's, 64 at most.
-int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Row tiles per workgroup: one or two of 16 rows, shared by the wavefronts, where they hold
+// all rows of a sequence; else four, one per wavefront.
+int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kWaves; }
 
-// Splits of the longest context the table holds: about 1024 workgroups, each at least 128
-// positions, and at most the page numbers that a workgroup stages.
+// Splits that balance a workgroup's fixed time F (finding its sequence, its pages and the first
+// step, and writing its result: about 4 us) against the time t of 128 positions: with more
+// workgroups than fit at once, the last one ends after about wgs S F / slots +
+// (len / (128 S)) t, least at S = sqrt(len t slots / (128 wgs F)). Fewer than one per slot
+// is never better.
+int64_t splits_for(int64_t len, int64_t wgs, bool by_rows) {
+  const double slots = by_rows ? 512.0 : 256.0, t_over_f = by_rows ? 0.4 : 0.2;
+  const int64_t best = static_cast<int64_t>(sqrt(len / 128.0 * t_over_f * slots / wgs) + 0.5);
+  const int64_t fill = static_cast<int64_t>(slots) / wgs;
+  return best > fill ? best : fill;
+}
+
+// Splits of the longest context the table holds: as above, each at least 128 positions, and at
+// most the page numbers that a workgroup stages.
 int pick_splits(int64_t seqs, int64_t max_len, int32_t page_size, int64_t rows, int32_t kv_heads) {
   const int64_t row_blocks = (rows + 16 * row_tiles(rows) - 1) / (16 * row_tiles(rows));
   const int64_t wgs = seqs * kv_heads * row_blocks;
-  int64_t s = (1024 + wgs - 1) / wgs;
+  int64_t s = splits_for(max_len, wgs, row_tiles(rows) == kWaves);
+  if (const char* env = tuning_env("AWQ_TREE_SPLITS")) s = atoi(env);
   const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
   s = s < most ? s : most;
   s = s < kMaxSplits ? s : kMaxSplits;
@@ -392,32 +695,40 @@ int pick_splits(int64_t seqs, int64_t max_len, int32_t page_size, int64_t rows, 
   return s < 1 ? 1 : static_cast<int>(s);
 }
 
-template <typename T, int DP, int NT, bool PAD>
-hipError_t launch_nt(const TreeArgs& a, hipStream_t st) {
-  static std::atomic<uint64_t> lds_done{0};
-  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(&attn_tree_kernel<T, DP, NT, PAD>),
-                                        Lds<DP, NT>::kTotal, lds_done);
+template <typename Kernel>
+hipError_t launch_kernel(Kernel kernel, std::atomic<uint64_t>& lds_done, int lds, const TreeArgs& a, hipStream_t st) {
+  const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kernel), lds, lds_done);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((attn_tree_kernel<T, DP, NT, PAD>),
-                     dim3(static_cast<unsigned>(a.row_blocks) * a.splits, a.kv_heads, a.seqs), dim3(256),
-                     (Lds<DP, NT>::kTotal), st, a);
-  const hipError_t e2 = hipGetLastError();
-  if (e2 != hipSuccess || a.part == nullptr) return e2;
-  hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3((a.max_q * a.q_heads + 3) / 4, a.seqs), dim3(256), 0,
-                     st, a);
+  hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(a.row_blocks) * a.splits, a.kv_heads, a.seqs), dim3(256),
+                     lds, st, a);
   return hipGetLastError();
 }
 
-template <typename T, int DP>
-hipError_t launch_dp(const TreeArgs& a, int nt, hipStream_t st) {
-  if (a.head_dim < DP) {
-    if (nt == 1) return launch_nt<T, DP, 1, true>(a, st);
-    if (nt == 2) return launch_nt<T, DP, 2, true>(a, st);
-    return launch_nt<T, DP, 4, true>(a, st);
+template <typename T, int DP, bool PAD>
+hipError_t launch_pad(const TreeArgs& a, int nt, hipStream_t st) {
+  if (nt == 1) {
+    static std::atomic<uint64_t> done{0};
+    return launch_kernel(&attn_tree_kernel<T, DP, 1, PAD>, done, Lds<DP, 1>::kTotal, a, st);
   }
-  if (nt == 1) return launch_nt<T, DP, 1, false>(a, st);
-  if (nt == 2) return launch_nt<T, DP, 2, false>(a, st);
-  return launch_nt<T, DP, 4, false>(a, st);
+  if (nt == 2) {
+    static std::atomic<uint64_t> done{0};
+    return launch_kernel(&attn_tree_kernel<T, DP, 2, PAD>, done, Lds<DP, 2>::kTotal, a, st);
+  }
+  static std::atomic<uint64_t> done{0};
+  return launch_kernel(&attn_tree_rows_kernel<T, DP, PAD>, done, kRing * 2 * kStep * DP * 2 + kTableEntries * 4, a, st);
+}
+
+template <typename T>
+hipError_t launch_t(const TreeArgs& a, int nt, hipStream_t st) {
+  const int d = a.head_dim;
+  const hipError_t e = d == 64    ? launch_pad<T, 64, false>(a, nt, st)
+                       : d < 64   ? launch_pad<T, 64, true>(a, nt, st)
+                       : d == 128 ? launch_pad<T, 128, false>(a, nt, st)
+                                  : launch_pad<T, 128, true>(a, nt, st);
+  if (e != hipSuccess || a.part == nullptr) return e;
+  hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3((a.max_q * a.q_heads + 3) / 4, a.seqs), dim3(256), 0,
+                     st, a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -457,6 +768,9 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   a.table_width = static_cast<int32_t>(g.table_width);
   a.pages = static_cast<int32_t>(g.pages);
   a.page_size = g.page_size;
+  a.page_shift = 31;
+  while ((int64_t{1} << (a.page_shift - 31)) < g.page_size) ++a.page_shift;
+  a.page_mul = static_cast<uint32_t>((uint64_t{1} << a.page_shift) / static_cast<uint32_t>(g.page_size) + 1);
   a.max_q = g.max_q;
   a.q_heads = g.q_heads;
   a.kv_heads = g.kv_heads;
@@ -468,9 +782,7 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   a.row_blocks = static_cast<int32_t>((rows + 16 * nt - 1) / (16 * nt));
   a.splits = attn_tree_splits(g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads);
   a.part = a.splits > 1 ? static_cast<float*>(g.ws) : nullptr;
-  if (g.dtype == AWQ_DT_F16)
-    return g.head_dim <= 64 ? launch_dp<F16, 64>(a, nt, st) : launch_dp<F16, 128>(a, nt, st);
-  return g.head_dim <= 64 ? launch_dp<BF16, 64>(a, nt, st) : launch_dp<BF16, 128>(a, nt, st);
+  return g.dtype == AWQ_DT_F16 ? launch_t<F16>(a, nt, st) : launch_t<BF16>(a, nt, st);
 }
 
 }  // namespace awq

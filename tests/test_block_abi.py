@@ -15,6 +15,8 @@ torch = pytest.importorskip("torch")
 awq = pytest.importorskip("bit_weight_only_w4a16_amd.awq")
 block = pytest.importorskip("bit_weight_only_w4a16_amd.block")
 
+import block_ctypes as c_abi  # noqa: E402
+
 OK, INVALID, UNSUPPORTED, MISALIGNED, WORKSPACE = 0, 1, 2, 3, 4
 P = 1 << 20   # an aligned stand-in address; never dereferenced, because validation fails first
 
@@ -23,21 +25,21 @@ P = 1 << 20   # an aligned stand-in address; never dereferenced, because validat
 def lib():
     if not os.path.exists(awq.LIB_PATH):
         pytest.skip("library not built")
-    return block.lib()
+    return c_abi.lib()
 
 
 def test_every_declared_symbol_is_exported(lib):
     text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
     names = sorted(set(re.findall(r"\b(awq_[a-z0-9_]+)\s*\(", text)))
-    assert names == sorted(block.EXPORTS)
+    assert names == sorted(block.EXPORTS) == sorted(c_abi._SIGNATURES)
     for n in names:
         assert hasattr(lib, n), n
 
 
 def test_structures_match_the_header(tmp_path):
     """Sizes and offsets as a C compiler lays out the header's structures."""
-    pairs = {"awq_rope_args": block.RopeArgs, "awq_attn_prompt_args": block.AttnPromptArgs,
-             "awq_attn_tree_args": block.AttnTreeArgs, "awq_epilogue": block.Epilogue}
+    pairs = {"awq_rope_args": c_abi.RopeArgs, "awq_attn_prompt_args": c_abi.AttnPromptArgs,
+             "awq_attn_tree_args": c_abi.AttnTreeArgs, "awq_epilogue": c_abi.Epilogue}
     lines = []
     for c, py in pairs.items():
         lines.append(f'printf("{c} %zu\\n", sizeof({c}));')
@@ -54,15 +56,6 @@ def test_structures_match_the_header(tmp_path):
         assert int(got[c]) == ctypes.sizeof(py)
         for f in py._fields_:
             assert int(got[f"{c}.{f[0]}"]) == getattr(py, f[0]).offset, f"{c}.{f[0]}"
-
-
-def test_packed_arguments_have_the_structures_layout():
-    for packed, py in ((block._ROPE, block.RopeArgs), (block._PROMPT, block.AttnPromptArgs),
-                       (block._TREE, block.AttnTreeArgs), (block._EPILOGUE, block.Epilogue)):
-        assert packed.size == ctypes.sizeof(py)
-        values = list(range(1, len(py._fields_) + 1))
-        got = py.from_buffer_copy(packed.pack(*values))
-        assert [int(getattr(got, f[0])) for f in py._fields_] == values
 
 
 def call(fn, args):
@@ -90,7 +83,7 @@ ROPE = dict(q=P, q_out=P, k=P, k_out=None, v=P, k_cache=P, v_cache=P, positions=
     (dict(positions=P + 2), MISALIGNED), (dict(slots=P + 4), MISALIGNED),
 ])
 def test_rope_refusals(lib, change, code):
-    assert call(lib.awq_rope, block.RopeArgs(**{**ROPE, **change})) == code
+    assert call(lib.awq_rope, c_abi.RopeArgs(**{**ROPE, **change})) == code
 
 
 PROMPT = dict(q=P, k=P, v=P, out=P, cu=P, tokens=100, seqs=2, q_token=512, q_head=128, k_token=256, k_head=128,
@@ -108,7 +101,7 @@ PROMPT = dict(q=P, k=P, v=P, out=P, cu=P, tokens=100, seqs=2, q_token=512, q_hea
     (dict(out=P + 4), MISALIGNED), (dict(cu=P + 2), MISALIGNED), (dict(k_head=132), MISALIGNED),
 ])
 def test_prompt_refusals(lib, change, code):
-    assert call(lib.awq_attn_prompt, block.AttnPromptArgs(**{**PROMPT, **change})) == code
+    assert call(lib.awq_attn_prompt, c_abi.AttnPromptArgs(**{**PROMPT, **change})) == code
 
 
 TREE = dict(q=P, k_cache=P, v_cache=P, out=P, block_table=P, ctx_lens=P, cu_q=P, mask=P, ws=P, ws_bytes=1 << 40,
@@ -130,7 +123,7 @@ TREE = dict(q=P, k_cache=P, v_cache=P, out=P, block_table=P, ctx_lens=P, cu_q=P,
     (dict(cache_head=2044), MISALIGNED), (dict(ctx_lens=P + 1), MISALIGNED),
 ])
 def test_tree_refusals(lib, change, code):
-    assert call(lib.awq_attn_tree, block.AttnTreeArgs(**{**TREE, **change})) == code
+    assert call(lib.awq_attn_tree, c_abi.AttnTreeArgs(**{**TREE, **change})) == code
 
 
 def test_tree_workspace_sizes(lib):
@@ -152,7 +145,7 @@ def test_tree_workspace_sizes(lib):
 def test_fused_refusals(lib, change, code):
     d = dict(m=0, n=128, k=256, group=128, x=P, act=0, reserved=0, bias=None, mul=None, residual=None, epi=True)
     d.update(change)
-    e = block.Epilogue(d["bias"], d["mul"], d["residual"], d["act"], d["reserved"])
+    e = c_abi.Epilogue(d["bias"], d["mul"], d["residual"], d["act"], d["reserved"])
     rc = lib.awq_gemm_fused(d["x"], None, P, d["m"], d["n"], d["k"], d["group"], 0,
                             ctypes.byref(e) if d["epi"] else None, P, None, 0, None)
     assert rc == code
@@ -173,6 +166,10 @@ def test_binding_refuses_host_tensors():
         block.awq_gemm_fused(x[0], None, x[0], 128, 64, act="tanh")
     with pytest.raises(ValueError):
         block.awq_gemm_fused(x[0], None, x[0], 128, 128)
+    with pytest.raises(TypeError):
+        block.awq_attn_prompt([1.0], x, x, cu)
+    with pytest.raises(TypeError):
+        block.awq_rope(x, None, None)
 
 
 def test_rope_frequencies():

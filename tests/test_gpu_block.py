@@ -503,3 +503,104 @@ def test_another_stream_and_a_graph():
             assert torch.equal(a, b), i
         for a, b in zip(eager, step()):
             assert torch.equal(a, b), i
+
+
+# ---------------------------------------------------------------------------- refusals
+
+def test_binding_refusals():
+    """Types, shapes, layouts and devices that do not fit are errors, and nothing runs."""
+    q = torch.zeros(4, 4, 64, dtype=F16, device=DEV)
+    k = torch.zeros(4, 2, 64, dtype=F16, device=DEV)
+    cu, pos = i32([0, 4]), i32([0, 1, 2, 3])
+    freq = torch.ones(32, device=DEV)
+    kc = torch.zeros(3, 2, 16, 64, dtype=F16, device=DEV)
+    slots = torch.arange(4, device=DEV)
+    prompt = block.awq_attn_prompt
+    rope = block.awq_rope
+    tree = block.awq_attn_tree
+    good = (q, kc, kc.clone(), i32([[0, 1]]), i32([3]), i32([0, 4]), 4)
+    tree(*good)
+
+    def change(i, t):
+        return good[:i] + (t,) + good[i + 1:]
+
+    for error, fn in [
+        (TypeError, lambda: prompt(q.float(), k, k, cu)),
+        (TypeError, lambda: prompt(q, k.bfloat16(), k, cu)),
+        (TypeError, lambda: prompt(q, k, k, cu.long())),
+        (TypeError, lambda: prompt(q, k, k, None)),
+        (ValueError, lambda: prompt(q, k[:3], k, cu)),
+        (ValueError, lambda: prompt(q, k, k[:, :1], cu)),
+        (ValueError, lambda: prompt(q[0], k, k, cu)),
+        (ValueError, lambda: prompt(q, k.transpose(1, 2), k, cu)),
+        (ValueError, lambda: prompt(q, k, k, cu[:0])),
+        (ValueError, lambda: prompt(q, k, k, cu.cpu())),
+        (ValueError, lambda: prompt(q, k, k, cu, out=q[:3])),
+        (TypeError, lambda: prompt(q, k, k, cu, out=q.float())),
+        (TypeError, lambda: prompt(q, k, k, cu, scale="x")),
+        (awq.AwqError, lambda: prompt(q, k, k, cu, scale=0.0)),
+        (awq.AwqError, lambda: prompt(q[:, :3], k, k, cu)),
+        (ValueError, lambda: rope(None, pos, freq)),
+        (ValueError, lambda: rope(q, pos[:3], freq)),
+        (TypeError, lambda: rope(q, pos.long(), freq)),
+        (TypeError, lambda: rope(q, pos, freq.double())),
+        (ValueError, lambda: rope(q, pos, torch.ones(33, device=DEV))),
+        (ValueError, lambda: rope(q, pos, freq, k=k[:2])),
+        (ValueError, lambda: rope(q, pos, freq, k_out=k)),
+        (ValueError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc, slots=slots)),
+        (ValueError, lambda: rope(q, pos, freq, k=k, k_cache=kc, v_cache=kc, slots=slots)),
+        (ValueError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc, v_cache=kc)),
+        (TypeError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc, v_cache=kc, slots=slots.int())),
+        (ValueError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc, v_cache=kc[:2], slots=slots)),
+        (ValueError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc[:, :1], v_cache=kc[:, :1], slots=slots)),
+        (TypeError, lambda: rope(q, pos, freq, k=k, v=k, k_cache=kc.float(), v_cache=kc.float(), slots=slots)),
+        (TypeError, lambda: tree(*change(0, q.float()))),
+        (ValueError, lambda: tree(*change(1, kc[0]))),
+        (ValueError, lambda: tree(*change(2, kc.transpose(0, 1)))),
+        (ValueError, lambda: tree(*change(3, i32([0, 1])))),
+        (ValueError, lambda: tree(*change(4, i32([3, 3])))),
+        (ValueError, lambda: tree(*change(5, i32([0, 4, 4])))),
+        (TypeError, lambda: tree(*change(6, None))),
+        (awq.AwqError, lambda: tree(*change(6, 65))),
+        (awq.AwqError, lambda: tree(*change(6, 0))),
+        (ValueError, lambda: tree(*good, mask=torch.zeros(3, dtype=torch.int64, device=DEV))),
+        (TypeError, lambda: tree(*good, mask=pos)),
+        (TypeError, lambda: tree(*good, ws=pos)),
+        (awq.AwqError, lambda: tree(q, kc, kc, torch.zeros(1, 500, dtype=torch.int32, device=DEV), *good[4:],
+                                    ws=torch.zeros(16, dtype=torch.uint8, device=DEV))),
+    ]:
+        with pytest.raises(error):
+            fn()
+    n, kk = 128, 256
+    packed, inv, _ = layer(n, kk, 128, 0, seed=1)
+    x = torch.zeros(3, kk, dtype=F16, device=DEV)
+    y = torch.zeros(3, n, dtype=F16, device=DEV)
+    fused = block.awq_gemm_fused
+    fused(x, inv, packed, n, kk, bias=y[0], mul=y, residual=y)
+    for error, fn in [
+        (ValueError, lambda: fused(x, inv, packed[:100], n, kk)),
+        (TypeError, lambda: fused(x.float(), inv, packed, n, kk)),
+        (ValueError, lambda: fused(x[:, :128], inv, packed, n, kk)),
+        (ValueError, lambda: fused(x, inv[:128], packed, n, kk)),
+        (ValueError, lambda: fused(x, inv, packed, n, kk, bias=y)),
+        (ValueError, lambda: fused(x, inv, packed, n, kk, mul=y[:2])),
+        (TypeError, lambda: fused(x, inv, packed, n, kk, residual=y.float())),
+        (ValueError, lambda: fused(x, inv, packed, n, kk, y=y.t())),
+        (ValueError, lambda: fused(x, inv, packed, n, kk, act="tanh")),
+        (awq.AwqError, lambda: fused(x[:, :200].contiguous(), None, packed, n, 200)),
+    ]:
+        with pytest.raises(error):
+            fn()
+    torch.cuda.synchronize()
+
+
+def test_calls_of_nothing():
+    q = torch.zeros(0, 4, 64, dtype=F16, device=DEV)
+    cu = i32([0])
+    assert block.awq_attn_prompt(q, q[:, :2], q[:, :2], cu).shape == (0, 4, 64)
+    assert block.awq_rope(q, i32([]), torch.ones(32, device=DEV))[0].shape == (0, 4, 64)
+    kc = torch.zeros(1, 2, 16, 64, dtype=F16, device=DEV)
+    assert block.awq_attn_tree(q, kc, kc, torch.zeros(1, 1, dtype=torch.int32, device=DEV), i32([0]), i32([0, 0]),
+                               1).shape == (0, 4, 64)
+    packed, inv, _ = layer(128, 128, 128, 0, seed=1)
+    assert block.awq_gemm_fused(torch.zeros(0, 128, dtype=F16, device=DEV), inv, packed, 128, 128).shape == (0, 128)
