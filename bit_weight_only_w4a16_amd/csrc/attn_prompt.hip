@@ -115,19 +115,15 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   }
   auto load_tile = [&](int kv0, int buf) {
     const int rows = min(kBK, len - kv0);
-    const __amdgpu_buffer_rsrc_t rk =
-        make_rsrc(kbase + kv0 * a.k_token, static_cast<uint32_t>((rows - 1) * a.k_token + a.head_dim) * 2);
-    const __amdgpu_buffer_rsrc_t rv =
-        make_rsrc(vbase + kv0 * a.v_token, static_cast<uint32_t>((rows - 1) * a.v_token + a.head_dim) * 2);
+    const u32x4 rk =
+        rsrc_words(kbase + kv0 * a.k_token, static_cast<uint32_t>((rows - 1) * a.k_token + a.head_dim) * 2);
+    const u32x4 rv =
+        rsrc_words(vbase + kv0 * a.v_token, static_cast<uint32_t>((rows - 1) * a.v_token + a.head_dim) * 2);
     unsigned char* dst = smem + buf * 2 * TILE + LOADS * wave * 1024;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void*)(dst + j * 1024), 16,
-                                               static_cast<int>(k_off[j]), 0, 0, 0);
+    for (int j = 0; j < LOADS; ++j) load_to_lds(rk, k_off[j], dst + j * 1024);
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void*)(dst + TILE + j * 1024), 16,
-                                               static_cast<int>(v_off[j]), 0, 0, 0);
+    for (int j = 0; j < LOADS; ++j) load_to_lds(rv, v_off[j], dst + TILE + j * 1024);
   };
 
   const int kv_end = min(len, q0 + kBQ);  // keys this workgroup needs
@@ -167,8 +163,8 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
 
   int buf = 0;
   for (int kv0 = 0; kv0 < kv_end; kv0 += kBK, buf ^= 1) {
-    __builtin_amdgcn_s_waitcnt(0);  // this wavefront's loads of the tile have landed
-    __syncthreads();                // everyone's have, and the other buffer is free
+    wait_loads<0>();  // this wavefront's loads of the tile have landed
+    lds_barrier();    // everyone's have, and the other buffer is free
     if (kv0 + kBK < kv_end) load_tile(kv0 + kBK, buf ^ 1);
     if (kv0 > wq0 + 31) continue;   // above the diagonal for this wavefront
     const unsigned char* ks = smem + buf * 2 * TILE;

@@ -11,7 +11,8 @@
 // unnormalised row) in the workspace, and a second launch adds the splits in their order.
 //
 // A step's keys and values go from memory straight into LDS (16 bytes per lane, no
-// registers), kStages steps ahead. Both products are formed transposed, S^T = K Q^T and
+// registers), one step ahead (every load instruction of a step counts in wait_loads: each
+// row's lanes cover all its chunks, so with D < DP some lane takes part in each). Both products are formed transposed, S^T = K Q^T and
 // O^T = V^T P^T (16 x 16 x 32 matrix instruction): lane l holds the scores of one query
 // (column l % 16), the positions it holds after S^T are the contraction slots it feeds to
 // O^T, and V^T is read from LDS in that order with the transposing 16-bit read.
@@ -20,13 +21,15 @@
 #include <math.h>
 #include <stdlib.h>
 
+#include <type_traits>
+
 namespace awq {
 namespace {
 
 constexpr int kStep = 32;        // positions per wavefront and step
 constexpr int kWaves = 4;
 constexpr int kStages = 2;
-constexpr int kMinChunk = kStep * kWaves;  // positions per split: a multiple of this
+constexpr int kMinChunk = kStep * kWaves;  // positions per split: at least this many
 constexpr int kTableEntries = 1024;        // page numbers of a split staged in LDS
 constexpr int kMaxSplits = 64;
 // P carries a factor 2^kShift: with the maximum in use at most kSlack below the true one,
@@ -67,10 +70,11 @@ __device__ __forceinline__ Seq sequence(const TreeArgs& a, int b) {
   s.len = static_cast<int>(len < a.max_len ? len : a.max_len);
   return s;
 }
-// Positions per split of a sequence: the same for every workgroup of it
+// Positions per split of a sequence: the same for every workgroup of it, a multiple of what a
+// step of the kernels takes
 __device__ __forceinline__ int chunk_of(int len, int splits) {
   const int per = (len + splits - 1) / splits;
-  return max((per + kMinChunk - 1) / kMinChunk, 1) * kMinChunk;
+  return max((per + 63) / 64 * 64, kMinChunk);
 }
 
 // Which of a step's 32 positions a row sees, as bits: `back` is the step's first position less
@@ -79,27 +83,6 @@ __device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
   const int k = min(max(-back, 0), 31);  // positions of the step that are context (< 32 here)
   const uint32_t bits = (static_cast<uint32_t>(mask >> (max(back, 0) & 63)) << k) | ((1u << k) - 1u);
   return left < 32 ? bits & ((1u << left) - 1u) : bits;
-}
-
-// Waits until at most N of this wavefront's memory loads are on their way (they land in
-// order). Every load instruction of a step counts: each row's lanes cover all its chunks, so
-// with D < DP some lane takes part in each.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  // vmcnt in bits 0..3 and 14..15, the other counters at their largest: not waited for
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
-  asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void wait_lds() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only
-  asm volatile("" ::: "memory");
-}
-// A barrier for LDS alone: loads into LDS that are on their way stay so.
-__device__ __forceinline__ void lds_barrier() {
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
 }
 
 // The factor that brings a partial result with maximum m and sum l to the maximum top. A
@@ -233,14 +216,8 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     for (int j = 0; j < LOADS; ++j) {
       const int r = ROWS * j + lane / RC;
       const int ck = 8 * k_pos<DP>(r, lane % RC), cv = 8 * v_pos<DP>(r, lane % RC);
-      if (!PAD || ck < a.head_dim)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(kbase + at[j] + ck),
-            (lds_void*)(dst + j * 1024), 16, 0, 0);
-      if (!PAD || cv < a.head_dim)
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)(vbase + at[j] + cv),
-            (lds_void*)(dst + TILE + j * 1024), 16, 0, 0);
+      if (!PAD || ck < a.head_dim) load_to_lds(kbase + at[j] + ck, dst + j * 1024);
+      if (!PAD || cv < a.head_dim) load_to_lds(vbase + at[j] + cv, dst + TILE + j * 1024);
     }
   };
 
@@ -264,8 +241,9 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     load_step(at, 0);
     if (first + kStride < p1) find_step(first + kStride, at);
   }
-  int stage = 0;
-  for (int s0 = first; s0 < p1; s0 += kStride, stage ^= 1) {
+  // (the stage is a compile-time value: the LDS addresses then differ by constants)
+  auto step = [&](auto stage_, int s0) {
+    constexpr int stage = decltype(stage_)::value;
     if (s0 + kStride < p1) {
       wait_lds();  // the last step's reads of this stage are done
       load_step(at, stage ^ 1);
@@ -340,6 +318,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
       for (int n = 0; n < NT; ++n) acc[n][d] = T::mfma16(vf, __builtin_bit_cast(v8, p[n]), acc[n][d]);
     }
     asm volatile("" ::: "memory");
+  };
+  for (int s0 = first; s0 < p1; s0 += 2 * kStride) {
+    step(std::integral_constant<int, 0>{}, s0);
+    if (s0 + kStride < p1) step(std::integral_constant<int, 1>{}, s0 + kStride);
   }
 
   // merge the four wavefronts: maxima, then the rows brought to the common maximum
@@ -400,35 +382,34 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   }
 }
 
-// The same for many query rows (more than 32 of a key / value head): here the wavefronts split
-// the rows, 16 each, and share the keys and values, 32 positions at a time, in a ring of
-// four steps, three of them on their way while one is used. A wavefront keeps its Q
-// operands in registers, needs no merge at the end, and the workgroup needs half the LDS,
-// so two of them share a CU.
-#ifndef KRING
-#define KRING 4
-#endif
-constexpr int kRing = KRING;
+// The same for many query rows (more than 32 of a key / value head): 64 rows per workgroup,
+// 64 positions per step, in LDS for all four wavefronts; each takes 32 of the rows and 32 of
+// the positions, so that a fragment of K or V read from LDS serves two row tiles. The
+// wavefronts keep their Q operands in registers and the two halves of the positions meet at
+// the end; 64 KiB of LDS let two workgroups share a CU.
+constexpr int kRowStep = 64;
+constexpr int kRowTiles = 2;  // of 16 rows, per wavefront
 
 template <typename T, int DP, bool PAD>
-__global__ void __launch_bounds__(256, KRING == 2 ? 4 : KRING == 3 ? 3 : 2) attn_tree_rows_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
   typedef typename T::v8 v8;
-  constexpr int RB = DP * 2, RC = DP / 8, TILE = kStep * RB;
+  constexpr int RB = DP * 2, RC = DP / 8, TILE = kRowStep * RB;
   constexpr int ROWS = 1024 / RB;               // positions one load instruction fills
-  constexpr int OWN = kStep / kWaves;           // positions a wavefront loads
-  constexpr int LOADS = OWN / ROWS;             // its load instructions per step, for K and for V
-  constexpr int NC = DP / 32, ND = DP / 16;
-  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [kRing][K tile, V tile], pages
-  int* pages = reinterpret_cast<int*>(smem + kRing * 2 * TILE);
+  constexpr int OWN = kRowStep / kWaves;        // positions a wavefront loads
+  constexpr int LOADS = OWN / ROWS;
+  constexpr int NC = DP / 32, ND = DP / 16, NT = kRowTiles;
+  extern __shared__ __attribute__((aligned(1024))) unsigned char smem[];  // [2][K tile, V tile], pages
+  int* pages = reinterpret_cast<int*>(smem + 4 * TILE);
 
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 1;  // of a step's positions
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, g = lane >> 4;
   const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
   const int kv_head = blockIdx.y, b = blockIdx.z;
   const Seq s = sequence(a, b);
   const int rows = s.count * a.group;
-  if (rb * 16 * kWaves >= rows) return;
+  if (rb * 64 >= rows) return;
   const int chunk = chunk_of(s.len, a.splits);
   const int p0 = split * chunk, p1 = min(s.len, p0 + chunk);
   if (p0 >= p1 && a.part != nullptr) return;  // the second launch knows that it is empty
@@ -438,23 +419,30 @@ __global__ void __launch_bounds__(256, KRING == 2 ? 4 : KRING == 3 ? 3 : 2) attn
   for (int i = threadIdx.x; i < n_pages; i += 256)
     pages[i] = min(max(a.table[static_cast<int64_t>(b) * a.table_width + t0 + i], 0), a.pages - 1);
   if constexpr (PAD) {  // chunks past D are never loaded: they stay 0
-    for (int i = threadIdx.x; i < kRing * 2 * TILE / 16; i += 256)
+    for (int i = threadIdx.x; i < 4 * TILE / 16; i += 256)
       *reinterpret_cast<u32x4*>(smem + 16 * i) = u32x4{0, 0, 0, 0};
   }
-  // this lane's row, its mask and its Q operands (rows past the last repeat it)
-  const int row = (rb * kWaves + wave) * 16 + col;
-  const int t = min(row, rows - 1) / a.group, hq = kv_head * a.group + min(row, rows - 1) % a.group;
-  const uint64_t sees = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
-  const uint16_t* q = a.q + (s.first + t) * a.q_token + hq * a.q_head;
-  v8 qf[NC];
+  // this lane's rows, their masks and their Q operands (rows past the last repeat it)
+  const int row0 = rb * 64 + 32 * (wave & 1) + col;
+  int token[NT], head[NT];
+  uint64_t sees[NT];
+  v8 qf[NT][NC];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
-    const int d = 32 * c + 8 * g;
-    u32x4 x = {0, 0, 0, 0};
-    if (!PAD || d < a.head_dim) x = *reinterpret_cast<const u32x4*>(q + d);
-    qf[c] = __builtin_bit_cast(v8, x);
+  for (int n = 0; n < NT; ++n) {
+    const int r = min(row0 + 16 * n, rows - 1);
+    const int t = r / a.group;
+    token[n] = s.first + t;
+    head[n] = kv_head * a.group + r - t * a.group;
+    sees[n] = a.mask != nullptr ? a.mask[token[n]] : (2ull << t) - 1;
+    const uint16_t* q = a.q + token[n] * a.q_token + head[n] * a.q_head;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int d = 32 * c + 8 * g;
+      u32x4 x = {0, 0, 0, 0};
+      if (!PAD || d < a.head_dim) x = *reinterpret_cast<const u32x4*>(q + d);
+      qf[n][c] = __builtin_bit_cast(v8, x);
+    }
   }
-  wait_loads<0>();  // Q and the mask: or the compiler waits for all loads at their use in the loop
   __syncthreads();
 
   const uint16_t* kbase = a.k + kv_head * a.cache_head;
@@ -471,40 +459,33 @@ __global__ void __launch_bounds__(256, KRING == 2 ? 4 : KRING == 3 ? 3 : 2) attn
     unsigned char* dst = smem + stage * 2 * TILE + OWN * wave * RB;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int r = OWN * wave + ROWS * j + lane / RC;
+      const int r = ROWS * j + lane / RC;  // (of this wavefront's 16, a multiple of the patterns' period)
       const int ck = 8 * k_pos<DP>(r, lane % RC), cv = 8 * v_pos<DP>(r, lane % RC);
-      if (!PAD || ck < a.head_dim)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(kbase + at[j] + ck),
-                                         (lds_void*)(dst + j * 1024), 16, 0, 0);
-      if (!PAD || cv < a.head_dim)
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(vbase + at[j] + cv),
-                                         (lds_void*)(dst + TILE + j * 1024), 16, 0, 0);
+      if (!PAD || ck < a.head_dim) load_to_lds(kbase + at[j] + ck, dst + j * 1024);
+      if (!PAD || cv < a.head_dim) load_to_lds(vbase + at[j] + cv, dst + TILE + j * 1024);
     }
   };
 
-  float4_t acc[ND];
+  float4_t acc[NT][ND];
+  float m[NT], l[NT];
 #pragma unroll
-  for (int d = 0; d < ND; ++d) acc[d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  float m = kNegInf, l = 0.0f;
-  const int steps = (p1 - p0 + kStep - 1) / kStep;  // <= 0: nothing
+  for (int n = 0; n < NT; ++n) {
+    m[n] = kNegInf;
+    l[n] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  }
   int64_t at[LOADS];
-#pragma unroll
-  for (int i = 0; i < kRing - 1; ++i)
-    if (i < steps) {
-      find_step(p0 + i * kStep, at);
-      load_step(at, i);
-    }
-  if (kRing - 1 < steps) find_step(p0 + (kRing - 1) * kStep, at);
-  for (int i = 0; i < steps; ++i) {
-    const int s0 = p0 + i * kStep, stage = i % kRing;
-    unsigned char* ks = smem + stage * 2 * TILE;
-    unsigned char* vs = ks + TILE;
-    // this wavefront's loads of the step have landed (those after it may be on their way)
-    if (i + kRing - 2 < steps) {
-      wait_loads<2 * LOADS * (kRing - 2)>();
-    } else {
-      wait_loads<0>();
-    }
+  if (p0 < p1) {
+    find_step(p0, at);
+    load_step(at, 0);
+    if (p0 + kRowStep < p1) find_step(p0 + kRowStep, at);
+  }
+  auto step = [&](auto stage_, int s0) {
+    constexpr int stage = decltype(stage_)::value;
+    const unsigned char* ks = smem + stage * 2 * TILE + 32 * half * RB;
+    unsigned char* vs = smem + stage * 2 * TILE + TILE;
+    wait_loads<0>();  // this wavefront's loads of the step have landed
     // V rows past the split: 0, each wavefront among those it loaded
     const int own = s0 + OWN * wave;
     if (own + OWN > p1) {
@@ -512,107 +493,163 @@ __global__ void __launch_bounds__(256, KRING == 2 ? 4 : KRING == 3 ? 3 : 2) attn
       for (int j = lane; j < (OWN - from) * RC; j += 64)
         *reinterpret_cast<u32x4*>(vs + (OWN * wave + from) * RB + 16 * j) = u32x4{0, 0, 0, 0};
     }
-    lds_barrier();  // the step is whole, and the step before it is done with
-    if (i + kRing - 1 < steps) load_step(at, (i + kRing - 1) % kRing);
-    if (i + kRing < steps) find_step(s0 + kRing * kStep, at);
+    lds_barrier();  // the step is whole, and the other stage is done with
+    if (s0 + kRowStep < p1) load_step(at, stage ^ 1);
+    if (s0 + 2 * kRowStep < p1) find_step(s0 + 2 * kRowStep, at);
+    const int mine = s0 + 32 * half;  // this wavefront's positions
+    if (mine >= p1) return;
+    vs += 32 * half * RB;
 
-    float4_t sc[2];
+    float4_t sc[NT][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      sc[j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) sc[n][j] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
         const int r = 16 * j + col;
         const v8 kf = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
-        sc[j] = T::mfma16(kf, qf[c], sc[j]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][j] = T::mfma16(kf, qf[n][c], sc[n][j]);
       }
     }
-    if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
-      const uint32_t bits = visible(sees, s0 - s.ctx, p1 - s0) >> (4 * g);
+    if (mine + 32 > s.ctx) {  // new tokens (or the end) among them: one bit per position
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t bits = visible(sees[n], mine - s.ctx, p1 - mine) >> (4 * g);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[n][j][e] = (bits & (1u << (16 * j + e))) != 0 ? sc[n][j][e] : kNegInf;
+      }
+    }
+    float top[NT];
+    bool grown = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      top[n] = fmaxf(fmaxf(fmaxf(sc[n][0][0], sc[n][0][1]), fmaxf(sc[n][0][2], sc[n][0][3])),
+                     fmaxf(fmaxf(sc[n][1][0], sc[n][1][1]), fmaxf(sc[n][1][2], sc[n][1][3]))) * a.c;
+      grown |= top[n] > m[n] + kSlack;
+    }
+    if (__ballot(grown) != 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 16));
+        top[n] = fmaxf(top[n], __shfl_xor(top[n], 32));
+        const float m_new = fmaxf(m[n], top[n]);
+        const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - m_new);
+        m[n] = m_new;
+        l[n] *= keep;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[n][d] *= keep;
+      }
+    }
+    u32x4 p[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float off = m[n] == kNegInf ? 0.0f : kShift - m[n];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[j][e] = (bits & (1u << (16 * j + e))) != 0 ? sc[j][e] : kNegInf;
+        for (int e = 0; e < 4; e += 2) {
+          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e], a.c, off));
+          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e + 1], a.c, off));
+          l[n] += e0 + e1;
+          p[n][2 * j + (e >> 1)] = T::pack2(e0, e1);
+        }
     }
-    float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                      fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * a.c;
-    if (__ballot(top > m + kSlack) != 0) {
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float m_new = fmaxf(m, top);
-      const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      l *= keep;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) acc[d] *= keep;
-    }
-    const float off = m == kNegInf ? 0.0f : kShift - m;
-    u32x4 p;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][e], a.c, off));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[j][e + 1], a.c, off));
-        l += e0 + e1;
-        p[2 * j + (e >> 1)] = T::pack2(e0, e1);
-      }
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
       const int ra = 4 * g + (col >> 2), rb2 = ra + 16;
       const int ch = 2 * d + ((col & 3) >> 1), byte = 8 * (col & 1);
       const short4_t lo = lds_read_tr(vs + ra * RB + 16 * v_pos<DP>(ra, ch) + byte);
       const short4_t hi = lds_read_tr(vs + rb2 * RB + 16 * v_pos<DP>(rb2, ch) + byte);
-      acc[d] = T::mfma16(join8<v8>(lo, hi), __builtin_bit_cast(v8, p), acc[d]);
+      const v8 vf = join8<v8>(lo, hi);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) acc[n][d] = T::mfma16(vf, __builtin_bit_cast(v8, p[n]), acc[n][d]);
     }
-    asm volatile("" ::: "memory");
+  };
+  for (int s0 = p0; s0 < p1; s0 += 2 * kRowStep) {
+    step(std::integral_constant<int, 0>{}, s0);
+    if (s0 + kRowStep < p1) step(std::integral_constant<int, 1>{}, s0 + kRowStep);
   }
 
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
-  bool broken = false;
+  // the second half's results through LDS to the first (lane by lane, the same rows)
 #pragma unroll
-  for (int d = 0; d < ND; ++d)
+  for (int n = 0; n < NT; ++n) {
+    l[n] += __shfl_xor(l[n], 16);
+    l[n] += __shfl_xor(l[n], 32);
+  }
+  lds_barrier();  // the stages are done with
+  float4_t* sums = reinterpret_cast<float4_t*>(smem) + (wave & 1) * NT * ND * 64 + lane;
+  float2_t* stats = reinterpret_cast<float2_t*>(smem + 2 * NT * ND * 64 * 16) + (wave & 1) * NT * 64 + lane;
+  if (half == 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) broken |= acc[d][i] != acc[d][i];
-  // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
-  uint64_t again = __ballot(broken && row < rows);
-  again = (again | (again >> 16) | (again >> 32) | (again >> 48)) & 0xFFFFu;
-  if (row < rows && ((again >> col) & 1) == 0) {
-    float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
-    const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits + split;
-    const float inv = inv_sum(l);
-    uint16_t* o = a.out + (s.first + t) * a.o_token + hq * a.o_head;
+    for (int n = 0; n < NT; ++n) {
+      stats[n * 64] = float2_t{m[n], l[n]};
+#pragma unroll
+      for (int d = 0; d < ND; ++d) sums[(n * ND + d) * 64] = acc[n][d];
+    }
+  }
+  lds_barrier();
+  if (half == 1) return;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const float2_t other = stats[n * 64];
+    const float top = fmaxf(m[n], other.x);
+    const float f0 = scale_of(m[n], l[n], top), f1 = scale_of(other.x, other.y, top);
+    m[n] = top;
+    l[n] = l[n] * f0 + other.y * f1;
+    bool broken = false;
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-      const int e = 16 * d + 4 * g;
-      if (PAD && e >= a.head_dim) continue;
-      if (a.part != nullptr) {
-        *reinterpret_cast<float4_t*>(a.part + at * a.head_dim + e) = acc[d];
-      } else {
-        *reinterpret_cast<uint2*>(o + e) =
-            make_uint2(T::pack2(acc[d][0] * inv, acc[d][1] * inv), T::pack2(acc[d][2] * inv, acc[d][3] * inv));
+      acc[n][d] = acc[n][d] * f0 + sums[(n * ND + d) * 64] * f1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) broken |= acc[n][d][i] != acc[n][d][i];
+    }
+    const bool real = row0 + 16 * n < rows;
+    // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
+    uint64_t again = __ballot(broken && real);
+    again = (again | (again >> 16) | (again >> 32) | (again >> 48)) & 0xFFFFu;
+    if (real && ((again >> col) & 1) == 0) {
+      const int64_t at_row = (static_cast<int64_t>(token[n]) * a.q_heads + head[n]) * a.splits + split;
+      const float inv = inv_sum(l[n]);
+      uint16_t* o = a.out + token[n] * a.o_token + head[n] * a.o_head;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        const int e = 16 * d + 4 * g;
+        if (PAD && e >= a.head_dim) continue;
+        if (a.part != nullptr) {
+          *reinterpret_cast<float4_t*>(a.part + at_row * a.head_dim + e) = acc[n][d];
+        } else {
+          *reinterpret_cast<uint2*>(o + e) = make_uint2(T::pack2(acc[n][d][0] * inv, acc[n][d][1] * inv),
+                                                        T::pack2(acc[n][d][2] * inv, acc[n][d][3] * inv));
+        }
+      }
+      if (a.part != nullptr && g == 0) {
+        float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
+        *reinterpret_cast<float2_t*>(ml + 2 * at_row) = float2_t{m[n], l[n]};
       }
     }
-    if (a.part != nullptr && g == 0) *reinterpret_cast<float2_t*>(ml + 2 * at) = float2_t{m, l};
-  }
-  while (again != 0) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    const int r = (rb * kWaves + wave) * 16 + i, tr = r / a.group, hr = kv_head * a.group + r % a.group;
-    const uint64_t bits = a.mask != nullptr ? a.mask[s.first + tr] : (2ull << tr) - 1;
-    float top, sum;
-    float2_t o;
-    attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1,
-                  [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
-                    const int64_t at = offset_of(static_cast<int>(j));
-                    kr = kbase + at;
-                    vr = vbase + at;
-                    const int64_t back = j - s.ctx;
-                    return back < 0 || ((bits >> (back & 63)) & 1) != 0;
-                  },
-                  top, sum, o);
-    store_row<T>(a, s.first + tr, hr, split, top, sum, o);
+    while (again != 0) {
+      const int i = __builtin_ctzll(again);
+      again &= again - 1;
+      const int r = rb * 64 + 32 * (wave & 1) + 16 * n + i, tr = r / a.group;
+      const int hr = kv_head * a.group + r % a.group;
+      const uint64_t bits = a.mask != nullptr ? a.mask[s.first + tr] : (2ull << tr) - 1;
+      float row_top, sum;
+      float2_t o;
+      attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1,
+                    [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
+                      const int64_t off = offset_of(static_cast<int>(j));
+                      kr = kbase + off;
+                      vr = vbase + off;
+                      const int64_t back = j - s.ctx;
+                      return back < 0 || ((bits >> (back & 63)) & 1) != 0;
+                    },
+                    row_top, sum, o);
+      store_row<T>(a, s.first + tr, hr, split, row_top, sum, o);
+    }
   }
 }
 
@@ -666,33 +703,37 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
 // all rows of a sequence; else four, one per wavefront.
 int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kWaves; }
 
-// Splits that balance a workgroup's fixed time F (finding its sequence, its pages and the first
-// step, and writing its result: about 4 us) against the time t of 128 positions: with more
-// workgroups than fit at once, the last one ends after about wgs S F / slots +
-// (len / (128 S)) t, least at S = sqrt(len t slots / (128 wgs F)). Fewer than one per slot
-// is never better.
-int64_t splits_for(int64_t len, int64_t wgs, bool by_rows) {
-  const double slots = by_rows ? 512.0 : 256.0, t_over_f = by_rows ? 0.4 : 0.2;
-  const int64_t best = static_cast<int64_t>(sqrt(len / 128.0 * t_over_f * slots / wgs) + 0.5);
-  const int64_t fill = static_cast<int64_t>(slots) / wgs;
-  return best > fill ? best : fill;
-}
-
-// Splits of the longest context the table holds: as above, each at least 128 positions, and at
-// most the page numbers that a workgroup stages.
-int pick_splits(int64_t seqs, int64_t max_len, int32_t page_size, int64_t rows, int32_t kv_heads) {
-  const int64_t row_blocks = (rows + 16 * row_tiles(rows) - 1) / (16 * row_tiles(rows));
-  const int64_t wgs = seqs * kv_heads * row_blocks;
-  int64_t s = splits_for(max_len, wgs, row_tiles(rows) == kWaves);
-  if (const char* env = tuning_env("AWQ_TREE_SPLITS")) s = atoi(env);
-  const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
-  s = s < most ? s : most;
-  s = s < kMaxSplits ? s : kMaxSplits;
-  // a split of `chunk` positions touches at most chunk / page_size + 1 pages
+// Splits of the longest context the table holds, by what a call is expected to take (us, from
+// timelines on MI355X): a workgroup's fixed time (finding its sequence, its pages and the
+// first step, and its result), its positions, the longest last workgroup, and with more
+// than one split the second launch and the traffic of the partial results. Lengths are not
+// known here: sequences are taken to be 0.6 of the longest on average. A split touches at
+// most as many pages as a workgroup stages.
+int pick_splits(int64_t tokens, int64_t seqs, int64_t max_len, int32_t page_size, int64_t max_rows, int32_t q_heads,
+                int32_t kv_heads, int32_t head_dim) {
+  const bool by_rows = row_tiles(max_rows) == kWaves;
+  const double slots = by_rows ? 512.0 : 256.0;  // workgroups that run at once
+  const double fixed = 4.0, per = (by_rows ? 1.1 / 64 : 0.9 / 128) * (head_dim <= 64 ? 0.6 : 1.0);
+  // workgroups per split: sequences of few rows need one row block, long ones several
+  const double blocks = by_rows ? static_cast<double>(tokens) * (q_heads / kv_heads) / 64 + 0.5 * seqs : seqs;
+  const double groups = kv_heads * (blocks > seqs ? blocks : seqs);
+  const double merged = static_cast<double>(tokens) * q_heads * head_dim * 8;  // bytes per split, both ways
   const int64_t limit = static_cast<int64_t>(kTableEntries - 1) * page_size / kMinChunk * kMinChunk;
   const int64_t least = (max_len + limit - 1) / limit;
-  s = s > least ? s : least;
-  return s < 1 ? 1 : static_cast<int>(s);
+  const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
+  int64_t best = 1;
+  double best_time = 0.0;
+  for (int64_t s = 1; s <= kMaxSplits && s <= most; ++s) {
+    const double longest = fixed + per * max_len / s, mean = fixed + per * 0.6 * max_len / s;
+    double time = groups * s <= slots ? longest : groups * s * mean / slots + 0.5 * longest;
+    if (s > 1) time += 4.0 + merged * s / 4e6;
+    if (s == 1 || time < best_time) {
+      best = s;
+      best_time = time;
+    }
+  }
+  if (const char* env = tuning_env("AWQ_TREE_SPLITS")) best = atoi(env) < most ? atoi(env) : most;
+  return static_cast<int>(best > least ? best : least);
 }
 
 template <typename Kernel>
@@ -715,7 +756,7 @@ hipError_t launch_pad(const TreeArgs& a, int nt, hipStream_t st) {
     return launch_kernel(&attn_tree_kernel<T, DP, 2, PAD>, done, Lds<DP, 2>::kTotal, a, st);
   }
   static std::atomic<uint64_t> done{0};
-  return launch_kernel(&attn_tree_rows_kernel<T, DP, PAD>, done, kRing * 2 * kStep * DP * 2 + kTableEntries * 4, a, st);
+  return launch_kernel(&attn_tree_rows_kernel<T, DP, PAD>, done, 4 * kRowStep * DP * 2 + kTableEntries * 4, a, st);
 }
 
 template <typename T>
@@ -731,17 +772,17 @@ hipError_t launch_t(const TreeArgs& a, int nt, hipStream_t st) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-int attn_tree_splits(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
-                     int32_t kv_heads) {
-  return pick_splits(seqs, table_width * page_size, page_size,
-                     static_cast<int64_t>(max_q) * (q_heads / kv_heads), kv_heads);
+int attn_tree_splits(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q,
+                     int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
+  return pick_splits(tokens, seqs, table_width * page_size, page_size,
+                     static_cast<int64_t>(max_q) * (q_heads / kv_heads), q_heads, kv_heads, head_dim);
 }
+
+}  // namespace
 
 size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size,
                                  int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
-  const int s = attn_tree_splits(seqs, table_width, page_size, max_q, q_heads, kv_heads);
+  const int s = attn_tree_splits(tokens, seqs, table_width, page_size, max_q, q_heads, kv_heads, head_dim);
   return s > 1 ? static_cast<size_t>(tokens) * q_heads * s * (head_dim + 2) * 4 : 0;
 }
 
@@ -780,7 +821,8 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   const int64_t rows = static_cast<int64_t>(g.max_q) * a.group;
   const int nt = row_tiles(rows);
   a.row_blocks = static_cast<int32_t>((rows + 16 * nt - 1) / (16 * nt));
-  a.splits = attn_tree_splits(g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads);
+  a.splits = attn_tree_splits(g.tokens, g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads,
+                              g.head_dim);
   a.part = a.splits > 1 ? static_cast<float*>(g.ws) : nullptr;
   return g.dtype == AWQ_DT_F16 ? launch_t<F16>(a, nt, st) : launch_t<BF16>(a, nt, st);
 }

@@ -8,8 +8,6 @@ namespace awq {
 
 hipError_t launch_rope(const awq_rope_args& a, hipStream_t st);
 hipError_t launch_attn_prompt(const awq_attn_prompt_args& a, hipStream_t st);
-int attn_tree_splits(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
-                     int32_t kv_heads);
 size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size,
                                  int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
 hipError_t launch_attn_tree(const awq_attn_tree_args& a, hipStream_t st);
@@ -61,7 +59,56 @@ struct BF16 {
   }
 };
 
-typedef __attribute__((address_space(3))) void lds_void;
+// Loads from memory straight into LDS: lane l's 16 bytes go to `dst` + 16 l (dst the same in
+// all lanes). Written as assembly because the compiler, which cannot tell the stages of a
+// ring apart, waits for every such load of its own before each transposing LDS read (the
+// prefetched step would be waited for in the middle of the one before it). The instructions
+// have no register result; the kernels wait with wait_loads, and a wait that the compiler
+// counts for a load of its own only gets longer by these.
+__device__ __forceinline__ uint32_t lds_offset(const unsigned char* p) {
+  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const unsigned char*)(p))));
+}
+__device__ __forceinline__ void load_to_lds(const void* src, unsigned char* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds_offset(dst)), "v"(src)
+               : "m0", "memory");
+}
+// the same from a buffer resource: an offset past its end writes zeros
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, unsigned char* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :
+               : "s"(lds_offset(dst)), "v"(offset), "s"(rsrc)
+               : "m0", "memory");
+}
+// the words of make_rsrc's resource, in scalar registers
+__device__ __forceinline__ u32x4 rsrc_words(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  auto uniform = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
+  return u32x4{uniform(static_cast<uint32_t>(a)), uniform(static_cast<uint32_t>(a >> 32) & 0xFFFFu), uniform(bytes),
+               0x00020000u};
+}
+// Waits until at most N of this wavefront's memory loads are on their way (they land in order).
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  // vmcnt in bits 0..3 and 14..15, the other counters at their largest: not waited for
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+  asm volatile("" ::: "memory");
+}
+// Waits for this wavefront's LDS accesses.
+__device__ __forceinline__ void wait_lds() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only
+  asm volatile("" ::: "memory");
+}
+// A barrier for LDS alone: loads into LDS that are on their way stay so.
+__device__ __forceinline__ void lds_barrier() {
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 typedef __attribute__((address_space(3))) short4_t lds_short4;
 
 // Transposed LDS read of 16-bit elements: lane i of each group of 16 lanes gets element
