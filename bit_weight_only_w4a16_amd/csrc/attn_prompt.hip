@@ -1,7 +1,7 @@
 // Causal attention over packed prompts (awq_attn_prompt in awq_block.h).
 //
-// One pass over the keys with a running maximum and sum per row (float32, base 2). A
-// workgroup owns 128 query rows of one head (four wavefronts of 32) and walks over the keys
+// One pass over the keys with a running maximum and sum per row (float32, base 2; the maximum
+// is brought up to date only when a tile needs it, see tile_step). A workgroup owns 128 query rows of one head (four wavefronts of 32) and walks over the keys
 // in tiles of 64 that all four share through LDS.
 //
 // Both products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with the 32 x 32 x 16
@@ -17,11 +17,14 @@
 // banks. Elements past D and rows past the sequence read as 0.
 #include "block_internal.hpp"
 
+#include <type_traits>
+
 namespace awq {
 namespace {
 
 constexpr int kBQ = 128;  // query rows per workgroup
 constexpr int kBK = 64;   // keys per tile
+constexpr float kShift = 12.0f, kMost = 4194304.0f;
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -46,6 +49,7 @@ __device__ __forceinline__ int v_pos(int r, int c) {
 // Finds the sequence of query tile `tile` (tiles are numbered sequence by sequence): 64
 // sequences at a time, one per lane. Returns false past the last tile.
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int& start, int& len, int& in_seq) {
+  if (tile < 0) return false;
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int b0 = 0; b0 < a.seqs; b0 += 64) {
@@ -75,6 +79,29 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int& st
   return false;
 }
 
+// Which query head and tile a workgroup takes. Workgroups go round the 8 XCDs, and each XCD's
+// L2 should see as few key / value heads as possible: XCD x takes head x, x + 8, .. one
+// after the other where the heads are a multiple of 8, and an equal share of the tiles of
+// head x % kv_heads where they divide 8. On an XCD the query heads of the group come first
+// (they read the same keys together), then the tiles, the last (longest) first.
+__device__ __forceinline__ void work_item(const PromptArgs& a, int& head, int& tile) {
+  const int kv_heads = a.q_heads / a.group, i = blockIdx.x;
+  int kv, at;  // key head, number among its tiles x group
+  if (kv_heads % 8 == 0) {
+    const int per = a.tiles * a.group, slot = i >> 3;
+    kv = (i & 7) + 8 * (slot / per);
+    at = slot % per;
+  } else if (8 % kv_heads == 0) {
+    kv = (i & 7) % kv_heads;
+    at = (i >> 3) * (8 / kv_heads) + (i & 7) / kv_heads;
+  } else {
+    kv = i / a.group % kv_heads;
+    at = i / a.q_heads * a.group + i % a.group;
+  }
+  head = kv * a.group + at % a.group;
+  tile = a.tiles - 1 - at / a.group;  // < 0 past the last of an uneven share
+}
+
 template <typename T, int DP>
 __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   constexpr int RB = DP * 2;            // bytes of a row in LDS
@@ -90,9 +117,10 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   const int lane = threadIdx.x & 63;
   const int col = lane & 31, h = lane >> 5;
 
-  const int head = blockIdx.x % a.q_heads;
+  int head, tile;
+  work_item(a, head, tile);
   int start, len, in_seq;
-  if (!find_tile(a, a.tiles - 1 - static_cast<int>(blockIdx.x / a.q_heads), start, len, in_seq)) return;
+  if (!find_tile(a, tile, start, len, in_seq)) return;
   start = __builtin_amdgcn_readfirstlane(start);
   len = __builtin_amdgcn_readfirstlane(len);
   const int q0 = __builtin_amdgcn_readfirstlane(in_seq) * kBQ;
@@ -113,21 +141,22 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
     k_off[j] = 8 * ck < a.head_dim ? static_cast<uint32_t>(r * a.k_token + 8 * ck) * 2 : kNoLoad;
     v_off[j] = 8 * cv < a.head_dim ? static_cast<uint32_t>(r * a.v_token + 8 * cv) * 2 : kNoLoad;
   }
-  auto load_tile = [&](int kv0, int buf) {
-    const int rows = min(kBK, len - kv0);
+  auto load_tile = [&](int j) {
+    const int kv0 = j * kBK, rows = min(kBK, len - kv0);
     const u32x4 rk =
         rsrc_words(kbase + kv0 * a.k_token, static_cast<uint32_t>((rows - 1) * a.k_token + a.head_dim) * 2);
     const u32x4 rv =
         rsrc_words(vbase + kv0 * a.v_token, static_cast<uint32_t>((rows - 1) * a.v_token + a.head_dim) * 2);
-    unsigned char* dst = smem + buf * 2 * TILE + LOADS * wave * 1024;
+    const uint32_t dst = lds_offset(smem) + (j & 1) * 2 * TILE + LOADS * wave * 1024;
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) load_to_lds(rk, k_off[j], dst + j * 1024);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(rk, k_off[i], dst + i * 1024);
 #pragma unroll
-    for (int j = 0; j < LOADS; ++j) load_to_lds(rv, v_off[j], dst + TILE + j * 1024);
+    for (int i = 0; i < LOADS; ++i) load_to_lds(rv, v_off[i], dst + TILE + i * 1024);
   };
 
-  const int kv_end = min(len, q0 + kBQ);  // keys this workgroup needs
-  load_tile(0, 0);
+  // key tiles this workgroup needs, and this wavefront (none where its rows are past the end)
+  const int tiles = (min(len, q0 + kBQ) + kBK - 1) / kBK;
+  const int mine = wq0 < len ? min(tiles, (wq0 + 31) / kBK + 1) : 0;
 
   // Q^T operand: column l % 32, channels 16 c + 8 h .. + 7 (rows past the sequence: 0)
   v8 qf[NC];
@@ -150,75 +179,89 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   for (int t = 0; t < ND; ++t)
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
-  // P carries a factor 2^kShift: with the maximum at most kSlack above the one in use,
-  // binary16 holds it, and probabilities down to 2^-21 of the maximum keep their digits
-  constexpr float kShift = 7.0f, kSlack = 8.0f;
-  float m = kNegInf;  // maximum in use, in units of scores * c
+  float m = kNegInf;  // maximum in use (see below), in units of scores * c
   float l = 0.0f;     // this lane's part of the sum
+  float off = -kNegInf;  // kShift - m
 
   // LDS read positions
   const int tr_row = 4 * h + ((lane & 15) >> 2);                       // + 16 cc + 32 s (+ 8)
   const int tr_chunk = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);      // + 4 dt
   const int tr_byte = 8 * (lane & 1);
 
-  int buf = 0;
-  for (int kv0 = 0; kv0 < kv_end; kv0 += kBK, buf ^= 1) {
-    wait_loads<0>();  // this wavefront's loads of the tile have landed
-    lds_barrier();    // everyone's have, and the other buffer is free
-    if (kv0 + kBK < kv_end) load_tile(kv0 + kBK, buf ^ 1);
-    if (kv0 > wq0 + 31) continue;   // above the diagonal for this wavefront
-    const unsigned char* ks = smem + buf * 2 * TILE;
+  // Tile j (from buffer `buf`). The probabilities are first formed with the maximum in use,
+  // whatever the tile's own is, and added up as they were rounded: two ALU instructions per
+  // pair and none for a maximum. Where the sum ran past kMost (or is NaN: an infinite one in
+  // binary16), the maximum and what was summed so far are brought up to date and the tile's
+  // probabilities formed again. P carries 2^kShift, which keeps what is far below the
+  // maximum out of binary16's subnormals; a maximum in use up to 2^(16 - kShift) too low
+  // only makes P larger.
+  auto tile_step = [&](auto buf_, int j) {
+    const unsigned char* ks = smem + decltype(buf_)::value * 2 * TILE;
     const unsigned char* vs = ks + TILE;
-
+    auto k_frag = [&](int t, int c) {
+      const int r = 32 * t + col;
+      return *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 2 * c + h));
+    };
+    // all K fragments are read before the first product (left to itself the compiler reads
+    // each right before its use and waits for LDS sixteen times)
     float16_t s[2];
+    v8 kf[2][NC];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int c = 0; c < NC; ++c) kf[t][c] = k_frag(t, c);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int r = 32 * t + col;
-        const v8 kf = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 2 * c + h));
-        s[t] = T::mfma32(kf, qf[c], s[t]);
-      }
+      for (int c = 0; c < NC; ++c) s[t] = T::mfma32(kf[t][c], qf[c], s[t]);
     }
-    if (kv0 + kBK - 1 > wq0) {  // the tile reaches past some row of the wavefront
+    if (j * kBK + kBK - 1 > wq0) {  // the tile reaches past some row of the wavefront
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int key = kv0 + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
+          const int key = j * kBK + 32 * t + 8 * (i >> 2) + 4 * h + (i & 3);
           s[t][i] = key <= row ? s[t][i] : kNegInf;
         }
     }
-    float top = kNegInf;
+    u32x4 p[4];  // P^T operands of the four 16-key steps
+    auto probabilities = [&]() {
+      float sum = 0.0f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
-    top = xor32_max(top) * a.c;
-    // rescale only when some row's maximum grew by more than the slack
-    if (__ballot(top > m + kSlack) != 0) {
-      const float m_new = fmaxf(m, top);
-      const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+        for (int i = 0; i < 16; i += 2) {
+          const uint32_t pair = T::pack2(__builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], a.c, off)),
+                                         __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i + 1], a.c, off)));
+          sum = T::add2(pair, sum);
+          p[2 * t + (i >> 3)][(i >> 1) & 3] = pair;
+        }
+      return sum;
+    };
+    float sum = probabilities();
+    if (__ballot(!(sum < kMost)) != 0) {
+      float top = kNegInf;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
+      top = fmaxf(m, xor32_max(top) * a.c);
+      // a row that has seen no finite score yet: its scores of -inf give 0 with off = 0
+      const float m_new = top == kNegInf ? kShift : top;
+      const float keep = __builtin_amdgcn_exp2f(m - m_new);
       m = m_new;
+      off = kShift - m;
       l *= keep;
 #pragma unroll
       for (int t = 0; t < ND; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] *= keep;
+      sum = probabilities();
     }
-    const float off = m == kNegInf ? 0.0f : kShift - m;
-    u32x4 p[4];  // P^T operands of the four 16-key steps
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], a.c, off));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i + 1], a.c, off));
-        l += e0 + e1;
-        p[2 * t + (i >> 3)][(i >> 1) & 3] = T::pack2(e0, e1);
-      }
+    l += sum;
 #pragma unroll
     for (int cc = 0; cc < 4; ++cc) {
       const v8 pf = __builtin_bit_cast(v8, p[cc]);
@@ -231,6 +274,18 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
         acc[dt] = T::mfma32(join8<v8>(lo, hi), pf, acc[dt]);
       }
     }
+  };
+
+  load_tile(0);
+  auto pass = [&](auto buf, int j) {
+    wait_loads<0>();  // this wavefront's loads of the tile have landed
+    lds_barrier();    // everyone's have, and the other buffer is free
+    if (j + 1 < tiles) load_tile(j + 1);
+    if (j < mine) tile_step(buf, j);
+  };
+  for (int j = 0; j < tiles; j += 2) {
+    pass(std::integral_constant<int, 0>{}, j);
+    if (j + 1 < tiles) pass(std::integral_constant<int, 1>{}, j + 1);
   }
 
   l = xor32_add(l);
@@ -240,9 +295,9 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) broken |= acc[dt][i] != acc[dt][i];
-  broken |= inv != inv;
-  // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
-  uint64_t again = __ballot(broken && row < len);
+  // rows that came out NaN though their probabilities' sum is not (masked ones add exactly 0):
+  // below, key by key, for a masked infinity or NaN may be the cause
+  uint64_t again = __ballot(broken && row < len && l == l);
   again = (again | (again >> 32)) & 0xFFFFFFFFu;
   if (row < len && ((again >> col) & 1) == 0) {
     uint16_t* o = a.out + (start + row) * a.o_token + head * a.o_head;
@@ -312,7 +367,7 @@ hipError_t launch_attn_prompt(const awq_attn_prompt_args& g, hipStream_t st) {
   a.group = g.q_heads / g.kv_heads;
   a.head_dim = g.head_dim;
   a.c = g.scale * kLog2e;
-  const int64_t blocks = tiles * g.q_heads;
+  const int64_t blocks = (tiles * g.q_heads + 7) / 8 * 8;  // (an uneven share leaves some idle)
   if (g.dtype == AWQ_DT_F16)
     return g.head_dim <= 64 ? launch_dp<F16, 64>(a, blocks, st) : launch_dp<F16, 128>(a, blocks, st);
   return g.head_dim <= 64 ? launch_dp<BF16, 64>(a, blocks, st) : launch_dp<BF16, 128>(a, blocks, st);

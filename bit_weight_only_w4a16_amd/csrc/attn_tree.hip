@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     *reinterpret_cast<u32x4*>(q_lds + r * RB + 16 * k_pos<DP>(r, ch)) = x;
   }
   unsigned char* ring = smem + wave * kStages * 2 * TILE;
+  const uint32_t ring_at = lds_offset(smem) + wave * kStages * 2 * TILE;
   if constexpr (PAD) {  // chunks past D are never loaded: they stay 0
     for (int i = lane; i < kStages * 2 * TILE / 16; i += 64)
       *reinterpret_cast<u32x4*>(ring + 16 * i) = u32x4{0, 0, 0, 0};
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     }
   };
   auto load_step = [&](const int64_t at[LOADS], int stage) {
-    unsigned char* dst = ring + stage * 2 * TILE;
+    const uint32_t dst = ring_at + stage * 2 * TILE;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       const int r = ROWS * j + lane / RC;
@@ -365,8 +366,9 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
         o += *reinterpret_cast<const float2_t*>(sums + (w * 16 * NT + r) * L::kSumStride + 2 * lane);
     }
     const int t = (r0 + r) / a.group, hq = kv_head * a.group + (r0 + r) % a.group;
-    // a row that came out NaN: again, key by key (a masked infinity or NaN may be the cause)
-    if (__ballot(o.x != o.x || o.y != o.y) != 0) {
+    // a row that came out NaN though its probabilities' sum is not: again, key by key (a
+    // masked infinity or NaN may be the cause)
+    if (sum == sum && __ballot(o.x != o.x || o.y != o.y) != 0) {
       const uint64_t bits = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
       attend_row<T>(a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, p0, p1,
                     [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
     for (int j = 0; j < LOADS; ++j) at[j] = offset_of(min(s0 + OWN * wave + ROWS * j + lane / RC, p1 - 1));
   };
   auto load_step = [&](const int64_t at[LOADS], int stage) {
-    unsigned char* dst = smem + stage * 2 * TILE + OWN * wave * RB;
+    const uint32_t dst = lds_offset(smem) + stage * 2 * TILE + OWN * wave * RB;
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       const int r = ROWS * j + lane / RC;  // (of this wavefront's 16, a multiple of the patterns' period)
@@ -608,8 +610,9 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
       for (int i = 0; i < 4; ++i) broken |= acc[n][d][i] != acc[n][d][i];
     }
     const bool real = row0 + 16 * n < rows;
-    // rows that came out NaN: below, key by key (a masked infinity or NaN may be the cause)
-    uint64_t again = __ballot(broken && real);
+    // rows that came out NaN though their probabilities' sum is not: below, key by key (a
+    // masked infinity or NaN may be the cause)
+    uint64_t again = __ballot(broken && real && l[n] == l[n]);
     again = (again | (again >> 16) | (again >> 32) | (again >> 48)) & 0xFFFFu;
     if (real && ((again >> col) & 1) == 0) {
       const int64_t at_row = (static_cast<int64_t>(token[n]) * a.q_heads + head[n]) * a.splits + split;

@@ -33,6 +33,10 @@ struct F16 {
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, half2_t));
   }
+  // sum + the two elements of a pair, in float32
+  static __device__ __forceinline__ float add2(uint32_t pair, float sum) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, pair), half2_t{1.0f, 1.0f}, sum, false);
+  }
   static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
@@ -51,6 +55,10 @@ struct BF16 {
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf2_t));
   }
+  static __device__ __forceinline__ float add2(uint32_t pair, float sum) {
+    const bf2_t ones = {static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)};
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2_t, pair), ones, sum, false);
+  }
   static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
@@ -59,33 +67,35 @@ struct BF16 {
   }
 };
 
-// Loads from memory straight into LDS: lane l's 16 bytes go to `dst` + 16 l (dst the same in
-// all lanes). Written as assembly because the compiler, which cannot tell the stages of a
-// ring apart, waits for every such load of its own before each transposing LDS read (the
-// prefetched step would be waited for in the middle of the one before it). The instructions
-// have no register result; the kernels wait with wait_loads, and a wait that the compiler
-// counts for a load of its own only gets longer by these.
-__device__ __forceinline__ uint32_t lds_offset(const unsigned char* p) {
-  return __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(
-      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const unsigned char*)(p))));
+// Loads from memory straight into LDS: lane l's 16 bytes go to LDS byte `dst` + 16 l (dst the
+// same in all lanes). Written as assembly because the compiler, which cannot tell the
+// stages of a ring apart, waits for every such load of its own before each transposing LDS
+// read (the prefetched step would be waited for in the middle of the one before it). The
+// instructions have no register result; the kernels wait with wait_loads, and a wait that
+// the compiler counts for a load of its own only gets longer by these.
+__device__ __forceinline__ uint32_t lds_offset(const void* shared) {
+  return static_cast<uint32_t>(
+      reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const unsigned char*)(shared)));
 }
-__device__ __forceinline__ void load_to_lds(const void* src, unsigned char* dst) {
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v)));
+}
+__device__ __forceinline__ void load_to_lds(const void* src, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
-               : "s"(lds_offset(dst)), "v"(src)
+               : "s"(uniform(dst)), "v"(src)
                : "m0", "memory");
 }
 // the same from a buffer resource: an offset past its end writes zeros
-__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, unsigned char* dst) {
+__device__ __forceinline__ void load_to_lds(u32x4 rsrc, uint32_t offset, uint32_t dst) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                :
-               : "s"(lds_offset(dst)), "v"(offset), "s"(rsrc)
+               : "s"(uniform(dst)), "v"(offset), "s"(rsrc)
                : "m0", "memory");
 }
 // the words of make_rsrc's resource, in scalar registers
 __device__ __forceinline__ u32x4 rsrc_words(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
-  auto uniform = [](uint32_t v) { return static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<int>(v))); };
   return u32x4{uniform(static_cast<uint32_t>(a)), uniform(static_cast<uint32_t>(a >> 32) & 0xFFFFu), uniform(bytes),
                0x00020000u};
 }
@@ -123,9 +133,25 @@ __device__ __forceinline__ V8 join8(short4_t a, short4_t b) {
   return __builtin_bit_cast(V8, short8_t{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w});
 }
 
-// v from the lane 32 (16) lanes away, combined by maximum / sum
-__device__ __forceinline__ float xor32_max(float v) { return fmaxf(v, __shfl_xor(v, 32)); }
-__device__ __forceinline__ float xor32_add(float v) { return v + __shfl_xor(v, 32); }
+// v combined with that of the lane 32 lanes away, by maximum / sum. The swap instruction
+// exchanges one operand's upper half with the other's lower: of v and a copy of it, the
+// results are the lower halves twice and the upper halves twice. (The copy is opaque to
+// the compiler, which otherwise takes the two results for one value.)
+__device__ __forceinline__ float2_t halves(float v) {
+  unsigned int a = __builtin_bit_cast(unsigned int, v), b = a;
+  asm("" : "+v"(b));
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  const unsigned int lo = r[0], hi = r[1];
+  return float2_t{__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)};
+}
+__device__ __forceinline__ float xor32_max(float v) {
+  const float2_t h = halves(v);
+  return fmaxf(h.x, h.y);
+}
+__device__ __forceinline__ float xor32_add(float v) {
+  const float2_t h = halves(v);
+  return h.x + h.y;
+}
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -146,7 +172,8 @@ __device__ __forceinline__ float inv_sum(float l) { return l == 0.0f ? 0.0f : 1.
 // row does not see are skipped, not multiplied by zero, so nothing in them reaches the row.
 // The matrix kernels multiply masked probabilities of exactly 0 with whatever the masked
 // value row holds; where that is an infinity or NaN the row comes out NaN, and the kernels
-// take this path for rows that came out NaN. key(j, k, v) gives key j's rows and whether the
+// take this path for rows that came out NaN while the sum of their probabilities, to which
+// masked keys add exactly 0, did not. key(j, k, v) gives key j's rows and whether the
 // row sees it.
 template <typename T, typename Key>
 __device__ __forceinline__ void attend_row(const uint16_t* q, int head_dim, float c, int64_t first,

@@ -43,37 +43,6 @@ __device__ __forceinline__ float apply_epilogue(float v, int n, int64_t o, const
 }
 __device__ __forceinline__ float apply_epilogue(float v, int, int64_t) { return v; }
 
-// the same for eight consecutive outputs of a row, with 16-byte accesses (n a multiple of 8)
-__device__ __forceinline__ void add8(float v[8], uint4 w) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] += static_cast<float>(as_h2(u[i]).x);
-    v[2 * i + 1] += static_cast<float>(as_h2(u[i]).y);
-  }
-}
-__device__ __forceinline__ void apply_epilogue8(float v[8], int n, int64_t o, const Epilogue& e, uint16_t* y) {
-  if (e.bias != nullptr) add8(v, *reinterpret_cast<const uint4*>(e.bias + n));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = activate(v[i], e.act);
-  if (e.mul != nullptr) {
-    const uint4 w = *reinterpret_cast<const uint4*>(e.mul + o);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] *= static_cast<float>(as_h2(u[i]).x);
-      v[2 * i + 1] *= static_cast<float>(as_h2(u[i]).y);
-    }
-  }
-  if (e.residual != nullptr) add8(v, *reinterpret_cast<const uint4*>(e.residual + o));
-  uint32_t r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = as_u32(half2_t{static_cast<_Float16>(v[2 * i]), static_cast<_Float16>(v[2 * i + 1])});
-  *reinterpret_cast<uint4*>(y + o) = make_uint4(r[0], r[1], r[2], r[3]);
-}
-__device__ __forceinline__ void apply_epilogue8(float*, int, int64_t, uint16_t*) {}
-
 // Orders one wavefront's LDS accesses for the compiler (the hardware executes them in order):
 // what some lanes store, other lanes read.
 __device__ __forceinline__ void wave_lds_fence() {
@@ -81,6 +50,80 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
+
+// the same for eight consecutive outputs of a row, whose factors and residuals are in m and r
+typedef float float8_t __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ float8_t widen8(uint4 w) {
+  const half8_t h = __builtin_bit_cast(half8_t, w);
+  return __builtin_convertvector(h, float8_t);
+}
+template <int ACT>
+__device__ __forceinline__ float8_t activate8(float8_t v) {
+  return float8_t{activate(v[0], ACT), activate(v[1], ACT), activate(v[2], ACT), activate(v[3], ACT),
+                  activate(v[4], ACT), activate(v[5], ACT), activate(v[6], ACT), activate(v[7], ACT)};
+}
+__device__ __forceinline__ uint4 apply_epilogue8(float8_t v, int n, uint4 m, uint4 r, const Epilogue& e) {
+  if (e.bias != nullptr) v += widen8(*reinterpret_cast<const uint4*>(e.bias + n));
+  switch (e.act) {  // once for the eight
+    case AWQ_ACT_RELU: v = activate8<AWQ_ACT_RELU>(v); break;
+    case AWQ_ACT_GELU: v = activate8<AWQ_ACT_GELU>(v); break;
+    case AWQ_ACT_GELU_TANH: v = activate8<AWQ_ACT_GELU_TANH>(v); break;
+    case AWQ_ACT_SILU: v = activate8<AWQ_ACT_SILU>(v); break;
+    default: break;
+  }
+  if (e.mul != nullptr) v *= widen8(m);
+  if (e.residual != nullptr) v += widen8(r);
+  return __builtin_bit_cast(uint4, __builtin_convertvector(v, half8_t));
+}
+
+// A wavefront's MS x WN matrix-core tiles of sums (element q of lane l of a tile is row
+// 4 (l / 16) + q, column l % 16) through its own LDS, 1 KiB per tile at tile(ms, j), so that
+// a lane gets eight consecutive outputs of a row and the tail's operands and y move in
+// 16-byte accesses; the operands of four such runs are on their way at a time (y may be one
+// of the operands, so the compiler moves no load past a store by itself). sums(ms, j) is
+// called once per tile, before its LDS is written. Rows from m0, columns from n0.
+template <int MS, int WN, typename Tile, typename Sums>
+__device__ __forceinline__ void store_tiles(Tile tile, Sums sums, int m0, int n0, int M, int N, const Epilogue& e,
+                                            uint16_t* y) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int ms = 0; ms < MS; ++ms)
+#pragma unroll
+    for (int j = 0; j < WN; ++j) {
+      const float4_t v = sums(ms, j);
+      wave_lds_fence();  // sums may have read the tile's place
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tile(ms, j)[(4 * (lane >> 4) + q) * 16 + (lane & 15)] = v[q];
+    }
+  wave_lds_fence();
+  constexpr int RUNS = MS * 32 * WN, AHEAD = RUNS >= 256 ? 4 : (RUNS + 63) / 64;
+#pragma unroll 1
+  for (int at0 = lane; at0 < RUNS; at0 += 64 * AHEAD) {
+    int64_t o[AHEAD];  // -1: past the output
+    uint4 m[AHEAD], r[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int at = at0 + 64 * i, row = m0 + at / (2 * WN), n = n0 + 8 * (at % (2 * WN));
+      o[i] = at < RUNS && row < M && n < N ? static_cast<int64_t>(row) * N + n : -1;
+      m[i] = r[i] = make_uint4(0, 0, 0, 0);
+      if (e.mul != nullptr && o[i] >= 0) m[i] = *reinterpret_cast<const uint4*>(e.mul + o[i]);
+      if (e.residual != nullptr && o[i] >= 0) r[i] = *reinterpret_cast<const uint4*>(e.residual + o[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (o[i] < 0) continue;
+      const int at = at0 + 64 * i, ms = at / (32 * WN), oct = at % (2 * WN);
+      const float* src = tile(ms, oct >> 1) + at / (2 * WN) % 16 * 16 + 8 * (oct & 1);
+      const float4_t lo = *reinterpret_cast<const float4_t*>(src);
+      const float4_t hi = *reinterpret_cast<const float4_t*>(src + 4);
+      const float8_t v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      *reinterpret_cast<uint4*>(y + o[i]) = apply_epilogue8(v, n0 + 8 * oct, m[i], r[i], e);
+    }
+  }
+  wave_lds_fence();
+}
+template <int MS, int WN, typename Tile, typename Sums>
+__device__ __forceinline__ void store_tiles(Tile, Sums, int, int, int, int, uint16_t*) {}
 
 hipError_t launch_gemv_fused(const uint16_t* x, const uint16_t* inv_s_c, const void* packed, int64_t M,
                              int64_t N, int64_t K, int32_t group, int32_t fmt, const Epilogue& e,

@@ -291,6 +291,20 @@ __global__ void __launch_bounds__(kGThreads * KS)
           acc[ms][j] += red[((((k2 - 1) * 4 + wave) * WM + ms) * WN + j) * 64 + lane];
   }
 
+  if constexpr (sizeof...(E) > 0) {
+    // The wavefront's LDS: for KS > 1 where the second slice's sums for it were (its own reads
+    // of them, above, are done), else its share of the X' buffers, half of the row tiles at
+    // a time where four column tiles need more than that.
+    constexpr int PASSES = KS > 1 || WN <= 2 ? 1 : 2, MSP = WM / PASSES;
+#pragma unroll
+    for (int pass = 0; pass < PASSES; ++pass)
+      store_tiles<MSP, WN>(
+          [&](int ms, int j) { return reinterpret_cast<float*>(xs_all) + ((wave * MSP + ms) * WN + j) * 256; },
+          [&](int ms, int j) { return acc[pass * MSP + ms][j]; }, m_blk + (wm * WM + pass * MSP) * 16,
+          n_blk + wn * WN * 16, a.M, a.N, epi..., a.y);
+    return;
+  }
+
   // epilogue: element q of acc[ms][j] is row 4 (l / 16) + q, column l % 16 of its tile;
   // binary16 y, or with split K this split's float32 partial sums
   float* part = a.part ? a.part + static_cast<int64_t>(split) * a.M * a.N : nullptr;
@@ -307,8 +321,7 @@ __global__ void __launch_bounds__(kGThreads * KS)
           if (part) {
             part[o] = acc[ms][j][q];
           } else {
-            const float v = apply_epilogue(acc[ms][j][q], n, o, epi...);
-            a.y[o] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+            a.y[o] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(acc[ms][j][q]));
           }
         }
       }

@@ -279,11 +279,9 @@ __global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a, E... ep
   }
 
   if constexpr (sizeof...(E) > 0) {
-    // Unsplit sums with an Epilogue go through LDS, so that a lane gets eight consecutive
-    // outputs of a row and the tail's operands and y move in 16-byte accesses instead of
-    // 2-byte ones. Column tile j of row tile ms of the wavefront has the 1 KiB at
-    // ((ms WN + j) 4 + wave) KiB: for KS = 2 (128 KiB of LDS) where the second half's sums of
-    // that tile, read just before, were; for KS = 1 (64 KiB) four row tiles at a time.
+    // Column tile j of row tile ms of a wavefront has the 1 KiB at ((ms WN + j) 4 + wave) KiB:
+    // for KS = 2 (128 KiB of LDS) where the second half's sums of that tile were, for KS = 1
+    // (64 KiB) four row tiles at a time.
     constexpr int PASSES = KS == 2 ? 1 : 2, MSP = WM / PASSES;
     float4_t* red = reinterpret_cast<float4_t*>(smem_all);
     if constexpr (KS == 2) {
@@ -297,38 +295,15 @@ __global__ void __launch_bounds__(256 * KS) gemm_wide_kernel(WideArgs a, E... ep
       if (half == 1) return;
     }
 #pragma unroll
-    for (int pass = 0; pass < PASSES; ++pass) {
-#pragma unroll
-      for (int ms = 0; ms < MSP; ++ms) {
-#pragma unroll
-        for (int j = 0; j < WN; ++j) {
-          const int slot = (ms * WN + j) * 4 + wave;
-          float4_t v = acc[pass * MSP + ms][j];
-          if constexpr (KS == 2) {
-            v += red[slot * 64 + lane];
-            wave_lds_fence();  // the slot is read before it is written again
-          }
-          float* tile = reinterpret_cast<float*>(smem_all) + slot * 256;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tile[(4 * p + q) * 16 + r] = v[q];
-        }
-      }
-      wave_lds_fence();
-#pragma unroll 1
-      for (int at = lane; at < MSP * 32 * WN; at += 64) {  // eight outputs each
-        const int ms = at / (32 * WN), row = at / (2 * WN) % 16, oct = at % (2 * WN);
-        const int m = m_blk + (pass * MSP + ms) * 16 + row, n = n_blk + wave * WN * 16 + 8 * oct;
-        if (m < a.M && n < a.N) {
-          const float* src = reinterpret_cast<const float*>(smem_all) +
-                             ((ms * WN + (oct >> 1)) * 4 + wave) * 256 + row * 16 + 8 * (oct & 1);
-          const float4_t lo = *reinterpret_cast<const float4_t*>(src);
-          const float4_t hi = *reinterpret_cast<const float4_t*>(src + 4);
-          float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-          apply_epilogue8(v, n, static_cast<int64_t>(m) * a.N + n, epi..., a.y);
-        }
-      }
-      wave_lds_fence();
-    }
+    for (int pass = 0; pass < PASSES; ++pass)
+      store_tiles<MSP, WN>(
+          [&](int ms, int j) { return reinterpret_cast<float*>(smem_all) + ((ms * WN + j) * 4 + wave) * 256; },
+          [&](int ms, int j) {
+            float4_t v = acc[pass * MSP + ms][j];
+            if constexpr (KS == 2) v += red[((ms * WN + j) * 4 + wave) * 64 + lane];
+            return v;
+          },
+          m_blk + pass * MSP * 16, n_blk + wave * WN * 16, a.M, a.N, epi..., a.y);
     return;
   }
 
