@@ -394,7 +394,8 @@ class QuantLinear:
     calibration rows, fold, quantize, pack, repack -- all in the library's kernels).
     Calls go to awq_gemm, which runs the decode kernel itself where that is faster (a few
     rows, or up to 16 rows on small layers); ``gemv_max_m`` sends up to that many rows to
-    awq_gemv directly instead.
+    awq_gemv directly instead. A call with a tail (bias [N], act, mul or residual [M, N]) is
+    block.awq_gemm_fused: act(x . deq(Wq)^T + bias) * mul + residual.
     """
 
     def __init__(self, packed, n, k, inv_s_c=None, group=GROUP, fmt=FMT_ASYM, gemv_max_m=0):
@@ -412,8 +413,12 @@ class QuantLinear:
         packed = awq_repack(qweight, scales, qzeros, n, k, group, fmt)
         return cls(packed, n, k, inv, group, fmt, **kw)
 
-    def __call__(self, x, y=None):
+    def __call__(self, x, y=None, *, bias=None, act="none", mul=None, residual=None):
         m = x.shape[0]
         ws = workspace(max(m, 1), self.n, self.k, x.device, self.group)
+        if bias is not None or act != "none" or mul is not None or residual is not None:
+            from . import block
+            return block.awq_gemm_fused(x, self.inv_s_c, self.packed, self.n, self.k, self.group, self.fmt,
+                                        bias=bias, act=act, mul=mul, residual=residual, y=y, ws=ws)
         fn = awq_gemv if 1 <= m <= self.gemv_max_m else awq_gemm
         return fn(x, self.inv_s_c, self.packed, self.n, self.k, self.group, self.fmt, y, ws)
