@@ -1,8 +1,11 @@
 // Causal attention over packed prompts (awq_attn_prompt in awq_block.h).
 //
 // One pass over the keys with a running maximum and sum per row (float32, base 2; the maximum
-// is brought up to date only when a tile needs it, see tile_step). A workgroup owns 128 query rows of one head (four wavefronts of 32) and walks over the keys
-// in tiles of 64 that all four share through LDS.
+// is brought up to date only when a tile needs it, see tile_step). A workgroup owns 128 query
+// rows of one key / value head, four wavefronts of 32 tokens of a query head, and walks over
+// the keys in tiles of 64 that all four share through LDS. The wavefronts take one query head
+// at 128 tokens, or 2 or 4 heads of the group at the same 64 or 32 tokens, which leaves fewer
+// rows empty in short sequences (pick_heads).
 //
 // Both products are formed transposed, S^T = K Q^T and O^T = V^T P^T, with the 32 x 32 x 16
 // matrix instruction: lane l then holds scores of one query (column l % 32) for 16 keys per
@@ -22,8 +25,7 @@
 namespace awq {
 namespace {
 
-constexpr int kBQ = 128;  // query rows per workgroup
-constexpr int kBK = 64;   // keys per tile
+constexpr int kBK = 64;  // keys per tile
 constexpr float kShift = 12.0f, kMost = 4194304.0f;
 
 struct PromptArgs {
@@ -32,6 +34,7 @@ struct PromptArgs {
   const int32_t* cu;
   int64_t q_token, k_token, v_token, o_token, q_head, k_head, v_head, o_head;
   int32_t tokens, seqs, tiles, q_heads, group, head_dim;
+  int32_t heads_log2;  // of a workgroup's query heads; its tokens are 128 >> heads_log2
   float c;  // scale * log2(e)
 };
 
@@ -46,60 +49,55 @@ __device__ __forceinline__ int v_pos(int r, int c) {
   return DP == 128 ? c ^ ((r & 3) << 2) : c ^ (((r >> 1) & 1) << 2);
 }
 
-// Finds the sequence of query tile `tile` (tiles are numbered sequence by sequence): 64
-// sequences at a time, one per lane. Returns false past the last tile.
-__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int& start, int& len, int& in_seq) {
-  if (tile < 0) return false;
-  const int lane = threadIdx.x & 63;
-  int before = 0;
-  for (int b0 = 0; b0 < a.seqs; b0 += 64) {
-    const int b = b0 + lane;
-    int s = 0, n = 0;
-    if (b < a.seqs) {
+// Finds the sequence of query tile `tile` and which of its tiles that is. Sequence b's tiles
+// are numbered from cu[b] / size + b, which leaves each its ceil(length / size) numbers and
+// few unused ones, and needs no sum over the sequences before: 64 lanes search 64 ways.
+// Returns false where the number is unused.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int tile, int& start, int& len, int& q0) {
+  const int lane = threadIdx.x & 63, shift = 7 - a.heads_log2;
+  int b0 = 0, count = a.seqs;
+  while (true) {  // the last of the sequences [b0, b0 + count) that starts at or before the tile
+    const int stride = (count + 63) >> 6, mine = lane * stride, b = b0 + mine;
+    int s = 0, e = 0;
+    if (mine < count) {
       s = min(max(a.cu[b], 0), a.tokens);
-      n = max(min(a.cu[b + 1], a.tokens) - s, 0);
+      e = min(max(a.cu[b + 1], 0), a.tokens);
     }
-    const int mine = (n + kBQ - 1) / kBQ;
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int other = __shfl_up(upto, d);
-      if (lane >= d) upto += other;
-    }
-    const uint64_t past = __ballot(before + upto > tile);
-    if (past != 0) {
-      const int w = __builtin_ctzll(past);
+    const uint64_t before = __ballot(mine < count && (s >> shift) + b <= tile);
+    if (before == 0) return false;
+    const int w = 63 - __builtin_clzll(before);
+    if (stride == 1) {
       start = __builtin_amdgcn_readlane(s, w);
-      len = __builtin_amdgcn_readlane(n, w);
-      in_seq = tile - before - __builtin_amdgcn_readlane(upto - mine, w);
-      return true;
+      len = __builtin_amdgcn_readlane(e, w) - start;
+      q0 = (tile - (start >> shift) - b0 - w) << shift;
+      return q0 < len;
     }
-    before += __builtin_amdgcn_readlane(upto, 63);
+    b0 += w * stride;
+    count = min(stride, count - w * stride);
   }
-  return false;
 }
 
-// Which query head and tile a workgroup takes. Workgroups go round the 8 XCDs, and each XCD's
-// L2 should see as few key / value heads as possible: XCD x takes head x, x + 8, .. one
-// after the other where the heads are a multiple of 8, and an equal share of the tiles of
-// head x % kv_heads where they divide 8. On an XCD the query heads of the group come first
-// (they read the same keys together), then the tiles, the last (longest) first.
+// Which query heads (from `head` on) and tile a workgroup takes. Workgroups go round the 8
+// XCDs, and each XCD's L2 should see as few key / value heads as possible: XCD x takes head
+// x, x + 8, .. one after the other where the heads are a multiple of 8, and an equal share of
+// the tiles of head x % kv_heads where they divide 8. On an XCD the parts of the group come
+// first (they read the same keys together), then the tiles, a sequence's last (longest) first.
 __device__ __forceinline__ void work_item(const PromptArgs& a, int& head, int& tile) {
-  const int kv_heads = a.q_heads / a.group, i = blockIdx.x;
-  int kv, at;  // key head, number among its tiles x group
+  const int kv_heads = a.q_heads / a.group, parts = a.group >> a.heads_log2, i = blockIdx.x;
+  int kv, at;  // key head, number among its tiles x parts of the group
   if (kv_heads % 8 == 0) {
-    const int per = a.tiles * a.group, slot = i >> 3;
+    const int per = a.tiles * parts, slot = i >> 3;
     kv = (i & 7) + 8 * (slot / per);
     at = slot % per;
   } else if (8 % kv_heads == 0) {
     kv = (i & 7) % kv_heads;
     at = (i >> 3) * (8 / kv_heads) + (i & 7) / kv_heads;
   } else {
-    kv = i / a.group % kv_heads;
-    at = i / a.q_heads * a.group + i % a.group;
+    kv = i / parts % kv_heads;
+    at = i / (kv_heads * parts) * parts + i % parts;
   }
-  head = kv * a.group + at % a.group;
-  tile = a.tiles - 1 - at / a.group;  // < 0 past the last of an uneven share
+  head = kv * a.group + (at % parts << a.heads_log2);
+  tile = a.tiles - 1 - at / parts;  // < 0 past the last of an uneven share
 }
 
 template <typename T, int DP>
@@ -119,14 +117,16 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
 
   int head, tile;
   work_item(a, head, tile);
-  int start, len, in_seq;
-  if (!find_tile(a, tile, start, len, in_seq)) return;
+  int start, len, q0;
+  if (!find_tile(a, tile, start, len, q0)) return;
   start = __builtin_amdgcn_readfirstlane(start);
   len = __builtin_amdgcn_readfirstlane(len);
-  const int q0 = __builtin_amdgcn_readfirstlane(in_seq) * kBQ;
-  const int kv_head = head / a.group;
-  const int wq0 = q0 + 32 * wave;    // this wavefront's first row
-  const int row = wq0 + col;         // this lane's row
+  q0 = __builtin_amdgcn_readfirstlane(q0);
+  const int kv_head = head / a.group, size = 128 >> a.heads_log2;
+  const int sub = wave & ((4 >> a.heads_log2) - 1);  // which 32 of the tile's tokens
+  head += wave >> (2 - a.heads_log2);
+  const int wq0 = q0 + 32 * sub;  // this wavefront's first row
+  const int row = wq0 + col;      // this lane's row
 
   const uint16_t* kbase = a.k + start * a.k_token + kv_head * a.k_head;
   const uint16_t* vbase = a.v + start * a.v_token + kv_head * a.v_head;
@@ -155,13 +155,13 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   };
 
   // key tiles this workgroup needs, and this wavefront (none where its rows are past the end)
-  const int tiles = (min(len, q0 + kBQ) + kBK - 1) / kBK;
+  const int tiles = (min(len, q0 + size) + kBK - 1) / kBK;
   const int mine = wq0 < len ? min(tiles, (wq0 + 31) / kBK + 1) : 0;
 
   // Q^T operand: column l % 32, channels 16 c + 8 h .. + 7 (rows past the sequence: 0)
   v8 qf[NC];
   {
-    const int rows = min(kBQ, len - q0);
+    const int rows = min(size, len - q0);
     const __amdgpu_buffer_rsrc_t rq =
         make_rsrc(a.q + (start + q0) * a.q_token + head * a.q_head,
                   static_cast<uint32_t>((rows - 1) * a.q_token + a.head_dim) * 2);
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
     for (int c = 0; c < NC; ++c) {
       const int d = 16 * c + 8 * h;
       const uint32_t off =
-          d < a.head_dim ? static_cast<uint32_t>((32 * wave + col) * a.q_token + d) * 2 : kNoLoad;
+          d < a.head_dim ? static_cast<uint32_t>((32 * sub + col) * a.q_token + d) * 2 : kNoLoad;
       qf[c] = __builtin_bit_cast(v8, buf_load16(rq, off, 0));
     }
   }
@@ -249,17 +249,19 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[t][i]);
       top = fmaxf(m, xor32_max(top) * a.c);
-      // a row that has seen no finite score yet: its scores of -inf give 0 with off = 0
-      const float m_new = top == kNegInf ? kShift : top;
-      const float keep = __builtin_amdgcn_exp2f(m - m_new);
-      m = m_new;
-      off = kShift - m;
+      // a row that has seen only scores of -inf: they give 0 with off = 0, and the next tile
+      // comes here again
+      const bool none = top == kNegInf;
+      const float keep = none ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      off = none ? 0.0f : kShift - m;
       l *= keep;
 #pragma unroll
       for (int t = 0; t < ND; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] *= keep;
       sum = probabilities();
+      off = kShift - m;
     }
     l += sum;
 #pragma unroll
@@ -341,6 +343,17 @@ hipError_t launch_dp(const PromptArgs& a, int64_t blocks, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Heads of a workgroup (log2). Many short sequences: as many as divide the group, for each
+// workgroup then fills its rows and a group's keys are read once (32 query heads on 8, D =
+// 128, 16 tokens each: 64, 256, 1024 sequences take 14, 36, 136 us; one head at a time 23, 83,
+// 332). From 256 tokens on, and where one head at a time leaves workgroups' slots empty, one:
+// the batches measured then take the same within 1 % (1 x 16 tokens 5.9 us, with four heads
+// 6.7; 6 ragged prompts of 993 tokens on average 121, 123; 8192 tokens 548, 552).
+int pick_heads(int64_t tokens, int64_t seqs, int q_heads, int group) {
+  if (tokens >= 256 * seqs || seqs * q_heads <= 512) return 0;
+  return group % 4 == 0 ? 2 : group % 2 == 0 ? 1 : 0;
+}
+
 }  // namespace
 
 hipError_t launch_attn_prompt(const awq_attn_prompt_args& g, hipStream_t st) {
@@ -360,14 +373,14 @@ hipError_t launch_attn_prompt(const awq_attn_prompt_args& g, hipStream_t st) {
   a.o_head = g.o_head;
   a.tokens = static_cast<int32_t>(g.tokens);
   a.seqs = static_cast<int32_t>(g.seqs);
-  // at most this many tiles for any lengths: sum of ceil(n / kBQ)
-  const int64_t tiles = g.tokens / kBQ + (g.seqs < g.tokens ? g.seqs : g.tokens);
-  a.tiles = static_cast<int32_t>(tiles);
   a.q_heads = g.q_heads;
   a.group = g.q_heads / g.kv_heads;
   a.head_dim = g.head_dim;
+  a.heads_log2 = pick_heads(g.tokens, g.seqs, g.q_heads, a.group);
+  const int64_t tiles = (g.tokens >> (7 - a.heads_log2)) + g.seqs;  // (the numbers, see find_tile)
+  a.tiles = static_cast<int32_t>(tiles);
   a.c = g.scale * kLog2e;
-  const int64_t blocks = (tiles * g.q_heads + 7) / 8 * 8;  // (an uneven share leaves some idle)
+  const int64_t blocks = ((tiles * g.q_heads >> a.heads_log2) + 7) / 8 * 8;  // (an uneven share leaves some idle)
   if (g.dtype == AWQ_DT_F16)
     return g.head_dim <= 64 ? launch_dp<F16, 64>(a, blocks, st) : launch_dp<F16, 128>(a, blocks, st);
   return g.head_dim <= 64 ? launch_dp<BF16, 64>(a, blocks, st) : launch_dp<BF16, 128>(a, blocks, st);

@@ -43,7 +43,8 @@ template <typename T, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(256) rope_kernel(awq_rope_args a, int heads_per_thread) {
   typedef typename Vec<V>::type vec;
   const int rot_chunks = a.rot_dim / (2 * V), chunks = rot_chunks + (a.head_dim - a.rot_dim) / V;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  // (a launch holds 2^32 threads along x)
+  const int64_t i = (static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
   const int64_t t = i / chunks;
   if (t >= a.tokens) return;
   const int c = static_cast<int>(i - t * chunks);
@@ -151,9 +152,11 @@ hipError_t launch_v(const awq_rope_args& a, hipStream_t st) {
   const int64_t blocks = (a.tokens * chunks + 255) / 256;
   const int rows = a.q_heads + 2 * a.kv_heads;
   // heads per thread: enough threads to fill the chip first, then up to 8
-  int per = static_cast<int>(blocks * rows / 2048);
-  per = per < 1 ? 1 : per > 8 ? 8 : per;
-  const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>((rows + per - 1) / per));
+  const int64_t share = blocks * rows / 2048;
+  const int per = share < 1 ? 1 : share > 8 ? 8 : static_cast<int>(share);
+  const int64_t z = (blocks + (1 << 23) - 1) >> 23;
+  const dim3 grid(static_cast<unsigned>((blocks + z - 1) / z), static_cast<unsigned>((rows + per - 1) / per),
+                  static_cast<unsigned>(z));
   if (a.interleaved) {
     hipLaunchKernelGGL((rope_kernel<T, V, true>), grid, dim3(256), 0, st, a, per);
   } else {

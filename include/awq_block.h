@@ -12,8 +12,9 @@
  *     statistics and rotations are float32.
  *   - Tokens are packed: x[token][head][d] with the head's D elements contiguous and the
  *     strides of the token and of the head (in elements) given, so that q, k and v may be
- *     views of one fused projection. Strides are multiples of 8 elements and less than
- *     2^24 (a cache's page stride is not limited); D is a multiple of 8, D <= 128.
+ *     views of one fused projection. Strides are multiples of 8 elements, a token's less
+ *     than 2^23 (those of heads, and of a cache, are not limited); D is a multiple of 8,
+ *     D <= 128. At most 4096 heads and 2^30 tokens.
  *   - `cu[B + 1]` (device, int32, not decreasing, cu[0] = 0) gives sequence b the packed
  *     tokens [cu[b], cu[b + 1]). Values are clamped to [0, tokens] on the device; outputs
  *     of tokens in no sequence are not written.
@@ -100,7 +101,7 @@ int awq_rope(const awq_rope_args* args, hipStream_t stream);
  * awq_attn_prompt - causal attention of packed prompts:
  *   out[t][h] = sum over j <= t of t's sequence of p_j v_j,  p = softmax(scale q_t . k_j)
  * Keys and values of later tokens never reach a row, infinities and NaN included.
- * scale is finite and positive.
+ * scale is finite and positive. (tokens / 128 + seqs) * q_heads <= 2^24 - 4096.
  */
 typedef struct awq_attn_prompt_args {
   const void* q;   /* [tokens][q_heads][D] */
@@ -133,6 +134,8 @@ int awq_attn_prompt(const awq_attn_prompt_args* args, hipStream_t stream);
  * see, and slots past the sequence's end, never reach it, infinities and NaN included.
  * block_table rows hold table_width entries; positions past table_width * page_size are
  * not there (the length is clamped), page numbers are clamped to [0, pages - 1].
+ * scale is finite and positive. At most 65535 sequences, table_width * page_size < 2^30,
+ * tokens * q_heads <= 2^31.
  * ws: device, awq_attn_tree_workspace_bytes() bytes (the partial results of a context split
  * over workgroups; overwritten by every call), may be NULL with ws_bytes == 0 where that is 0.
  */

@@ -98,6 +98,7 @@ PROMPT = dict(q=P, k=P, v=P, out=P, cu=P, tokens=100, seqs=2, q_token=512, q_hea
     (dict(scale=float("nan")), INVALID), (dict(k_token=120), INVALID), (dict(v_head=-8), INVALID),
     (dict(head_dim=256), UNSUPPORTED), (dict(k_token=1 << 23), UNSUPPORTED), (dict(q_heads=8192), UNSUPPORTED),
     (dict(tokens=1 << 30, q_heads=4096, seqs=1), UNSUPPORTED), (dict(q=P + 8), MISALIGNED),
+    (dict(tokens=1 << 29, seqs=1 << 22), UNSUPPORTED),
     (dict(out=P + 4), MISALIGNED), (dict(cu=P + 2), MISALIGNED), (dict(k_head=132), MISALIGNED),
 ])
 def test_prompt_refusals(lib, change, code):
@@ -121,6 +122,7 @@ TREE = dict(q=P, k_cache=P, v_cache=P, out=P, block_table=P, ctx_lens=P, cu_q=P,
     (dict(table_width=1 << 27), UNSUPPORTED), (dict(cache_slot=120), INVALID), (dict(cache_head=-8), INVALID),
     (dict(q=P + 2), MISALIGNED), (dict(mask=P + 4), MISALIGNED), (dict(ws=P + 8), MISALIGNED),
     (dict(cache_head=2044), MISALIGNED), (dict(ctx_lens=P + 1), MISALIGNED),
+    (dict(tokens=1 << 30), UNSUPPORTED),
 ])
 def test_tree_refusals(lib, change, code):
     assert call(lib.awq_attn_tree, c_abi.AttnTreeArgs(**{**TREE, **change})) == code

@@ -274,6 +274,26 @@ def test_prompt_large_scores():
     ref.check(out, *ref.prompt(q, k, v, lengths))
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_prompt_scores_of_minus_infinity_first(dtype):
+    """Rows whose first tiles hold only scores of -inf, then finite ones far below 0."""
+    n, d = 300, 64
+    g = torch.Generator().manual_seed(21)
+    q = torch.rand(n, 1, d, generator=g) + 0.5
+    k = -20 * (torch.rand(n, 1, d, generator=g) + 0.5)
+    k[:150, 0, 3] = float("-inf")
+    v = torch.randn(n, 1, d, generator=g)
+    q, k, v = (t.to(dtype).to(DEV) for t in (q, k, v))
+    out = block.awq_attn_prompt(q, k, v, cumulative([n]))
+    # (keys of -inf have probability 0: the reference's rows past them leave them out)
+    for t in (150, 151, 200, 299):
+        sees = (torch.arange(n) >= 150)[None] & (torch.arange(n) <= t)[None]
+        finite = torch.where(torch.isinf(k), torch.zeros_like(k), k)
+        want, bound = ref.attend(ref.cpu64(q[t:t + 1, 0]), ref.cpu64(finite[:, 0]), ref.cpu64(v[:, 0]), sees, d ** -0.5,
+                                 dtype)
+        ref.check(out[t:t + 1, 0], want, bound, f"row {t}")
+
+
 def test_prompt_many_sequences():
     """More sequences than a wavefront has lanes, empty ones among them."""
     lengths = [(i * 7) % 11 for i in range(150)]
@@ -281,6 +301,26 @@ def test_prompt_many_sequences():
     q, k, v = qkv.to(DEV).split([2, 2, 2], 1)
     out = block.awq_attn_prompt(q, k, v, cumulative(lengths))
     ref.check(out, *ref.prompt(q, k, v, lengths))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("count,hq,hkv", [(300, 8, 2), (140, 12, 3), (300, 2, 1), (5000, 4, 1)])
+def test_prompt_batches_of_short_sequences(dtype, count, hq, hkv):
+    """Several heads of a group in one workgroup; lengths of 0 to 70 tokens, one of 200. The
+    largest batch is checked at a few sequences."""
+    g = torch.Generator().manual_seed(count + hq)
+    lengths = torch.randint(0, 71 if count < 1000 else 9, (count,), generator=g).tolist()
+    lengths[count // 2] = 200
+    qkv, _ = prompt_inputs(lengths, hq, hkv, 64, dtype, seed=count)
+    q, k, v = qkv.to(DEV).split([hq, hkv, hkv], 1)
+    out = block.awq_attn_prompt(q, k, v, cumulative(lengths))
+    assert not bool(torch.isnan(out).any())
+    starts = [0]
+    for n in lengths:
+        starts.append(starts[-1] + n)
+    for b in {0, 1, 63, 64, 65, count // 2, count // 2 + 1, count - 2, count - 1}:
+        at = slice(starts[b], starts[b + 1])
+        ref.check(out[at], *ref.prompt(q[at], k[at], v[at], [lengths[b]]), f"sequence {b} of {lengths[b]}")
 
 
 def test_prompt_long():
@@ -444,6 +484,19 @@ def test_tree_offsets_past_32_bits():
     freq, _ = block.rope_frequencies(d, device=DEV)
     block.awq_rope(k, i32([5, 6]), freq, k=k, v=v, k_cache=kc, v_cache=vc, slots=slots)
     assert torch.equal(vc[pages - 1, :, 3], v[0]) and torch.equal(vc[pages - 40, :, 0], v[1])
+
+
+def test_rope_of_more_threads_than_a_launch_has_along_x():
+    """2^31 + threads: tokens of 16 elements, rotated by pairs of single elements."""
+    n, d = (1 << 31) // 15 + 1000, 16
+    x = torch.zeros(n, 1, d, dtype=F16, device=DEV)
+    x[-5:] = 1.0
+    positions = torch.zeros(n, dtype=torch.int32, device=DEV)
+    freq = torch.tensor([1.0], device=DEV)
+    positions[-5:] = i32([0, 1, 2, 3, 4])
+    block.awq_rope(x, positions, freq, q_out=x)
+    ref.check(x[-5:], *ref.rope(torch.ones(5, 1, d, dtype=F16), positions[-5:], freq))
+    assert float(x[:-5].abs().max()) == 0.0
 
 
 def test_tree_lengths_past_the_table_are_clamped():
