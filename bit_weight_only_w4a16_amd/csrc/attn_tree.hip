@@ -18,6 +18,7 @@
 // O^T, and V^T is read from LDS in that order with the transposing 16-bit read.
 #include "block_internal.hpp"
 
+#include <limits.h>
 #include <math.h>
 #include <stdlib.h>
 
@@ -657,38 +658,66 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
 }
 
 // Adds the splits of a row in their order: one wavefront per token and head, lane i has
-// d = 2 i, 2 i + 1.
+// d = 2 i, 2 i + 1. The launch is a few microseconds long and made of waiting, so everything
+// the first eight splits need is asked for at once: their maxima, sums and rows, which are
+// found from the token alone, and the sequences, 64 of them, that say how many splits count.
 constexpr int kMergeLoads = 8;
+
+// The sequence of a token: the last that starts at or before it. 64 lanes search 64 ways.
+__device__ __forceinline__ bool sequence_of(const TreeArgs& a, int token, Seq& s) {
+  const int lane = threadIdx.x & 63;
+  int b0 = 0, count = a.seqs;
+  while (true) {
+    const int stride = (count + 63) >> 6, at = lane * stride;
+    Seq mine = {INT_MAX, 0, 0, 0};
+    if (at < count) mine = sequence(a, b0 + at);
+    const uint64_t before = __ballot(mine.first <= token);
+    if (before == 0) return false;
+    const int w = 63 - __builtin_clzll(before);
+    if (stride == 1) {
+      s.first = __builtin_amdgcn_readlane(mine.first, w);
+      s.count = __builtin_amdgcn_readlane(mine.count, w);
+      s.len = __builtin_amdgcn_readlane(mine.len, w);
+      return token - s.first < s.count;
+    }
+    b0 += w * stride;
+    count = min(stride, count - w * stride);
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int b = blockIdx.y;
-  const Seq s = sequence(a, b);
-  const int i = blockIdx.x * 4 + wave;
-  const int t = i / a.q_heads, hq = i - t * a.q_heads;
-  if (t >= s.count) return;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + wave;
+  if (row >= static_cast<int64_t>(a.tokens) * a.q_heads) return;
+  const int token = static_cast<int>(row / a.q_heads), hq = static_cast<int>(row - static_cast<int64_t>(token) * a.q_heads);
+  const int64_t at = row * a.splits;
+  const float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim + 2 * at;
+  const float* part = a.part + at * a.head_dim + min(2 * lane, a.head_dim - 2);
+  // (splits past the sequence's hold anything: they are read and not used)
+  auto load = [&](int first, float2_t x[kMergeLoads]) {
+#pragma unroll
+    for (int j = 0; j < kMergeLoads; ++j)
+      x[j] = *reinterpret_cast<const float2_t*>(part + static_cast<int64_t>(min(first + j, a.splits - 1)) * a.head_dim);
+  };
+  float2_t x[kMergeLoads], own = *reinterpret_cast<const float2_t*>(ml + 2 * min(lane, a.splits - 1));
+  load(0, x);
+  Seq s;
+  if (!sequence_of(a, token, s)) return;
   const int chunk = chunk_of(s.len, a.splits);
   const int n = (s.len + chunk - 1) / chunk;
-  const int64_t at = (static_cast<int64_t>(s.first + t) * a.q_heads + hq) * a.splits;
-  const float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim + 2 * at;
-  float top = kNegInf;
-  for (int w = lane; w < n; w += 64) top = fmaxf(top, ml[2 * w]);
+  float top = lane < n ? own.x : kNegInf;
+  for (int w = lane + 64; w < n; w += 64) top = fmaxf(top, ml[2 * w]);
   top = wave_max(top);
   float sum = 0.0f;
   float2_t o = {0.0f, 0.0f};
-  const float* part = a.part + at * a.head_dim + min(2 * lane, a.head_dim - 2);
   for (int w0 = 0; w0 < n; w0 += 64) {  // 64 splits' factors, one per lane
-    const int w = w0 + lane;
-    const float l = w < n ? ml[2 * w + 1] : 0.0f;
-    const float f = w < n ? scale_of(ml[2 * w], l, top) : 0.0f;
-    sum += wave_sum(l * f);
+    if (w0 > 0) own = *reinterpret_cast<const float2_t*>(ml + 2 * min(w0 + lane, n - 1));
+    const float f = w0 + lane < n ? scale_of(own.x, own.y, top) : 0.0f;
+    sum += wave_sum(w0 + lane < n ? own.y * f : 0.0f);
     const int here = min(64, n - w0);
     for (int i = 0; i < here; i += kMergeLoads) {  // that many rows in flight
-      float2_t x[kMergeLoads];
-#pragma unroll
-      for (int j = 0; j < kMergeLoads; ++j)
-        x[j] = *reinterpret_cast<const float2_t*>(part + static_cast<int64_t>(min(w0 + i + j, n - 1)) * a.head_dim);
+      if (w0 + i > 0) load(w0 + i, x);
 #pragma unroll
       for (int j = 0; j < kMergeLoads; ++j) {
         const float fj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (i + j) & 63));
@@ -698,7 +727,7 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
   }
   const float inv = inv_sum(sum);
   if (2 * lane < a.head_dim)
-    *reinterpret_cast<uint32_t*>(a.out + (s.first + t) * a.o_token + hq * a.o_head + 2 * lane) =
+    *reinterpret_cast<uint32_t*>(a.out + token * a.o_token + hq * a.o_head + 2 * lane) =
         T::pack2(o.x * inv, o.y * inv);
 }
 
@@ -770,8 +799,8 @@ hipError_t launch_t(const TreeArgs& a, int nt, hipStream_t st) {
                        : d == 128 ? launch_pad<T, 128, false>(a, nt, st)
                                   : launch_pad<T, 128, true>(a, nt, st);
   if (e != hipSuccess || a.part == nullptr) return e;
-  hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3((a.max_q * a.q_heads + 3) / 4, a.seqs), dim3(256), 0,
-                     st, a);
+  const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
+  hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

@@ -9,7 +9,7 @@ namespace {
 
 constexpr int64_t kMaxStride = int64_t{1} << 23;  // elements: 128 rows stay below 2^31 bytes
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
-constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 4096, kMaxRows = int64_t{1} << 31;
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 4096, kMaxRows = int64_t{1} << 25;
 constexpr int kMaxHeadDim = 128, kMaxHeads = 4096;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -130,7 +130,8 @@ static int check_tree_sizes(int64_t tokens, int64_t seqs, int64_t table_width, i
   if (max_q > AWQ_TREE_MAX_TOKENS || seqs > 65535 || tokens > kMaxTokens) return AWQ_ERR_UNSUPPORTED;
   if (table_width >= (int64_t{1} << 31) || table_width * page_size >= (int64_t{1} << 30))
     return AWQ_ERR_UNSUPPORTED;
-  // at most 2^21 splits (pages of one position) of 130 floats: the workspace's size fits 64 bits
+  // a wavefront per row in the second launch, which holds 2^32 threads; with at most 2^21
+  // splits (pages of one position) of 130 floats a row the workspace's size fits 64 bits
   if (tokens * q_heads > kMaxRows) return AWQ_ERR_UNSUPPORTED;
   return AWQ_OK;
 }
