@@ -1,9 +1,14 @@
 // Attention of the last (new or drafted) tokens of each sequence over its paged cache
 // (awq_attn_tree in awq_block.h). A handful of query rows read every cached key and value
-// once: the kernel is bound by streaming the cache from memory.
+// once: large calls are bound by streaming the cache from memory (16 sequences of up to 32768
+// positions, 64 heads on 8, D = 128, single tokens: 1.33 GB in 237 us, 5.6 TB/s, more than a
+// copy's reads and writes reach), small ones by the chain of a launch, the sequence, its pages
+// and its first step (one token over 517 positions, 32 heads: 9.2 us; over 16 to 128
+// positions 5-6 us).
 //
 // The query rows that share a key / value head (tokens x heads of the group) are handled
-// together, 16 NT rows per workgroup, so the cache is read once for all of them. The
+// together, so the cache is read once for all of them: up to 16 rows in one workgroup of
+// the kernel described here, more in workgroups of 64 (attn_tree_rows_kernel). The
 // context is split over workgroups, and inside a workgroup over its four wavefronts: each
 // takes every fourth step of 32 positions and runs alone, with a running maximum and sum of
 // its own, its own LDS ring and no barriers, until the four results are merged through LDS.
@@ -12,10 +17,11 @@
 //
 // A step's keys and values go from memory straight into LDS (16 bytes per lane, no
 // registers), one step ahead (every load instruction of a step counts in wait_loads: each
-// row's lanes cover all its chunks, so with D < DP some lane takes part in each). Both products are formed transposed, S^T = K Q^T and
-// O^T = V^T P^T (16 x 16 x 32 matrix instruction): lane l holds the scores of one query
-// (column l % 16), the positions it holds after S^T are the contraction slots it feeds to
-// O^T, and V^T is read from LDS in that order with the transposing 16-bit read.
+// row's lanes cover all its chunks, so with D < DP some lane takes part in each). Both
+// products are formed transposed, S^T = K Q^T and O^T = V^T P^T (16 x 16 x 32 matrix
+// instruction): lane l holds the scores of one query (column l % 16), the positions it holds
+// after S^T are the contraction slots it feeds to O^T, and V^T is read from LDS in that order
+// with the transposing 16-bit read.
 #include "block_internal.hpp"
 
 #include <limits.h>
@@ -29,7 +35,7 @@ namespace {
 
 constexpr int kStep = 32;        // positions per wavefront and step
 constexpr int kWaves = 4;
-constexpr int kStages = 2;
+constexpr int kStages = 2;       // of a wavefront's ring: one in use, one on its way
 constexpr int kMinChunk = kStep * kWaves;  // positions per split: at least this many
 constexpr int kTableEntries = 1024;        // page numbers of a split staged in LDS
 constexpr int kMaxSplits = 64;
@@ -124,24 +130,24 @@ __device__ __forceinline__ void store_row(const TreeArgs& a, int token, int hq, 
 }
 
 // LDS bytes of a workgroup: the rings (later the four float32 results), Q, the page numbers
-template <int DP, int NT>
+template <int DP>
 struct Lds {
   static constexpr int kRow = DP * 2;
   static constexpr int kTile = kStep * kRow;
   static constexpr int kRing = kWaves * kStages * 2 * kTile;
   static constexpr int kSumStride = DP + 4;  // floats: rows 4 banks apart
-  static constexpr int kSums = kWaves * 16 * NT * kSumStride * 4;
+  static constexpr int kSums = kWaves * 16 * kSumStride * 4;
   static constexpr int kBig = kRing > kSums ? kRing : kSums;
-  static constexpr int kQ = 16 * NT * kRow;
-  static constexpr int kStats = kWaves * 16 * NT * 2 * 4;
+  static constexpr int kQ = 16 * kRow;
+  static constexpr int kStats = kWaves * 16 * 2 * 4;
   static constexpr int kTotal = kBig + kQ + kStats + kTableEntries * 4;
 };
 
 // PAD: head_dim < DP
-template <typename T, int DP, int NT, bool PAD>
+template <typename T, int DP, bool PAD>
 __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   typedef typename T::v8 v8;
-  typedef Lds<DP, NT> L;
+  typedef Lds<DP> L;
   constexpr int RB = L::kRow, RC = DP / 8, TILE = L::kTile;
   constexpr int ROWS = 1024 / RB;        // positions one load instruction fills
   constexpr int LOADS = kStep / ROWS;
@@ -154,11 +160,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const int col = lane & 15, g = lane >> 4;
-  const int split = blockIdx.x % a.splits, rb = blockIdx.x / a.splits;
-  const int kv_head = blockIdx.y, b = blockIdx.z;
+  const int split = blockIdx.x, kv_head = blockIdx.y, b = blockIdx.z;
   const Seq s = sequence(a, b);
-  const int r0 = rb * 16 * NT, rows = min(s.count * a.group - r0, 16 * NT);
-  if (rows <= 0) return;
+  const int rows = s.count * a.group;
+  if (rows == 0) return;
   const int chunk = chunk_of(s.len, a.splits);
   const int p0 = split * chunk, p1 = min(s.len, p0 + chunk);
   if (p0 >= p1 && a.part != nullptr) return;  // the second launch knows that it is empty
@@ -169,11 +174,11 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   for (int i = threadIdx.x; i < n_pages; i += 256)
     pages[i] = min(max(a.table[static_cast<int64_t>(b) * a.table_width + t0 + i], 0), a.pages - 1);
   // Q rows (row r: token r / group, head r % group of the key head), 0 past the last
-  for (int i = threadIdx.x; i < 16 * NT * RC; i += 256) {
+  for (int i = threadIdx.x; i < 16 * RC; i += 256) {
     const int r = i / RC, ch = i % RC;
     u32x4 x = {0, 0, 0, 0};
     if (r < rows && 8 * ch < a.head_dim) {
-      const int t = (r0 + r) / a.group, hq = kv_head * a.group + (r0 + r) % a.group;
+      const int t = r / a.group, hq = kv_head * a.group + r % a.group;
       x = *reinterpret_cast<const u32x4*>(a.q + (s.first + t) * a.q_token + hq * a.q_head + 8 * ch);
     }
     *reinterpret_cast<u32x4*>(q_lds + r * RB + 16 * k_pos<DP>(r, ch)) = x;
@@ -185,13 +190,9 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
       *reinterpret_cast<u32x4*>(ring + 16 * i) = u32x4{0, 0, 0, 0};
     __builtin_amdgcn_s_waitcnt(0);
   }
-  uint64_t sees[NT];  // this lane's rows' masks over the new tokens
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = 16 * n + col;
-    const int t = min((r0 + r) / a.group, max(s.count - 1, 0));
-    sees[n] = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
-  }
+  // this lane's row's mask over the new tokens
+  const int own = min(col / a.group, s.count - 1);
+  const uint64_t sees = a.mask != nullptr ? a.mask[s.first + own] : (2ull << own) - 1;
   __syncthreads();
 
   const uint16_t* kbase = a.k + kv_head * a.cache_head;
@@ -223,15 +224,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     }
   };
 
-  float4_t acc[NT][ND];
-  float m[NT], l[NT];
+  float4_t acc[ND];
+  float m = kNegInf, l = 0.0f;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    m[n] = kNegInf;
-    l[n] = 0.0f;
-#pragma unroll
-    for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  }
+  for (int d = 0; d < ND; ++d) acc[d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   // One step is used while the next is on its way, and the addresses of the one after that
   // are found meanwhile.
@@ -268,56 +264,50 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
         const int r = 16 * t + col;
         kf[t][c] = *reinterpret_cast<const v8*>(ks + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
       }
-    u32x4 p[NT];
+    float4_t sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float4_t sc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int r = 16 * n + col;
-        const v8 qf = *reinterpret_cast<const v8*>(q_lds + r * RB + 16 * k_pos<DP>(r, 4 * c + g));
-        sc[0] = T::mfma16(kf[0][c], qf, sc[0]);
-        sc[1] = T::mfma16(kf[1][c], qf, sc[1]);
-      }
-      if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
-        const uint32_t bits = visible(sees[n], s0 - s.ctx, p1 - s0) >> (4 * g);
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][i] = (bits & (1u << (16 * t + i))) != 0 ? sc[t][i] : kNegInf;
-      }
-      float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
-                        fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * a.c;
-      if (__ballot(top > m[n] + kSlack) != 0) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        const float m_new = fmaxf(m[n], top);
-        const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m[n] - m_new);
-        m[n] = m_new;
-        l[n] *= keep;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[n][d] *= keep;
-      }
-      const float off = m[n] == kNegInf ? 0.0f : kShift - m[n];
+    for (int c = 0; c < NC; ++c) {
+      const v8 qf = *reinterpret_cast<const v8*>(q_lds + col * RB + 16 * k_pos<DP>(col, 4 * c + g));
+      sc[0] = T::mfma16(kf[0][c], qf, sc[0]);
+      sc[1] = T::mfma16(kf[1][c], qf, sc[1]);
+    }
+    if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
+      const uint32_t bits = visible(sees, s0 - s.ctx, p1 - s0) >> (4 * g);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.c, off));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i + 1], a.c, off));
-          l[n] += e0 + e1;
-          p[n][2 * t + (i >> 1)] = T::pack2(e0, e1);
-        }
+        for (int i = 0; i < 4; ++i) sc[t][i] = (bits & (1u << (16 * t + i))) != 0 ? sc[t][i] : kNegInf;
     }
+    float top = fmaxf(fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[0][2], sc[0][3])),
+                      fmaxf(fmaxf(sc[1][0], sc[1][1]), fmaxf(sc[1][2], sc[1][3]))) * a.c;
+    if (__ballot(top > m + kSlack) != 0) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float m_new = fmaxf(m, top);
+      const float keep = m_new == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - m_new);
+      m = m_new;
+      l *= keep;
+#pragma unroll
+      for (int d = 0; d < ND; ++d) acc[d] *= keep;
+    }
+    const float off = m == kNegInf ? 0.0f : kShift - m;
+    u32x4 p;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.c, off));
+        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i + 1], a.c, off));
+        l += e0 + e1;
+        p[2 * t + (i >> 1)] = T::pack2(e0, e1);
+      }
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-      const int ra = 4 * g + (col >> 2), rb2 = ra + 16;
+      const int ra = 4 * g + (col >> 2), rb = ra + 16;
       const int ch = 2 * d + ((col & 3) >> 1), byte = 8 * (col & 1);
       const short4_t lo = lds_read_tr(vs + ra * RB + 16 * v_pos<DP>(ra, ch) + byte);
-      const short4_t hi = lds_read_tr(vs + rb2 * RB + 16 * v_pos<DP>(rb2, ch) + byte);
-      const v8 vf = join8<v8>(lo, hi);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) acc[n][d] = T::mfma16(vf, __builtin_bit_cast(v8, p[n]), acc[n][d]);
+      const short4_t hi = lds_read_tr(vs + rb * RB + 16 * v_pos<DP>(rb, ch) + byte);
+      acc[d] = T::mfma16(join8<v8>(lo, hi), __builtin_bit_cast(v8, p), acc[d]);
     }
     asm volatile("" ::: "memory");
   };
@@ -327,46 +317,41 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   }
 
   // merge the four wavefronts: maxima, then the rows brought to the common maximum
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    l[n] += __shfl_xor(l[n], 16);
-    l[n] += __shfl_xor(l[n], 32);
-    if (g == 0) {
-      stats[(wave * 16 * NT + 16 * n + col) * 2] = m[n];
-      stats[(wave * 16 * NT + 16 * n + col) * 2 + 1] = l[n];
-    }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    stats[(wave * 16 + col) * 2] = m;
+    stats[(wave * 16 + col) * 2 + 1] = l;
   }
   __syncthreads();  // also: every ring is done with
   float* sums = reinterpret_cast<float*>(smem);
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const int r = 16 * n + col;
+  {
     float top = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 * NT + r) * 2]);
-    const float f = scale_of(m[n], l[n], top);
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 + col) * 2]);
+    const float f = scale_of(m, l, top);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
-      *reinterpret_cast<float4_t*>(sums + (wave * 16 * NT + r) * L::kSumStride + 16 * d + 4 * g) = acc[n][d] * f;
+      *reinterpret_cast<float4_t*>(sums + (wave * 16 + col) * L::kSumStride + 16 * d + 4 * g) = acc[d] * f;
   }
   __syncthreads();
   // one wavefront per row: lane i has d = 2 i, 2 i + 1
   for (int r = wave; r < rows; r += kWaves) {
     float top = kNegInf, sum = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 * NT + r) * 2]);
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stats[(w * 16 + r) * 2]);
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
-      const float mw = stats[(w * 16 * NT + r) * 2], lw = stats[(w * 16 * NT + r) * 2 + 1];
+      const float mw = stats[(w * 16 + r) * 2], lw = stats[(w * 16 + r) * 2 + 1];
       sum += lw * scale_of(mw, lw, top);
     }
     float2_t o = {0.0f, 0.0f};
     if (2 * lane < DP) {
 #pragma unroll
       for (int w = 0; w < kWaves; ++w)
-        o += *reinterpret_cast<const float2_t*>(sums + (w * 16 * NT + r) * L::kSumStride + 2 * lane);
+        o += *reinterpret_cast<const float2_t*>(sums + (w * 16 + r) * L::kSumStride + 2 * lane);
     }
-    const int t = (r0 + r) / a.group, hq = kv_head * a.group + (r0 + r) % a.group;
+    const int t = r / a.group, hq = kv_head * a.group + r % a.group;
     // a row that came out NaN though its probabilities' sum is not: again, key by key (a
     // masked infinity or NaN may be the cause)
     if (sum == sum && __ballot(o.x != o.x || o.y != o.y) != 0) {
@@ -385,11 +370,15 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   }
 }
 
-// The same for many query rows (more than 32 of a key / value head): 64 rows per workgroup,
+// The same for more query rows, or more workgroups than run at once: 64 rows per workgroup,
 // 64 positions per step, in LDS for all four wavefronts; each takes 32 of the rows and 32 of
 // the positions, so that a fragment of K or V read from LDS serves two row tiles. The
 // wavefronts keep their Q operands in registers and the two halves of the positions meet at
-// the end; 64 KiB of LDS let two workgroups share a CU.
+// the end; 64 KiB of LDS let two workgroups share a CU. Eight sequences of 0 to 4096 positions
+// and 1 to 32 drafted tokens, 32 heads on 8 (58 MB of cache): 22.5 us and 5 us for the second
+// launch; 64 sequences of 512 positions with 16 tokens each 29 us, 5.2 TB/s. (A
+// wavefront on 16 rows and all positions, with loads that the compiler waited for, took 35 and
+// 112 us where this takes 26 and 48: 8 and 32 sequences of 2048 positions, 16 tokens each.)
 constexpr int kRowStep = 64;
 constexpr int kRowTiles = 2;  // of 16 rows, per wavefront
 
@@ -731,9 +720,14 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
         T::pack2(o.x * inv, o.y * inv);
 }
 
-// Row tiles per workgroup: one or two of 16 rows, shared by the wavefronts, where they hold
-// all rows of a sequence; else four, one per wavefront.
-int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kWaves; }
+// Which of the two kernels: 64 rows per workgroup for more than 16 rows (24 and 32 rows, 512
+// positions, 64 sequences, 8 key heads: 27 us; two tiles of 16 in the other kernel 34, 36), and
+// for fewer where the other's workgroups, one per CU (two up to D = 64), would not all run at
+// once (4 and 16 rows: 256 sequences of 16 positions 23, 26 us, the other 30, 43; 64 of 512 26,
+// 26 and 27, 30; but 16 of 2048, which do, 31, 32 and 27, 29).
+bool by_rows(int64_t max_rows, int64_t seqs, int32_t kv_heads, int32_t head_dim) {
+  return max_rows > 16 || seqs * kv_heads > (head_dim <= 64 ? 512 : 256);
+}
 
 // Splits of the longest context the table holds, by what a call is expected to take (us, from
 // timelines on MI355X): a workgroup's fixed time (finding its sequence, its pages and the
@@ -743,11 +737,11 @@ int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : kWaves; }
 // most as many pages as a workgroup stages.
 int pick_splits(int64_t tokens, int64_t seqs, int64_t max_len, int32_t page_size, int64_t max_rows, int32_t q_heads,
                 int32_t kv_heads, int32_t head_dim) {
-  const bool by_rows = row_tiles(max_rows) == kWaves;
-  const double slots = by_rows ? 512.0 : 256.0;  // workgroups that run at once
-  const double fixed = 4.0, per = (by_rows ? 1.1 / 64 : 0.9 / 128) * (head_dim <= 64 ? 0.6 : 1.0);
+  const bool many = by_rows(max_rows, seqs, kv_heads, head_dim);
+  const double slots = many ? 512.0 : 256.0;  // workgroups that run at once
+  const double fixed = 4.0, per = (many ? 1.1 / 64 : 0.9 / 128) * (head_dim <= 64 ? 0.6 : 1.0);
   // workgroups per split: sequences of few rows need one row block, long ones several
-  const double blocks = by_rows ? static_cast<double>(tokens) * (q_heads / kv_heads) / 64 + 0.5 * seqs : seqs;
+  const double blocks = many ? static_cast<double>(tokens) * (q_heads / kv_heads) / 64 + 0.5 * seqs : seqs;
   const double groups = kv_heads * (blocks > seqs ? blocks : seqs);
   const double merged = static_cast<double>(tokens) * q_heads * head_dim * 8;  // bytes per split, both ways
   const int64_t limit = static_cast<int64_t>(kTableEntries - 1) * page_size / kMinChunk * kMinChunk;
@@ -778,26 +772,22 @@ hipError_t launch_kernel(Kernel kernel, std::atomic<uint64_t>& lds_done, int lds
 }
 
 template <typename T, int DP, bool PAD>
-hipError_t launch_pad(const TreeArgs& a, int nt, hipStream_t st) {
-  if (nt == 1) {
+hipError_t launch_pad(const TreeArgs& a, bool many, hipStream_t st) {
+  if (!many) {
     static std::atomic<uint64_t> done{0};
-    return launch_kernel(&attn_tree_kernel<T, DP, 1, PAD>, done, Lds<DP, 1>::kTotal, a, st);
-  }
-  if (nt == 2) {
-    static std::atomic<uint64_t> done{0};
-    return launch_kernel(&attn_tree_kernel<T, DP, 2, PAD>, done, Lds<DP, 2>::kTotal, a, st);
+    return launch_kernel(&attn_tree_kernel<T, DP, PAD>, done, Lds<DP>::kTotal, a, st);
   }
   static std::atomic<uint64_t> done{0};
   return launch_kernel(&attn_tree_rows_kernel<T, DP, PAD>, done, 4 * kRowStep * DP * 2 + kTableEntries * 4, a, st);
 }
 
 template <typename T>
-hipError_t launch_t(const TreeArgs& a, int nt, hipStream_t st) {
+hipError_t launch_t(const TreeArgs& a, bool many, hipStream_t st) {
   const int d = a.head_dim;
-  const hipError_t e = d == 64    ? launch_pad<T, 64, false>(a, nt, st)
-                       : d < 64   ? launch_pad<T, 64, true>(a, nt, st)
-                       : d == 128 ? launch_pad<T, 128, false>(a, nt, st)
-                                  : launch_pad<T, 128, true>(a, nt, st);
+  const hipError_t e = d == 64    ? launch_pad<T, 64, false>(a, many, st)
+                       : d < 64   ? launch_pad<T, 64, true>(a, many, st)
+                       : d == 128 ? launch_pad<T, 128, false>(a, many, st)
+                                  : launch_pad<T, 128, true>(a, many, st);
   if (e != hipSuccess || a.part == nullptr) return e;
   const int64_t rows = static_cast<int64_t>(a.tokens) * a.q_heads;
   hipLaunchKernelGGL(attn_tree_merge_kernel<T>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(256), 0, st, a);
@@ -851,12 +841,12 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   a.head_dim = g.head_dim;
   a.c = g.scale * kLog2e;
   const int64_t rows = static_cast<int64_t>(g.max_q) * a.group;
-  const int nt = row_tiles(rows);
-  a.row_blocks = static_cast<int32_t>((rows + 16 * nt - 1) / (16 * nt));
+  const bool many = by_rows(rows, g.seqs, g.kv_heads, g.head_dim);
+  a.row_blocks = static_cast<int32_t>(many ? (rows + 63) / 64 : 1);
   a.splits = attn_tree_splits(g.tokens, g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads,
                               g.head_dim);
   a.part = a.splits > 1 ? static_cast<float*>(g.ws) : nullptr;
-  return g.dtype == AWQ_DT_F16 ? launch_t<F16>(a, nt, st) : launch_t<BF16>(a, nt, st);
+  return g.dtype == AWQ_DT_F16 ? launch_t<F16>(a, many, st) : launch_t<BF16>(a, many, st);
 }
 
 }  // namespace awq

@@ -2,14 +2,16 @@
 // (awq_rope in awq_block.h).
 //
 // Three multiply-adds per element: the kernel is bound by reading and writing each element
-// once. A thread owns one chunk position of the head (V first elements and V second
+// once (671 MB of 16384 tokens x 72 heads in 146 us, 4.6 TB/s; 50 MB of 2048 tokens x 48
+// heads in 10.6 us, 4.7 TB/s; a large copy moves 4.95 TB/s; one token of 96 heads 3.6 us, the
+// launch and two memory round trips). A thread owns one chunk position of the head (V first elements and V second
 // elements of V pairs: 16 + 16 bytes) of one token, forms the V cosines and sines once, and
 // walks over a share of the heads with them, so the trigonometry is paid once per token
 // and share and not per head.
 //
 // The angle in turns, positions * inv_freq / (2 pi), is formed and reduced to [-1/2, 1/2] in
 // float64: at position 10^5 a float32 product would be off by up to 0.004 rad. The hardware
-// sine and cosine take turns.
+// sine and cosine take turns; at most 8 of them per thread, they hide behind the loads.
 #include "block_internal.hpp"
 
 namespace awq {
@@ -151,7 +153,9 @@ hipError_t launch_v(const awq_rope_args& a, hipStream_t st) {
   const int chunks = a.rot_dim / (2 * V) + (a.head_dim - a.rot_dim) / V;
   const int64_t blocks = (a.tokens * chunks + 255) / 256;
   const int rows = a.q_heads + 2 * a.kv_heads;
-  // heads per thread: enough threads to fill the chip first, then up to 8
+  // heads per thread: enough threads to fill the chip first, then up to 8 for one set of
+  // cosines (1, 4, 8, 16 heads: one token 4.1, 4.8, 6.7, 10.5 us; 2048 tokens x 48 heads 12.7,
+  // 10.7, 12.3, 17.4; 16384 tokens x 72 heads 157, 149, 145, 167)
   const int64_t share = blocks * rows / 2048;
   const int per = share < 1 ? 1 : share > 8 ? 8 : static_cast<int>(share);
   const int64_t z = (blocks + (1 << 23) - 1) >> 23;

@@ -449,6 +449,16 @@ def test_tree_masked_tokens_never_reach_a_row(dtype, bad):
         assert bool(torch.isnan(out[[2, 4, 8, 10]]).all())
 
 
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("count,hq,hkv,d,longest", [(140, 4, 2, 128, 60), (270, 2, 1, 72, 300), (300, 2, 2, 64, 40)])
+def test_tree_batches_of_many_sequences(dtype, count, hq, hkv, d, longest):
+    """More workgroups than run at once, with a few rows each; empty sequences among them."""
+    g = torch.Generator().manual_seed(count)
+    ctx = torch.randint(0, longest, (count,), generator=g).tolist()
+    drafts = torch.randint(0, 4, (count,), generator=g).tolist()
+    run_tree(ctx, drafts, hq, hkv, d, 16, dtype, seed=count)
+
+
 def test_tree_many_splits():
     """One sequence over a wide table of single-position pages: more splits than a wavefront
     has lanes, most of them empty for the short sequence beside it."""
