@@ -24,7 +24,7 @@
 // wavefronts of a SIMD. One sequence of 8192 tokens, 32 heads on 8, D = 128: 551 us, 1.0
 // PFLOP/s of the triangle's products (a large matrix product reaches 1.3); six ragged
 // prompts of 1 to 2048 tokens (bfloat16) 110-120 us, 0.70-0.76 PFLOP/s (the last tiles and the
-// diagonals); 128 tokens 8.3 us, of which the launch and the first tile's way from memory are
+// diagonals); five of 1 to 120 tokens 8.3 us, of which the launch and the first tile's way from memory are
 // most. 64 keys and 128 rows leave 104 registers and 64 KiB of LDS, two workgroups per CU;
 // 256 rows were 1.5 % faster on the long sequence and 10 % slower on the ragged ones.
 #include "block_internal.hpp"
