@@ -33,13 +33,16 @@ _WS = {}
 
 def _workspace(need: int, index: int) -> torch.Tensor:
     """A workspace of at least `need` bytes, cached per device and stream and grown on
-    demand, as awq.workspace."""
+    demand. A buffer that a larger one replaces is kept: a graph captured with it goes on
+    writing to it (each is at least twice the one before, so they come to no more than the
+    last). Graphs captured on one stream share it and must not be replayed side by side;
+    calls that may be take a `ws` of their own."""
     key = (index, awq._stream(index))
-    cur = _WS.get(key)
-    if cur is None or cur.numel() < need:
-        cur = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=torch.device("cuda", index))
-        _WS[key] = cur
-    return cur
+    kept = _WS.setdefault(key, [])
+    if not kept or kept[-1].numel() < need:
+        size = max(need, 2 * kept[-1].numel() if kept else 1 << 20)
+        kept.append(torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", index)))
+    return kept[-1]
 
 
 _block.setup(awq._stream, _workspace, awq.AwqError)

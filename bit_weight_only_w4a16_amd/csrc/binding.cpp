@@ -22,6 +22,12 @@ PyObject *g_error = nullptr;      // AwqError(status, function)
 
 struct Refused {};  // thrown with a Python error set
 
+// A reference that ends with its scope
+struct Owned {
+  PyObject* object = nullptr;
+  ~Owned() { Py_XDECREF(object); }
+};
+
 [[noreturn]] void refuse(PyObject* kind, const char* format, const char* name) {
   PyErr_Format(kind, format, name);
   throw Refused{};
@@ -288,21 +294,20 @@ PyObject* attn_tree(PyObject* const* in, Py_ssize_t n) {
   a.scale = in[8] == Py_None ? 1.0f / std::sqrt(static_cast<float>(a.head_dim)) : static_cast<float>(number(in[8]));
   at::Tensor out = output(in[9], "out", q);
   a.out = call.packed<void>(out, "out", a.o_token, a.o_head);
-  PyObject* made = nullptr;
+  Owned made;  // until the launch: without the GIL another thread may have it replaced
   if (ws == nullptr) {
     const size_t need = awq_attn_tree_workspace_bytes(a.tokens, a.seqs, a.table_width, a.page_size, a.max_q,
                                                       a.q_heads, a.kv_heads, a.head_dim);
     if (need > 0) {
-      made = PyObject_CallFunction(g_workspace, "nL", static_cast<Py_ssize_t>(need), static_cast<long long>(call.device));
-      if (made == nullptr) throw Refused{};
-      ws = &THPVariable_Unpack(made);
+      made.object = PyObject_CallFunction(g_workspace, "nL", static_cast<Py_ssize_t>(need), static_cast<long long>(call.device));
+      if (made.object == nullptr) throw Refused{};
+      ws = &THPVariable_Unpack(made.object);
     }
   }
   if (ws != nullptr) {
     a.ws = call.vector<void>(ws, "ws", at::kByte, {-1});
     a.ws_bytes = static_cast<size_t>(ws->size(0));
   }
-  Py_XDECREF(made);  // the cache of workspaces keeps it
   const hipStream_t stream = call.stream();
   run("awq_attn_tree", [&] { return awq_attn_tree(&a, stream); });
   return THPVariable_Wrap(out);

@@ -568,6 +568,32 @@ def test_another_stream_and_a_graph():
             assert torch.equal(a, b), i
 
 
+def test_a_graph_keeps_its_workspace():
+    """A call that grows the stream's workspace after a graph was captured with the smaller
+    one: what is allocated then is not what the graph writes to."""
+    stream = torch.cuda.Stream()
+    small, large = (tree_inputs([n], [t], 8, 1, 128, 16, F16, seed=n) for n, t in ((4000, 1), (9000, 40)))
+
+    need = [block.awq_attn_tree_workspace_bytes(t, 1, x[3].shape[1], 16, t, 8, 1, 128) for x, t in ((small, 1), (large, 40))]
+    assert 0 < need[0] < (1 << 20) < need[1]
+    with torch.cuda.stream(stream):
+        n1, cu1, n2, cu2 = i32([4000]), cumulative([1]), i32([9000]), cumulative([40])
+        want = block.awq_attn_tree(*small, n1, cu1, 1)
+        graph = torch.cuda.CUDAGraph()
+        stream.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            out = block.awq_attn_tree(*small, n1, cu1, 1)
+        block.awq_attn_tree(*large, n2, cu2, 40)
+        others = [torch.full((1 << 20,), 77, dtype=torch.uint8, device=DEV) for _ in range(8)]
+        for _ in range(3):
+            out.zero_()
+            graph.replay()
+            stream.synchronize()
+            assert torch.equal(out, want)
+            assert all(bool((x == 77).all()) for x in others)
+
+
+
 # ---------------------------------------------------------------------------- refusals
 
 def test_binding_refusals():
