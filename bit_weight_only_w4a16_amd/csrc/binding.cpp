@@ -2,7 +2,7 @@
 // checks its tensors, forms the argument structure and calls the C entry point on PyTorch's
 // current stream. A decode step makes these calls for every layer, and their kernels take a
 // few microseconds: checked and marshalled in Python, a call costs 9 to 13 us of host time,
-// here 4 to 6 (MI355X host). block.py holds the signatures and the documentation.
+// here 5 to 8 (MI355X host). block.py holds the signatures and the documentation.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
