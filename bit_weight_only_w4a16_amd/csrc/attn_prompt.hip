@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
     const int t = wq0 + i;
     float mr, lr;
     float2_t orow;
-    attend_row<T>(a.q + (start + t) * a.q_token + head * a.q_head, a.head_dim, a.c, 0, t + 1,
+    attend_row<T>(a.q + (start + t) * a.q_token + head * a.q_head, a.head_dim, a.c, 0, t + 1, kShift,
                   [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
                     kr = kbase + j * a.k_token;
                     vr = vbase + j * a.v_token;

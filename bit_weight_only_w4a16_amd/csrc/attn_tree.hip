@@ -92,7 +92,8 @@ __device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
   return left < 32 ? bits & ((1u << left) - 1u) : bits;
 }
 
-// The factor that brings a partial result with maximum m and sum l to the maximum top. A
+// The factor that brings a partial result with maximum m and sum l to the maximum top (sums
+// and rows of every part carry 2^kShift, those of rows done key by key too). A
 // part that saw no finite score (m = -inf) has l = 0, or NaN if it saw a NaN, and passes
 // that on.
 __device__ __forceinline__ float scale_of(float m, float l, float top) {
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     // masked infinity or NaN may be the cause)
     if (sum == sum && __ballot(o.x != o.x || o.y != o.y) != 0) {
       const uint64_t bits = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
-      attend_row<T>(a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, p0, p1,
+      attend_row<T>(a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, p0, p1, kShift,
                     [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
                       const int64_t at = offset_of(static_cast<int>(j));
                       kr = kbase + at;
@@ -632,7 +633,7 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
       const uint64_t bits = a.mask != nullptr ? a.mask[s.first + tr] : (2ull << tr) - 1;
       float row_top, sum;
       float2_t o;
-      attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1,
+      attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1, kShift,
                     [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
                       const int64_t off = offset_of(static_cast<int>(j));
                       kr = kbase + off;

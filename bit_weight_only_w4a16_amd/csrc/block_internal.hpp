@@ -168,7 +168,8 @@ __device__ __forceinline__ float wave_sum(float v) {
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
 // One row of attention by one wavefront, key by key, in float32: the running maximum m and
-// sum l (base 2, of exponents q.k * c) and, in lane i, o for d = 2 i, 2 i + 1. Keys that the
+// sum l (base 2, of exponents q.k * c) and, in lane i, o for d = 2 i, 2 i + 1. l and o carry
+// the factor 2^shift of the matrix kernels' own, with which they may be added to theirs. Keys that the
 // row does not see are skipped, not multiplied by zero, so nothing in them reaches the row.
 // The matrix kernels multiply masked probabilities of exactly 0 with whatever the masked
 // value row holds; where that is an infinity or NaN the row comes out NaN, and the kernels
@@ -177,8 +178,8 @@ __device__ __forceinline__ float inv_sum(float l) { return l == 0.0f ? 0.0f : 1.
 // row sees it.
 template <typename T, typename Key>
 __device__ __forceinline__ void attend_row(const uint16_t* q, int head_dim, float c, int64_t first,
-                                        int64_t end, Key key, float& m_out, float& l_out,
-                                        float2_t& o_out) {
+                                        int64_t end, float shift, Key key, float& m_out,
+                                        float& l_out, float2_t& o_out) {
   const int lane = threadIdx.x & 63;
   float m = kNegInf, l = 0.0f;
   float2_t o = {0.0f, 0.0f};
@@ -194,7 +195,7 @@ __device__ __forceinline__ void attend_row(const uint16_t* q, int head_dim, floa
     }
     const float m_new = fmaxf(m, wave_max(s));
     const float base = m_new == kNegInf ? 0.0f : m_new;
-    const float p = sees ? __builtin_amdgcn_exp2f(s - base) : 0.0f;
+    const float p = sees ? __builtin_amdgcn_exp2f(s - base + shift) : 0.0f;
     const float keep = __builtin_amdgcn_exp2f(m - base);
     l = l * keep + wave_sum(p);
     o *= keep;
