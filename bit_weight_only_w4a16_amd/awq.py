@@ -367,24 +367,27 @@ def awq_gemv_chain(layers, state: torch.Tensor):
 _WS = {}
 
 
+def scratch(need: int, index: int) -> torch.Tensor:
+    """A workspace of at least `need` bytes on device `index`, cached per device and stream
+    and grown on demand (the library overwrites what it uses on every call, so no
+    initialisation is needed). Calls that share a workspace must be ordered; keying the cache
+    by the current stream keeps calls on different streams on different buffers. A buffer
+    that a larger one replaces is kept: a graph captured with it goes on writing to it (each
+    is at least twice the one before, so they come to no more than the last)."""
+    kept = _WS.setdefault((index, _stream(index)), [])
+    if not kept or kept[-1].numel() < need:
+        size = max(need, 2 * kept[-1].numel() if kept else 1 << 20)
+        kept.append(torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", index)))
+    return kept[-1]
+
+
 def workspace(m: int, n: int, k: int, device, group: int = GROUP) -> torch.Tensor | None:
-    """A workspace large enough for (m, n, k), cached per device and per stream and grown
-    on demand (the library overwrites what it uses on every call, so no initialisation
-    is needed). Calls that share a workspace must be ordered; keying the cache by the
-    current stream keeps layers called on different streams on different buffers. A
-    buffer replaced by a larger one goes back to PyTorch's caching allocator, which hands
-    its memory out again only in the order of that stream."""
+    """The cached workspace (`scratch`) for a product of (m, n, k), None where none is used."""
     need = awq_workspace_bytes(m, n, k, group)
     if need == 0:
         return None
     dev = torch.device(device)
-    index = dev.index if dev.index is not None else torch.cuda.current_device()
-    key = (dev.type, index, _stream(index))
-    cur = _WS.get(key)
-    if cur is None or cur.numel() < need:
-        cur = torch.empty(max(need, 1 << 20), dtype=torch.uint8, device=dev)
-        _WS[key] = cur
-    return cur
+    return scratch(need, dev.index if dev.index is not None else torch.cuda.current_device())
 
 
 class QuantLinear:

@@ -28,24 +28,7 @@ ACTS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 TREE_MAX_TOKENS = 64
 EXPORTS = ("awq_attn_prompt", "awq_attn_tree", "awq_attn_tree_workspace_bytes", "awq_gemm_fused", "awq_rope")
 
-_WS = {}
-
-
-def _workspace(need: int, index: int) -> torch.Tensor:
-    """A workspace of at least `need` bytes, cached per device and stream and grown on
-    demand. A buffer that a larger one replaces is kept: a graph captured with it goes on
-    writing to it (each is at least twice the one before, so they come to no more than the
-    last). Graphs captured on one stream share it and must not be replayed side by side;
-    calls that may be take a `ws` of their own."""
-    key = (index, awq._stream(index))
-    kept = _WS.setdefault(key, [])
-    if not kept or kept[-1].numel() < need:
-        size = max(need, 2 * kept[-1].numel() if kept else 1 << 20)
-        kept.append(torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", index)))
-    return kept[-1]
-
-
-_block.setup(awq._stream, _workspace, awq.AwqError)
+_block.setup(awq._stream, awq.scratch, awq.AwqError)
 
 
 def awq_gemm_fused(x, inv_s_c, packed, n: int, k: int, group: int = awq.GROUP, fmt: int = awq.FMT_ASYM, *,
