@@ -367,14 +367,30 @@ def awq_gemv_chain(layers, state: torch.Tensor):
 _WS = {}
 
 
+def _capturing(index: int) -> bool:
+    """Whether the current stream of a device is being captured into a graph."""
+    if index == torch._C._cuda_getDevice():
+        return torch._C._cuda_isCurrentStreamCapturing()
+    with torch.cuda.device(index):
+        return torch._C._cuda_isCurrentStreamCapturing()
+
+
 def scratch(need: int, index: int) -> torch.Tensor:
-    """A workspace of at least `need` bytes on device `index`, cached per device and stream
-    and grown on demand (the library overwrites what it uses on every call, so no
-    initialisation is needed). Calls that share a workspace must be ordered; keying the cache
-    by the current stream keeps calls on different streams on different buffers. A buffer
-    that a larger one replaces is kept: a graph captured with it goes on writing to it (each
-    is at least twice the one before, so they come to no more than the last)."""
-    kept = _WS.setdefault((index, _stream(index)), [])
+    """A workspace of at least `need` bytes on device `index` (the library overwrites what it
+    uses on every call, so no initialisation is needed).
+
+    While the current stream is captured into a graph: a new one from the graph's memory, so
+    that graphs captured on one stream may be replayed side by side. Else one that is cached
+    per device and stream and grown on demand; calls that share it must be ordered, and
+    calls on one stream are. One that a larger one replaces is kept, for a caller may have
+    captured a graph with it (each is at least twice the one before, so they come to no more
+    than the last)."""
+    if _capturing(index):
+        return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    key = (index, _stream(index))
+    kept = _WS.get(key)
+    if kept is None:
+        kept = _WS.setdefault(key, [])
     if not kept or kept[-1].numel() < need:
         size = max(need, 2 * kept[-1].numel() if kept else 1 << 20)
         kept.append(torch.empty(size, dtype=torch.uint8, device=torch.device("cuda", index)))
@@ -382,7 +398,7 @@ def scratch(need: int, index: int) -> torch.Tensor:
 
 
 def workspace(m: int, n: int, k: int, device, group: int = GROUP) -> torch.Tensor | None:
-    """The cached workspace (`scratch`) for a product of (m, n, k), None where none is used."""
+    """The workspace (`scratch`) for a product of (m, n, k), None where none is used."""
     need = awq_workspace_bytes(m, n, k, group)
     if need == 0:
         return None
