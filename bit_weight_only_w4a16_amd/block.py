@@ -124,7 +124,7 @@ def awq_attn_tree(q, k_cache, v_cache, block_table, ctx_lens, cu_q, max_q: int, 
     most new tokens of a sequence (<= 64). mask int64 [tokens]: bit j of a token's word lets
     it see new token j of its sequence (`tree_mask` forms it from a tree); without one, new
     tokens see those up to themselves. A token that sees nothing gets zeros. ws: uint8,
-    awq_attn_tree_workspace_bytes() of them; when absent, the stream's cached one or, under
+    awq_attn_tree_workspace_bytes() of them; when absent, one cached per stream and thread or, under
     capture, one of the graph's own (awq.scratch). Graphs captured with the same ws must not be
     replayed side by side."""
     return _block.attn_tree(q, k_cache, v_cache, block_table, ctx_lens, cu_q, max_q, mask, scale, out, ws)

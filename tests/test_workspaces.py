@@ -1,5 +1,6 @@
 """The workspaces that the binding caches: which calls share one, and how long it lives."""
 import os
+import threading
 import weakref
 
 import pytest
@@ -40,6 +41,26 @@ def test_every_captured_call_has_a_workspace_of_its_own(on_host, monkeypatch):
     assert awq.scratch(100, 0) is not first
     monkeypatch.setattr(awq, "_capturing", lambda index: False)
     assert awq.scratch(100, 0) is eager
+
+
+def test_threads_on_one_stream_have_workspaces_of_their_own(on_host):
+    """The launches of one call that uses a workspace may stand between those of another's."""
+    inside, together = {}, threading.Barrier(2)
+
+    def call(name):
+        first = awq.scratch(100, 0)
+        together.wait()   # (both threads live: their numbers differ)
+        inside[name] = (first, awq.scratch(50, 0), awq.workspace(64, 4096, 4096, "cuda:0"))
+        together.wait()
+
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert inside[i][0] is inside[i][1]
+    assert len({t.data_ptr() for i in range(2) for t in inside[i]}) == 4
 
 
 @pytest.mark.gpu
