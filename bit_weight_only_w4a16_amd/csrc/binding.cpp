@@ -71,7 +71,8 @@ struct Call {
     if (!t->is_contiguous()) refuse(PyExc_ValueError, "%s must be contiguous", name);
     return static_cast<T*>(t->data_ptr());
   }
-  // a packed operand [tokens, heads, D]; a dimension of one has no stride that matters
+  // a packed operand [tokens, heads, D]; a dimension of one has no stride that matters (one
+  // token cut out of a long tensor keeps that tensor's)
   template <typename T>
   T* packed(const at::Tensor& t, const char* name, int64_t& token, int64_t& head) const {
     on_device(t, name);
@@ -79,7 +80,7 @@ struct Call {
     if (t.dim() != 3) refuse(PyExc_ValueError, "%s must be [tokens, heads, head_dim]", name);
     if (t.stride(2) != 1) refuse(PyExc_ValueError, "the elements of a head of %s must be contiguous", name);
     head = t.size(1) > 1 ? t.stride(1) : t.size(2);
-    token = t.size(0) > 1 ? t.stride(0) : std::max(t.stride(0), t.size(1) * t.size(2));
+    token = t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);
     return static_cast<T*>(t.data_ptr());
   }
   // a paged cache [pages, kv_heads, page_size, D] of two tensors with one layout
@@ -91,15 +92,16 @@ struct Call {
     if (v.scalar_type() != dtype) refuse(PyExc_TypeError, "%s has another type than the other operands", "v_cache");
     if (k.dim() != 4 || k.size(1) != heads || k.size(3) != d)
       refuse(PyExc_ValueError, "%s must be [pages, kv_heads, page_size, head_dim]", "k_cache");
-    if (k.sizes() != v.sizes() || k.strides() != v.strides())
-      refuse(PyExc_ValueError, "%s must have k_cache's shape and layout", "v_cache");
+    bool same = k.sizes() == v.sizes();
+    for (int i = 0; same && i < 4; ++i) same = k.size(i) <= 1 || k.stride(i) == v.stride(i);
+    if (!same) refuse(PyExc_ValueError, "%s must have k_cache's shape and layout", "v_cache");
     if (k.stride(3) != 1) refuse(PyExc_ValueError, "the elements of a slot of %s must be contiguous", "k_cache");
     if (k.size(2) > INT32_MAX) refuse(PyExc_ValueError, "%s has too large pages", "k_cache");
     pages = k.size(0);
     page_size = static_cast<int32_t>(k.size(2));
-    page = k.stride(0);
-    head = k.stride(1);
-    slot = page_size > 1 ? k.stride(2) : std::max(k.stride(2), d);
+    page = pages > 1 ? k.stride(0) : 0;
+    head = heads > 1 ? k.stride(1) : 0;
+    slot = page_size > 1 ? k.stride(2) : d;
   }
   hipStream_t stream() const {
     PyObject* index = PyLong_FromLongLong(device);

@@ -26,8 +26,8 @@ int check_heads(int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t dty
   return AWQ_OK;
 }
 
-// a packed operand: strides that hold a head's elements (one head, or one token, may have
-// any stride) and keep 16-byte accesses aligned
+// a packed operand: strides that hold a head's elements (one head may have any stride) and
+// keep 16-byte accesses aligned
 int check_strides(int64_t token, int64_t head, int32_t heads, int32_t head_dim) {
   if (token < 0 || head < 0) return AWQ_ERR_INVALID_ARG;
   if ((heads > 1 && head < head_dim) || token < head_dim) return AWQ_ERR_INVALID_ARG;

@@ -69,3 +69,43 @@ def test_a_visible_nan_stays_in_its_channel(dtype, drafts, hq, hkv):
     want, bound = ref.tree(q, kc, vc, table, ctx, drafts, None)
     assert int(torch.isnan(want).sum()) == hq * (2 * drafts[0] + drafts[1])
     ref.check(out, want, bound)
+
+
+# ---------------------------------------------------- strides of dimensions of one element
+
+def test_one_token_of_a_long_tensor():
+    """The last token of a prompt, as a model's decode takes it: its token stride is that of the
+    whole prompt, and is not one of the call's."""
+    q, k, v = (randn(1, 1100, h, 128, seed=s).to(DEV)[:, -1] for s, h in enumerate((64, 8, 8)))
+    assert q.stride(0) > 1 << 23
+    freq, _ = block.rope_frequencies(128, device=DEV)
+    got_q, got_k = block.awq_rope(q, i32([77]), freq, k=k)
+    ref.check(got_q, *ref.rope(q, i32([77]), freq))
+    ref.check(got_k, *ref.rope(k, i32([77]), freq))
+    ref.check(block.awq_attn_prompt(q, k, v, cumulative([1])), *ref.prompt(q, k, v, [1]))
+    into = torch.zeros(1, 1100, 64, 128, dtype=F16, device=DEV)
+    block.awq_attn_prompt(q, k, v, cumulative([1]), out=into[:, 5])
+    ref.check(into[:, 5], *ref.prompt(q, k, v, [1]))
+    assert float(into[:, :5].abs().max()) == 0.0 and float(into[:, 6:].abs().max()) == 0.0
+    _, kc, vc, table = tree_inputs([50], [1], 64, 8, 128, 16, F16, 3)
+    out = block.awq_attn_tree(q, kc, vc, table, i32([50]), cumulative([1]), 1)
+    ref.check(out, *ref.tree(q, kc, vc, table, [50], [1], None))
+
+
+@pytest.mark.parametrize("pages,hkv,page", [(40, 1, 1), (40, 2, 1), (5, 1, 8), (1, 1, 40), (1, 2, 40)])
+def test_caches_with_dimensions_of_one(pages, hkv, page):
+    """Strides that address nothing (3 for a dimension of one) are not looked at."""
+    d = 64
+    kc, vc = (randn(pages, hkv, page, d, seed=s).to(DEV) for s in (1, 2))
+    odd = [3 if n == 1 else s for n, s in zip(kc.shape, kc.stride())]
+    kv = [t.as_strided(t.shape, odd) for t in (kc, vc)]
+    table, ctx = torch.arange(pages, dtype=torch.int32, device=DEV)[None], [pages * page - 2]
+    q = randn(2, 4, d, seed=3).to(DEV)
+    for k, v in (kv, (kv[0], vc)):
+        out = block.awq_attn_tree(q, k, v, table, i32(ctx), cumulative([2]), 2)
+        ref.check(out, *ref.tree(q, kc, vc, table, ctx, [2], None))
+    freq, _ = block.rope_frequencies(d, device=DEV)
+    new = randn(1, hkv, d, seed=4).to(DEV)
+    block.awq_rope(None, i32([0]), freq, k=new, v=new, k_cache=kv[0], v_cache=kv[1],
+                   slots=torch.tensor([pages * page - 1], device=DEV))
+    assert torch.equal(vc[-1, :, -1], new[0]) and torch.equal(kc[-1, :, -1], new[0])
