@@ -730,12 +730,17 @@ bool by_rows(int64_t max_rows, int64_t seqs, int32_t kv_heads, int32_t head_dim)
   return max_rows > 16 || seqs * kv_heads > (head_dim <= 64 ? 512 : 256);
 }
 
+// Splits that keep the pages of each within what a workgroup stages
+int64_t least_splits(int64_t max_len, int32_t page_size) {
+  const int64_t limit = static_cast<int64_t>(kTableEntries - 1) * page_size / kMinChunk * kMinChunk;
+  return (max_len + limit - 1) / limit;
+}
+
 // Splits of the longest context the table holds, by what a call is expected to take (us, from
 // timelines on MI355X): a workgroup's fixed time (finding its sequence, its pages and the
 // first step, and its result), its positions, the longest last workgroup, and with more
 // than one split the second launch and the traffic of the partial results. Lengths are not
-// known here: sequences are taken to be 0.6 of the longest on average. A split touches at
-// most as many pages as a workgroup stages.
+// known here: sequences are taken to be 0.6 of the longest on average.
 int pick_splits(int64_t tokens, int64_t seqs, int64_t max_len, int32_t page_size, int64_t max_rows, int32_t q_heads,
                 int32_t kv_heads, int32_t head_dim) {
   const bool many = by_rows(max_rows, seqs, kv_heads, head_dim);
@@ -745,8 +750,7 @@ int pick_splits(int64_t tokens, int64_t seqs, int64_t max_len, int32_t page_size
   const double blocks = many ? static_cast<double>(tokens) * (q_heads / kv_heads) / 64 + 0.5 * seqs : seqs;
   const double groups = kv_heads * (blocks > seqs ? blocks : seqs);
   const double merged = static_cast<double>(tokens) * q_heads * head_dim * 8;  // bytes per split, both ways
-  const int64_t limit = static_cast<int64_t>(kTableEntries - 1) * page_size / kMinChunk * kMinChunk;
-  const int64_t least = (max_len + limit - 1) / limit;
+  const int64_t least = least_splits(max_len, page_size);
   const int64_t most = (max_len + kMinChunk - 1) / kMinChunk;
   int64_t best = 1;
   double best_time = 0.0;
@@ -795,6 +799,11 @@ hipError_t launch_t(const TreeArgs& a, bool many, hipStream_t st) {
   return hipGetLastError();
 }
 
+// workgroups of 64 rows that a sequence's new tokens may need (1 in the kernel of 16 rows)
+int64_t row_blocks(int64_t max_rows, int64_t seqs, int32_t kv_heads, int32_t head_dim) {
+  return by_rows(max_rows, seqs, kv_heads, head_dim) ? (max_rows + 63) / 64 : 1;
+}
+
 int attn_tree_splits(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q,
                      int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   return pick_splits(tokens, seqs, table_width * page_size, page_size,
@@ -807,6 +816,13 @@ size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_wid
                                  int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
   const int s = attn_tree_splits(tokens, seqs, table_width, page_size, max_q, q_heads, kv_heads, head_dim);
   return s > 1 ? static_cast<size_t>(tokens) * q_heads * s * (head_dim + 2) * 4 : 0;
+}
+
+int64_t attn_tree_blocks(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim) {
+  const int64_t least = least_splits(table_width * page_size, page_size);
+  return row_blocks(static_cast<int64_t>(max_q) * (q_heads / kv_heads), seqs, kv_heads, head_dim) *
+         (least > kMaxSplits ? least : kMaxSplits);
 }
 
 hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
@@ -843,7 +859,7 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   a.c = g.scale * kLog2e;
   const int64_t rows = static_cast<int64_t>(g.max_q) * a.group;
   const bool many = by_rows(rows, g.seqs, g.kv_heads, g.head_dim);
-  a.row_blocks = static_cast<int32_t>(many ? (rows + 63) / 64 : 1);
+  a.row_blocks = static_cast<int32_t>(row_blocks(rows, g.seqs, g.kv_heads, g.head_dim));
   a.splits = attn_tree_splits(g.tokens, g.seqs, g.table_width, g.page_size, g.max_q, g.q_heads, g.kv_heads,
                               g.head_dim);
   a.part = a.splits > 1 ? static_cast<float*>(g.ws) : nullptr;

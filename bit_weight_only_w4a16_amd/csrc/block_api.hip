@@ -10,6 +10,7 @@ namespace {
 constexpr int64_t kMaxStride = int64_t{1} << 23;  // elements: 128 rows stay below 2^31 bytes
 constexpr int64_t kMaxTokens = int64_t{1} << 30;
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 4096, kMaxRows = int64_t{1} << 25;
+constexpr int64_t kMaxBlocks = (int64_t{1} << 24) - 1;
 constexpr int kMaxHeadDim = 128, kMaxHeads = 4096;
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -133,6 +134,9 @@ static int check_tree_sizes(int64_t tokens, int64_t seqs, int64_t table_width, i
   // a wavefront per row in the second launch, which holds 2^32 threads; with at most 2^21
   // splits (pages of one position) of 130 floats a row the workspace's size fits 64 bits
   if (tokens * q_heads > kMaxRows) return AWQ_ERR_UNSUPPORTED;
+  // workgroups of 256 threads along x, of which a launch holds 2^32
+  if (awq::attn_tree_blocks(seqs, table_width, page_size, max_q, q_heads, kv_heads, head_dim) > kMaxBlocks)
+    return AWQ_ERR_UNSUPPORTED;
   return AWQ_OK;
 }
 

@@ -10,6 +10,9 @@ hipError_t launch_rope(const awq_rope_args& a, hipStream_t st);
 hipError_t launch_attn_prompt(const awq_attn_prompt_args& a, hipStream_t st);
 size_t attn_tree_workspace_bytes(int64_t tokens, int64_t seqs, int64_t table_width, int32_t page_size,
                                  int32_t max_q, int32_t q_heads, int32_t kv_heads, int32_t head_dim);
+// most workgroups of a call along x: row blocks times splits
+int64_t attn_tree_blocks(int64_t seqs, int64_t table_width, int32_t page_size, int32_t max_q, int32_t q_heads,
+                         int32_t kv_heads, int32_t head_dim);
 hipError_t launch_attn_tree(const awq_attn_tree_args& a, hipStream_t st);
 
 constexpr float kLog2e = 1.4426950408889634f;

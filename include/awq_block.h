@@ -135,7 +135,8 @@ int awq_attn_prompt(const awq_attn_prompt_args* args, hipStream_t stream);
  * block_table rows hold table_width entries; positions past table_width * page_size are
  * not there (the length is clamped), page numbers are clamped to [0, pages - 1].
  * scale is finite and positive. At most 65535 sequences, table_width * page_size < 2^30,
- * tokens * q_heads <= 2^25.
+ * tokens * q_heads <= 2^25; with pages of a few positions and thousands of heads in a group,
+ * less (UNSUPPORTED where row blocks times splits of the context exceed a launch).
  * ws: device, awq_attn_tree_workspace_bytes() bytes (the partial results of a context split
  * over workgroups; overwritten by every call), may be NULL with ws_bytes == 0 where that is 0.
  */
