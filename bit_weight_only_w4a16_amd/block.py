@@ -43,7 +43,7 @@ def awq_gemm_fused(x, inv_s_c, packed, n: int, k: int, group: int = awq.GROUP, f
 
 
 def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-                     original: int = 8192, low: float = 1.0, high: float = 4.0, device="cpu"):
+                     original: int = 8192, low: float = 1.0, high: float | None = None, device="cpu"):
     """(inv_freq float32 [rot_dim / 2], scale): base ** (-2 i / rot_dim), stretched for
     contexts `factor` times as long as the `original` one:
 
@@ -56,6 +56,7 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
       "yarn"    the same blend, linear in the pair's index between the pairs that turn `high`
                 and `low` times, and scale = 0.1 ln(factor) + 1 on q and k.
 
+    `high` is 4 for "bands" and 32 for "yarn" unless given, as published for each.
     Computed once, in float64, and rounded to float32."""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be even and positive")
@@ -70,6 +71,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str | None = 
             raise ValueError("ntk scaling needs more than one pair")
         freq = (base * factor ** (rot_dim / (rot_dim - 2))) ** -i
     elif scaling in ("bands", "yarn"):
+        if high is None:
+            high = 4.0 if scaling == "bands" else 32.0
         if not 0 < low < high:
             raise ValueError("low must be positive and less than high")
         if scaling == "bands":
