@@ -306,11 +306,69 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
   for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
     for (int i = 0; i < 16; ++i) broken |= acc[dt][i] != acc[dt][i];
-  // rows that came out NaN though their probabilities' sum is not (masked ones add exactly 0):
-  // below, key by key, for a masked infinity or NaN may be the cause
-  uint64_t again = __ballot(broken && row < len && l == l);
-  again = (again | (again >> 32)) & 0xFFFFFFFFu;
-  if (row < len && ((again >> col) & 1) == 0) {
+  // Rows that came out NaN though their probabilities' sum is not (masked ones add exactly 0),
+  // and an infinity or NaN among the values of the diagonal's tile, which some rows do not see:
+  // the products once more without that tile, whose values each row gets key by key. (Here
+  // and not in the loop: a look at the tile's values there cost 1 to 7 % of every call.)
+  if (__ballot(broken && row < len && l == l) != 0) {
+    const int diagonal = (mine - 1) * kBK;
+    bool finite = true;
+    if (diagonal + lane < len)
+      for (int d = 0; d < a.head_dim; d += 8)
+        finite = finite && T::finite8(*reinterpret_cast<const u32x4*>(vbase + (diagonal + lane) * a.v_token + d));
+    if (__ballot(!finite) != 0) {
+      const float shift = m == kNegInf ? 0.0f : kShift - m;
+#pragma unroll
+      for (int dt = 0; dt < ND; ++dt)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[dt][i] = 0.0f;
+#pragma unroll 1
+      for (int kv0 = 0; kv0 < diagonal; kv0 += 32) {
+        float16_t s;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          const int d = 16 * c + 8 * h;
+          u32x4 k = {0, 0, 0, 0};
+          if (d < a.head_dim) k = *reinterpret_cast<const u32x4*>(kbase + (kv0 + col) * a.k_token + d);
+          s = T::mfma32(__builtin_bit_cast(v8, k), qf[c], s);
+        }
+#pragma unroll
+        for (int cc = 0; cc < 2; ++cc) {
+          u32x4 p;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2)
+            p[i >> 1] = T::pack2(__builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * cc + i], a.c, shift)),
+                                 __builtin_amdgcn_exp2f(__builtin_fmaf(s[8 * cc + i + 1], a.c, shift)));
+#pragma unroll
+          for (int dt = 0; dt < ND; ++dt) {
+            typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+            u16x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (32 * dt + col < a.head_dim) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                v[i] = vbase[(kv0 + 16 * cc + 8 * (i >> 2) + 4 * h + (i & 3)) * a.v_token + 32 * dt + col];
+            }
+            acc[dt] = T::mfma32(__builtin_bit_cast(v8, v), __builtin_bit_cast(v8, p), acc[dt]);
+          }
+        }
+      }
+      if (row < len)
+        add_keys<T, 4 * ND>(
+            a.q + (start + row) * a.q_token + head * a.q_head, a.head_dim, a.c, shift, diagonal, min(len, wq0 + 32),
+            4 * h, 8,
+            [&](int j, const uint16_t*& kr, const uint16_t*& vr) {
+              kr = kbase + j * a.k_token;
+              vr = vbase + j * a.v_token;
+              return j <= row;
+            },
+            [&](int r, int i, float p, float x) {
+              acc[r >> 2][4 * (r & 3) + i] = __builtin_fmaf(p, x, acc[r >> 2][4 * (r & 3) + i]);
+            });
+    }
+  }
+  if (row < len) {
     uint16_t* o = a.out + (start + row) * a.o_token + head * a.o_head;
 #pragma unroll
     for (int dt = 0; dt < ND; ++dt)
@@ -321,23 +379,6 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
           *reinterpret_cast<uint2*>(o + d) = make_uint2(T::pack2(acc[dt][i] * inv, acc[dt][i + 1] * inv),
                                                         T::pack2(acc[dt][i + 2] * inv, acc[dt][i + 3] * inv));
       }
-  }
-  while (again != 0) {
-    const int i = __builtin_ctzll(again);
-    again &= again - 1;
-    const int t = wq0 + i;
-    float mr, lr;
-    float2_t orow;
-    attend_row<T>(a.q + (start + t) * a.q_token + head * a.q_head, a.head_dim, a.c, 0, t + 1, kShift,
-                  [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
-                    kr = kbase + j * a.k_token;
-                    vr = vbase + j * a.v_token;
-                    return true;
-                  },
-                  mr, lr, orow);
-    if (2 * lane < a.head_dim)
-      *reinterpret_cast<uint32_t*>(a.out + (start + t) * a.o_token + head * a.o_head + 2 * lane) =
-          T::pack2(orow.x * inv_sum(lr), orow.y * inv_sum(lr));
   }
 }
 

@@ -10,7 +10,7 @@
 // together, so the cache is read once for all of them: up to 16 rows in one workgroup of
 // the kernel described here, more in workgroups of 64 (attn_tree_rows_kernel). The
 // context is split over workgroups, and inside a workgroup over its four wavefronts: each
-// takes every fourth step of 32 positions and runs alone, with a running maximum and sum of
+// takes every fourth step of 32 positions, from the last to the first, and runs alone, with a running maximum and sum of
 // its own, its own LDS ring and no barriers, until the four results are merged through LDS.
 // With more than one split the merged result is a partial one (float32 maximum, sum and
 // unnormalised row) in the workspace, and a second launch adds the splits in their order.
@@ -93,7 +93,7 @@ __device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
 }
 
 // The factor that brings a partial result with maximum m and sum l to the maximum top (sums
-// and rows of every part carry 2^kShift, those of rows done key by key too). A
+// and rows of every part carry 2^kShift). A
 // part that saw no finite score (m = -inf) has l = 0, or NaN if it saw a NaN, and passes
 // that on.
 __device__ __forceinline__ float scale_of(float m, float l, float top) {
@@ -231,23 +231,26 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   for (int d = 0; d < ND; ++d) acc[d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   // One step is used while the next is on its way, and the addresses of the one after that
-  // are found meanwhile.
+  // are found meanwhile. The last step, which may hold new tokens, comes first: where the sums
+  // are NaN after it, they start again from zero without its values (see add_keys).
   const int first = p0 + kStep * wave;
   constexpr int kStride = kStep * kWaves;
+  const int last = first < p1 ? first + (p1 - 1 - first) / kStride * kStride : first - 1;
+  bool left_out = false;  // the last step's values are missing in acc
   int64_t at[LOADS];
-  if (first < p1) {
-    find_step(first, at);
+  if (last >= first) {
+    find_step(last, at);
     load_step(at, 0);
-    if (first + kStride < p1) find_step(first + kStride, at);
+    if (last - kStride >= first) find_step(last - kStride, at);
   }
   // (the stage is a compile-time value: the LDS addresses then differ by constants)
   auto step = [&](auto stage_, int s0) {
     constexpr int stage = decltype(stage_)::value;
-    if (s0 + kStride < p1) {
-      wait_lds();  // the last step's reads of this stage are done
+    if (s0 - kStride >= first) {
+      wait_lds();  // the step before's reads of this stage are done
       load_step(at, stage ^ 1);
       wait_loads<2 * LOADS>();  // the step has landed
-      if (s0 + 2 * kStride < p1) find_step(s0 + 2 * kStride, at);
+      if (s0 - 2 * kStride >= first) find_step(s0 - 2 * kStride, at);
     } else {
       wait_loads<0>();
     }
@@ -272,7 +275,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
       sc[0] = T::mfma16(kf[0][c], qf, sc[0]);
       sc[1] = T::mfma16(kf[1][c], qf, sc[1]);
     }
-    if (s0 + kStep > s.ctx) {  // new tokens (or the end) in the step: one bit per position
+    // new tokens (or the end) in the step: one bit per position. (At most 16 tokens: a
+    // wavefront meets one such step, its last.)
+    const bool masked = s0 + kStep > s.ctx;
+    if (masked) {
       const uint32_t bits = visible(sees, s0 - s.ctx, p1 - s0) >> (4 * g);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -310,11 +316,36 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
       const short4_t hi = lds_read_tr(vs + rb * RB + 16 * v_pos<DP>(rb, ch) + byte);
       acc[d] = T::mfma16(join8<v8>(lo, hi), __builtin_bit_cast(v8, p), acc[d]);
     }
+    if (masked) {
+      bool nan = false;
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) nan |= acc[d][i] != acc[d][i];
+      if (__ballot(nan) != 0) {
+        left_out = true;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    }
     asm volatile("" ::: "memory");
   };
-  for (int s0 = first; s0 < p1; s0 += 2 * kStride) {
+  for (int s0 = last; s0 >= first; s0 -= 2 * kStride) {
     step(std::integral_constant<int, 0>{}, s0);
-    if (s0 + kStride < p1) step(std::integral_constant<int, 1>{}, s0 + kStride);
+    if (s0 - kStride >= first) step(std::integral_constant<int, 1>{}, s0 - kStride);
+  }
+  if (left_out && col < rows) {
+    const int t = col / a.group, hq = kv_head * a.group + col % a.group;
+    add_keys<T, ND>(
+        a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, m == kNegInf ? 0.0f : kShift - m, last,
+        min(last + kStep, p1), 4 * g, 16,
+        [&](int j, const uint16_t*& kr, const uint16_t*& vr) {
+          const int64_t off = offset_of(j);
+          kr = kbase + off;
+          vr = vbase + off;
+          return j < s.ctx || ((sees >> ((j - s.ctx) & 63)) & 1) != 0;
+        },
+        [&](int r, int i, float p, float x) { acc[r][i] = __builtin_fmaf(p, x, acc[r][i]); });
   }
 
   // merge the four wavefronts: maxima, then the rows brought to the common maximum
@@ -353,20 +384,6 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
         o += *reinterpret_cast<const float2_t*>(sums + (w * 16 + r) * L::kSumStride + 2 * lane);
     }
     const int t = r / a.group, hq = kv_head * a.group + r % a.group;
-    // a row that came out NaN though its probabilities' sum is not: again, key by key (a
-    // masked infinity or NaN may be the cause)
-    if (sum == sum && __ballot(o.x != o.x || o.y != o.y) != 0) {
-      const uint64_t bits = a.mask != nullptr ? a.mask[s.first + t] : (2ull << t) - 1;
-      attend_row<T>(a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, p0, p1, kShift,
-                    [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
-                      const int64_t at = offset_of(static_cast<int>(j));
-                      kr = kbase + at;
-                      vr = vbase + at;
-                      const int64_t back = j - s.ctx;
-                      return back < 0 || ((bits >> (back & 63)) & 1) != 0;
-                    },
-                    top, sum, o);
-    }
     store_row<T>(a, s.first + t, hq, split, top, sum, o);
   }
 }
@@ -383,8 +400,9 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
 constexpr int kRowStep = 64;
 constexpr int kRowTiles = 2;  // of 16 rows, per wavefront
 
+// (D up to 64: 128 registers and 36 KiB of LDS, four workgroups per CU)
 template <typename T, int DP, bool PAD>
-__global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
+__global__ void __launch_bounds__(256, DP == 64 ? 4 : 2) attn_tree_rows_kernel(TreeArgs a) {
   typedef typename T::v8 v8;
   constexpr int RB = DP * 2, RC = DP / 8, TILE = kRowStep * RB;
   constexpr int ROWS = 1024 / RB;               // positions one load instruction fills
@@ -468,11 +486,15 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
 #pragma unroll
     for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
   }
+  // The last steps, which may hold new tokens, come first: where the sums are NaN after one,
+  // they start again from zero without the values so far (see add_keys).
+  const int last = p0 < p1 ? p0 + (p1 - 1 - p0) / kRowStep * kRowStep : p0 - 1;
+  int left_out = INT_MAX;  // the values from this step of the wavefront's on are missing in acc
   int64_t at[LOADS];
-  if (p0 < p1) {
-    find_step(p0, at);
+  if (last >= p0) {
+    find_step(last, at);
     load_step(at, 0);
-    if (p0 + kRowStep < p1) find_step(p0 + kRowStep, at);
+    if (last - kRowStep >= p0) find_step(last - kRowStep, at);
   }
   auto step = [&](auto stage_, int s0) {
     constexpr int stage = decltype(stage_)::value;
@@ -487,8 +509,8 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
         *reinterpret_cast<u32x4*>(vs + (OWN * wave + from) * RB + 16 * j) = u32x4{0, 0, 0, 0};
     }
     lds_barrier();  // the step is whole, and the other stage is done with
-    if (s0 + kRowStep < p1) load_step(at, stage ^ 1);
-    if (s0 + 2 * kRowStep < p1) find_step(s0 + 2 * kRowStep, at);
+    if (s0 - kRowStep >= p0) load_step(at, stage ^ 1);
+    if (s0 - 2 * kRowStep >= p0) find_step(s0 - 2 * kRowStep, at);
     const int mine = s0 + 32 * half;  // this wavefront's positions
     if (mine >= p1) return;
     vs += 32 * half * RB;
@@ -506,7 +528,8 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
         for (int n = 0; n < NT; ++n) sc[n][j] = T::mfma16(kf, qf[n][c], sc[n][j]);
       }
     }
-    if (mine + 32 > s.ctx) {  // new tokens (or the end) among them: one bit per position
+    const bool masked = mine + 32 > s.ctx;  // new tokens (or the end) among them: one bit per position
+    if (masked) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const uint32_t bits = visible(sees[n], mine - s.ctx, p1 - mine) >> (4 * g);
@@ -561,10 +584,44 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) acc[n][d] = T::mfma16(vf, __builtin_bit_cast(v8, p[n]), acc[n][d]);
     }
+    if (masked) {
+      bool nan = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) nan |= acc[n][d][e] != acc[n][d][e];
+      if (__ballot(nan) != 0) {
+        left_out = mine;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int d = 0; d < ND; ++d) acc[n][d] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+    }
   };
-  for (int s0 = p0; s0 < p1; s0 += 2 * kRowStep) {
+  for (int s0 = last; s0 >= p0; s0 -= 2 * kRowStep) {
     step(std::integral_constant<int, 0>{}, s0);
-    if (s0 + kRowStep < p1) step(std::integral_constant<int, 1>{}, s0 + kRowStep);
+    if (s0 - kRowStep >= p0) step(std::integral_constant<int, 1>{}, s0 - kRowStep);
+  }
+  for (int s0 = left_out; s0 < p1; s0 += kRowStep) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int x = opaque(lane), r = min(rb * 64 + 32 * (wave & 1) + 16 * n + (x & 15), rows - 1);
+      const int t = r / a.group, own = s.first + t;
+      const uint64_t bits = a.mask != nullptr ? a.mask[own] : (2ull << t) - 1;
+      add_keys<T, ND>(
+          a.q + own * a.q_token + (kv_head * a.group + r - t * a.group) * a.q_head, a.head_dim, a.c,
+          m[n] == kNegInf ? 0.0f : kShift - m[n], s0, min(s0 + 32, p1), 4 * (x >> 4), 16,
+          [&](int j, const uint16_t*& kr, const uint16_t*& vr) {
+            const int64_t off = offset_of(j);
+            kr = kbase + off;
+            vr = vbase + off;
+            return j < s.ctx || ((bits >> ((j - s.ctx) & 63)) & 1) != 0;
+          },
+          [&](int r, int i, float p, float x) { acc[n][r][i] = __builtin_fmaf(p, x, acc[n][r][i]); });
+    }
   }
 
   // the second half's results through LDS to the first (lane by lane, the same rows)
@@ -593,56 +650,26 @@ __global__ void __launch_bounds__(256, 2) attn_tree_rows_kernel(TreeArgs a) {
     const float f0 = scale_of(m[n], l[n], top), f1 = scale_of(other.x, other.y, top);
     m[n] = top;
     l[n] = l[n] * f0 + other.y * f1;
-    bool broken = false;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[n][d] = acc[n][d] * f0 + sums[(n * ND + d) * 64] * f1;
+    if (row0 + 16 * n >= rows) continue;
+    const int64_t at_row = (static_cast<int64_t>(token[n]) * a.q_heads + head[n]) * a.splits + split;
+    const float inv = inv_sum(l[n]);
+    uint16_t* o = a.out + token[n] * a.o_token + head[n] * a.o_head;
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
-      acc[n][d] = acc[n][d] * f0 + sums[(n * ND + d) * 64] * f1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) broken |= acc[n][d][i] != acc[n][d][i];
-    }
-    const bool real = row0 + 16 * n < rows;
-    // rows that came out NaN though their probabilities' sum is not: below, key by key (a
-    // masked infinity or NaN may be the cause)
-    uint64_t again = __ballot(broken && real && l[n] == l[n]);
-    again = (again | (again >> 16) | (again >> 32) | (again >> 48)) & 0xFFFFu;
-    if (real && ((again >> col) & 1) == 0) {
-      const int64_t at_row = (static_cast<int64_t>(token[n]) * a.q_heads + head[n]) * a.splits + split;
-      const float inv = inv_sum(l[n]);
-      uint16_t* o = a.out + token[n] * a.o_token + head[n] * a.o_head;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const int e = 16 * d + 4 * g;
-        if (PAD && e >= a.head_dim) continue;
-        if (a.part != nullptr) {
-          *reinterpret_cast<float4_t*>(a.part + at_row * a.head_dim + e) = acc[n][d];
-        } else {
-          *reinterpret_cast<uint2*>(o + e) = make_uint2(T::pack2(acc[n][d][0] * inv, acc[n][d][1] * inv),
-                                                        T::pack2(acc[n][d][2] * inv, acc[n][d][3] * inv));
-        }
-      }
-      if (a.part != nullptr && g == 0) {
-        float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
-        *reinterpret_cast<float2_t*>(ml + 2 * at_row) = float2_t{m[n], l[n]};
+      const int e = 16 * d + 4 * g;
+      if (PAD && e >= a.head_dim) continue;
+      if (a.part != nullptr) {
+        *reinterpret_cast<float4_t*>(a.part + at_row * a.head_dim + e) = acc[n][d];
+      } else {
+        *reinterpret_cast<uint2*>(o + e) = make_uint2(T::pack2(acc[n][d][0] * inv, acc[n][d][1] * inv),
+                                                      T::pack2(acc[n][d][2] * inv, acc[n][d][3] * inv));
       }
     }
-    while (again != 0) {
-      const int i = __builtin_ctzll(again);
-      again &= again - 1;
-      const int r = rb * 64 + 32 * (wave & 1) + 16 * n + i, tr = r / a.group;
-      const int hr = kv_head * a.group + r % a.group;
-      const uint64_t bits = a.mask != nullptr ? a.mask[s.first + tr] : (2ull << tr) - 1;
-      float row_top, sum;
-      float2_t o;
-      attend_row<T>(a.q + (s.first + tr) * a.q_token + hr * a.q_head, a.head_dim, a.c, p0, p1, kShift,
-                    [&](int64_t j, const uint16_t*& kr, const uint16_t*& vr) {
-                      const int64_t off = offset_of(static_cast<int>(j));
-                      kr = kbase + off;
-                      vr = vbase + off;
-                      const int64_t back = j - s.ctx;
-                      return back < 0 || ((bits >> (back & 63)) & 1) != 0;
-                    },
-                    row_top, sum, o);
-      store_row<T>(a, s.first + tr, hr, split, row_top, sum, o);
+    if (a.part != nullptr && g == 0) {
+      float* ml = a.part + static_cast<int64_t>(a.tokens) * a.q_heads * a.splits * a.head_dim;
+      *reinterpret_cast<float2_t*>(ml + 2 * at_row) = float2_t{m[n], l[n]};
     }
   }
 }

@@ -40,6 +40,14 @@ struct F16 {
   static __device__ __forceinline__ float add2(uint32_t pair, float sum) {
     return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, pair), half2_t{1.0f, 1.0f}, sum, false);
   }
+  // whether eight elements are neither infinities nor NaN
+  static __device__ __forceinline__ bool finite8(u32x4 x) {
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      finite = finite && (x[i] & 0x7C00u) != 0x7C00u && (x[i] & 0x7C000000u) != 0x7C000000u;
+    return finite;
+  }
   static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
   }
@@ -61,6 +69,14 @@ struct BF16 {
   static __device__ __forceinline__ float add2(uint32_t pair, float sum) {
     const bf2_t ones = {static_cast<__bf16>(1.0f), static_cast<__bf16>(1.0f)};
     return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf2_t, pair), ones, sum, false);
+  }
+  // whether eight elements are neither infinities nor NaN
+  static __device__ __forceinline__ bool finite8(u32x4 x) {
+    bool finite = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      finite = finite && (x[i] & 0x7F80u) != 0x7F80u && (x[i] & 0x7F800000u) != 0x7F800000u;
+    return finite;
   }
   static __device__ __forceinline__ float16_t mfma32(v8 a, v8 b, float16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -170,56 +186,50 @@ __device__ __forceinline__ float wave_sum(float v) {
 // 1 / sum of a row's probabilities; 0 for a row that saw nothing
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 
-// One row of attention by one wavefront, key by key, in float32: the running maximum m and
-// sum l (base 2, of exponents q.k * c) and, in lane i, o for d = 2 i, 2 i + 1. l and o carry
-// the factor 2^shift of the matrix kernels' own, with which they may be added to theirs. Keys that the
-// row does not see are skipped, not multiplied by zero, so nothing in them reaches the row.
-// The matrix kernels multiply masked probabilities of exactly 0 with whatever the masked
-// value row holds; where that is an infinity or NaN the row comes out NaN, and the kernels
-// take this path for rows that came out NaN while the sum of their probabilities, to which
-// masked keys add exactly 0, did not. key(j, k, v) gives key j's rows and whether the
-// row sees it.
-template <typename T, typename Key>
-__device__ __forceinline__ void attend_row(const uint16_t* q, int head_dim, float c, int64_t first,
-                                        int64_t end, float shift, Key key, float& m_out,
-                                        float& l_out, float2_t& o_out) {
-  const int lane = threadIdx.x & 63;
-  float m = kNegInf, l = 0.0f;
-  float2_t o = {0.0f, 0.0f};
-  for (int64_t j0 = first; j0 < end; j0 += 64) {
-    const int64_t j = j0 + lane;
-    const uint16_t *k = nullptr, *v = nullptr;
-    const bool sees = j < end && key(j, k, v);
-    float s = kNegInf;
-    if (sees) {
-      float dot = 0.0f;
-      for (int d = 0; d < head_dim; ++d) dot = __builtin_fmaf(T::to_float(q[d]), T::to_float(k[d]), dot);
-      s = dot * c;
-    }
-    const float m_new = fmaxf(m, wave_max(s));
-    const float base = m_new == kNegInf ? 0.0f : m_new;
-    const float p = sees ? __builtin_amdgcn_exp2f(s - base + shift) : 0.0f;
-    const float keep = __builtin_amdgcn_exp2f(m - base);
-    l = l * keep + wave_sum(p);
-    o *= keep;
-    m = m_new;
-    uint64_t left = __ballot(sees);
-    while (left != 0) {
-      const int i = __builtin_ctzll(left);
-      left &= left - 1;
-      const float pi = __shfl(p, i);
-      const uint64_t va = reinterpret_cast<uint64_t>(v);
-      const uint32_t lo = __shfl(static_cast<int>(va), i), hi = __shfl(static_cast<int>(va >> 32), i);
-      const uint16_t* vi = reinterpret_cast<const uint16_t*>((static_cast<uint64_t>(hi) << 32) | lo);
-      if (2 * lane < head_dim) {
-        o.x = __builtin_fmaf(pi, T::to_float(vi[2 * lane]), o.x);
-        o.y = __builtin_fmaf(pi, T::to_float(vi[2 * lane + 1]), o.y);
+// Values that a row does not see have probability 0, and the matrix instruction multiplies them
+// with it: an infinity or NaN among them makes the row NaN. That can only happen in the steps
+// that hold values which not every row sees (a causal tile's diagonal, the new tokens). Where it
+// may have, a kernel forms its sums without such a step, and add_keys adds what each row
+// sees of it, key by key. What is NaN after that is NaN by its definition, in its own channel.
+
+// v, of which the compiler knows nothing: what is computed from it is computed there, and not kept
+// in registers over a loop for code that hardly ever runs.
+__device__ __forceinline__ int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// p_j v_j of keys first .. end - 1 that this lane's row sees, in float32, with the probabilities
+// rounded as the matrix instruction takes them: channels at + step r .. + 3 by add(r, i, p, v)
+// for r < RUNS, i < 4. key(j, k, v) gives key j's rows and whether the row sees it.
+template <typename T, int RUNS, typename Key, typename Add>
+__device__ __forceinline__ void add_keys(const uint16_t* q, int head_dim, float c, float off, int first, int end, int at,
+                                         int step, Key key, Add add) {
+#pragma unroll 1
+  for (int j = first; j < end; ++j) {
+    const uint16_t *k, *v;
+    if (!key(j, k, v)) continue;
+    float dot = 0.0f;
+#pragma unroll 1
+    for (int d = 0; d < head_dim; d += 8) {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(q + d), b = *reinterpret_cast<const u32x4*>(k + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        dot = __builtin_fmaf(T::to_float(a[i] & 0xFFFFu), T::to_float(b[i] & 0xFFFFu), dot);
+        dot = __builtin_fmaf(T::to_float(a[i] >> 16), T::to_float(b[i] >> 16), dot);
       }
     }
+    const float p = T::to_float(T::bits(__builtin_amdgcn_exp2f(__builtin_fmaf(dot, c, off))));
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      if (at + step * r >= head_dim) continue;
+      const uint2 x = *reinterpret_cast<const uint2*>(v + at + step * r);
+      add(r, 0, p, T::to_float(x.x & 0xFFFFu));
+      add(r, 1, p, T::to_float(x.x >> 16));
+      add(r, 2, p, T::to_float(x.y & 0xFFFFu));
+      add(r, 3, p, T::to_float(x.y >> 16));
+    }
   }
-  m_out = m;
-  l_out = l;
-  o_out = o;
 }
 
 }  // namespace awq

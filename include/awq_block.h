@@ -19,6 +19,9 @@
  *     tokens [cu[b], cu[b + 1]). Values are clamped to [0, tokens] on the device; outputs
  *     of tokens in no sequence are not written.
  *   - Query head h reads key / value head h / (Hq / Hkv).
+ *   - Attention: what a row does not see never reaches it, infinities and NaN included. What it
+ *     sees and is NaN makes the row NaN (a key) or that channel of it (a value); a visible
+ *     infinity in a value gives infinity or, where its probability rounds to 0, NaN.
  *   - A paged cache holds position i of a sequence in slot i % page_size of page
  *     block_table[b][i / page_size]; a slot index is page * page_size + slot.
  */
@@ -100,7 +103,6 @@ int awq_rope(const awq_rope_args* args, hipStream_t stream);
 /*
  * awq_attn_prompt - causal attention of packed prompts:
  *   out[t][h] = sum over j <= t of t's sequence of p_j v_j,  p = softmax(scale q_t . k_j)
- * Keys and values of later tokens never reach a row, infinities and NaN included.
  * scale is finite and positive. (tokens / 128 + seqs) * q_heads <= 2^24 - 4096.
  */
 typedef struct awq_attn_prompt_args {
@@ -130,8 +132,8 @@ int awq_attn_prompt(const awq_attn_prompt_args* args, hipStream_t stream);
  * cache at positions ctx_lens[b] .. ctx_lens[b] + T - 1 (awq_rope puts them there). Token t
  * sees the whole context, and new token j where bit j of mask[cu_q[b] + t] is set (a tree of
  * drafted tokens: its ancestors and itself); without a mask, the new tokens j <= t. T == 1
- * is plain decoding. A token that sees nothing gets zeros. Positions that a token does not
- * see, and slots past the sequence's end, never reach it, infinities and NaN included.
+ * is plain decoding. A token that sees nothing gets zeros. Slots past the sequence's end are
+ * not seen.
  * block_table rows hold table_width entries; positions past table_width * page_size are
  * not there (the length is clamped), page numbers are clamped to [0, pages - 1].
  * scale is finite and positive. At most 65535 sequences, table_width * page_size < 2^30,

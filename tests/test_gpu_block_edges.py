@@ -109,3 +109,95 @@ def test_caches_with_dimensions_of_one(pages, hkv, page):
     block.awq_rope(None, i32([0]), freq, k=new, v=new, k_cache=kv[0], v_cache=kv[1],
                    slots=torch.tensor([pages * page - 1], device=DEV))
     assert torch.equal(vc[-1, :, -1], new[0]) and torch.equal(kc[-1, :, -1], new[0])
+
+
+# ------------------------------------------------------ what infinities and NaN cost, and do
+
+def milliseconds(call):
+    call()
+    times = []
+    for _ in range(3):
+        begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        begin.record()
+        call()
+        end.record()
+        torch.cuda.synchronize()
+        times.append(begin.elapsed_time(end))
+    return min(times)
+
+
+# What a NaN costs: the products of a wavefront's tiles once more, with loads that nothing hides (a
+# few times the call's 0.2 ms), and for a tile or step that holds it and is not seen whole by
+# every row, key by key, at most 64 keys (two rows of loads each, 5 us if nothing overlaps, 0.3 ms;
+# with 4096 wavefronts of which 2048 run at once twice that). Whole rows key by key took
+# 114 ms with one NaN in the first value.
+
+@pytest.mark.parametrize("where", ["first value", "first key", "every value", "every key", "last value", "value 2000"])
+def test_a_visible_nan_does_not_slow_a_prompt_down(where):
+    n, hq, hkv, d = 4096, 32, 8, 128
+    q, k, v = randn(n, hq + 2 * hkv, d, seed=1).to(DEV).split([hq, hkv, hkv], 1)
+    cu = cumulative([n])
+    target = k if "key" in where else v
+    first, last = {"first": (0, 1), "every": (0, n), "last": (n - 1, n), "value": (2000, 2001)}[where.split()[0]]
+    target[first:last, 0, 7] = float("nan")
+    assert milliseconds(lambda: block.awq_attn_prompt(q, k, v, cu)) < 2.0
+    nan = torch.isnan(block.awq_attn_prompt(q, k, v, cu))
+    hit = torch.zeros_like(nan)
+    hit[first:, :4, :] = "key" in where
+    hit[first:, :4, 7] = True
+    assert torch.equal(nan, hit)
+
+
+@pytest.mark.parametrize("drafts", [1, 8, 64])
+def test_a_visible_nan_does_not_slow_drafts_down(drafts):
+    ctx, hq, hkv, d, page = [20000], 32, 8, 128, 16
+    q, kc, vc, table = tree_inputs(ctx, [drafts], hq, hkv, d, page, F16, seed=drafts)
+    n, cu = i32(ctx), cumulative([drafts])
+    for pos in (0, 9999, 20000):
+        vc[at(table, 0, pos, page) + (7,)] = float("nan")
+    assert milliseconds(lambda: block.awq_attn_tree(q, kc, vc, table, n, cu, drafts)) < 2.0
+    nan = torch.isnan(block.awq_attn_tree(q, kc, vc, table, n, cu, drafts))
+    assert bool(nan[..., 7].all()) and int(nan.sum()) == drafts * hq
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("d", [128, 64, 40])
+def test_prompt_rows_before_a_bad_token(dtype, bad, d):
+    """One token's value holds an infinity or NaN in a channel, at every place of a tile: the rows
+    before it are right everywhere, the rows from it on in the other channels."""
+    lengths, hq, hkv = [40, 333, 33], 4, 2
+    qkv = randn(sum(lengths), hq + 2 * hkv, d, seed=d, dtype=dtype, gain=1.5)
+    want, bound = ref.prompt(*qkv.split([hq, hkv, hkv], 1), lengths)
+    for token in (0, 31, 32, 50, 63, 64, 100, 127, 128, 149, 250, 319, 332):
+        x = qkv.clone()
+        x[40 + token, hq + hkv:, 3] = bad
+        out = block.awq_attn_prompt(*x.to(DEV).split([hq, hkv, hkv], 1), cumulative(lengths))
+        hit = torch.zeros(want.shape, dtype=torch.bool)
+        hit[40 + token:373, :, 3] = True
+        assert not bool(torch.isfinite(out.cpu()[hit]).any()), token
+        assert int(torch.isnan(out).sum()) == (int(hit.sum()) if bad != bad else 0), token
+        ref.check(torch.where(hit, 0.0, out.cpu()), torch.where(hit, 0.0, want), bound, f"token {token}")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("-inf")])
+@pytest.mark.parametrize("ctx", [[64, 300], [3000, 90]])
+def test_drafts_of_which_some_are_bad(dtype, bad, ctx):
+    """64 drafted tokens, some of them bad in one channel: rows that do not see one are right, the
+    others in the other channels, wherever the new tokens start in a step."""
+    drafts, hq, hkv, d, page = [64, 61], 4, 2, 72, 16
+    for shift in (0, 1, 17, 31, 40):
+        at_ctx = [c + shift for c in ctx]
+        q, kc, vc, table = tree_inputs(at_ctx, drafts, hq, hkv, d, page, dtype, seed=shift)
+        masks = tree_masks(drafts, shift)
+        want, bound = ref.tree(q, kc, vc, table, at_ctx, drafts, masks)
+        hit = torch.zeros(want.shape, dtype=torch.bool)
+        for b in range(2):
+            for j in (0, 3, 33, 60):
+                vc[at(table, b, at_ctx[b] + j, page) + (5,)] = bad
+                for t in range(drafts[b]):
+                    hit[b * 64 + t, :, 5] |= bool(masks[b * 64 + t] >> j & 1)
+        out = block.awq_attn_tree(q, kc, vc, table, i32(at_ctx), cumulative(drafts), 64, mask=words(masks)).cpu()
+        assert not bool(torch.isfinite(out[hit]).any())
+        ref.check(torch.where(hit, 0.0, out), torch.where(hit, 0.0, want), bound, f"shift {shift}")
