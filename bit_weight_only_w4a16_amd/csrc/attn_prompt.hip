@@ -29,13 +29,14 @@
 // 256 rows were 1.5 % faster on the long sequence and 10 % slower on the ragged ones.
 #include "block_internal.hpp"
 
+#include <math.h>
+
 #include <type_traits>
 
 namespace awq {
 namespace {
 
 constexpr int kBK = 64;  // keys per tile
-constexpr float kShift = 12.0f, kMost = 4194304.0f;
 
 struct PromptArgs {
   const uint16_t *q, *k, *v;
@@ -45,6 +46,7 @@ struct PromptArgs {
   int32_t tokens, seqs, tiles, q_heads, group, head_dim;
   int32_t heads_log2;  // of a workgroup's query heads; its tokens are 128 >> heads_log2
   float c;  // scale * log2(e)
+  float shift, most;  // see tile_step
 };
 
 // chunk position of chunk c of row r in LDS. K is read 16 rows at one chunk, V 4 rows x 64
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
     for (int i = 0; i < 16; ++i) acc[t][i] = 0.0f;
   float m = kNegInf;  // maximum in use (see below), in units of scores * c
   float l = 0.0f;     // this lane's part of the sum
-  float off = -kNegInf;  // kShift - m
+  float off = -kNegInf;  // a.shift - m
 
   // LDS read positions
   const int tr_row = 4 * h + ((lane & 15) >> 2);                       // + 16 cc + 32 s (+ 8)
@@ -199,11 +201,13 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
 
   // Tile j (from buffer `buf`). The probabilities are first formed with the maximum in use,
   // whatever the tile's own is, and added up as they were rounded: two ALU instructions per
-  // pair and none for a maximum. Where the sum ran past kMost (or is NaN: an infinite one in
-  // binary16), the maximum and what was summed so far are brought up to date and the tile's
-  // probabilities formed again. P carries 2^kShift, which keeps what is far below the
-  // maximum out of binary16's subnormals; a maximum in use up to 2^(16 - kShift) too low
-  // only makes P larger.
+  // pair and none for a maximum. Where the sum ran past `most` = 2^(shift + 10) (or is NaN: an
+  // infinite one in binary16), the maximum and what was summed so far are brought up to date
+  // and the tile's probabilities formed again. P carries 2^shift. In binary16 that is 2^12,
+  // which keeps what is far below the maximum out of the subnormals; a maximum in use up to
+  // 2^4 too low only makes P larger. bfloat16 has float32's exponents, and there it is small
+  // enough (2^-6 / tokens) that all of a row's P add up to less than 1 (32 keys of a lane and
+  // tile to at most `most`): no sum of values of any size passes float32's largest.
   auto tile_step = [&](auto buf_, int j) {
     const unsigned char* ks = smem + decltype(buf_)::value * 2 * TILE;
     const unsigned char* vs = ks + TILE;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
       return sum;
     };
     float sum = probabilities();
-    if (__ballot(!(sum < kMost)) != 0) {
+    if (__ballot(!(sum < a.most)) != 0) {
       float top = kNegInf;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -263,14 +267,14 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
       const bool none = top == kNegInf;
       const float keep = none ? 1.0f : __builtin_amdgcn_exp2f(m - top);
       m = top;
-      off = none ? 0.0f : kShift - m;
+      off = none ? 0.0f : a.shift - m;
       l *= keep;
 #pragma unroll
       for (int t = 0; t < ND; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[t][i] *= keep;
       sum = probabilities();
-      off = kShift - m;
+      off = a.shift - m;
     }
     l += sum;
 #pragma unroll
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
       for (int d = 0; d < a.head_dim; d += 8)
         finite = finite && T::finite8(*reinterpret_cast<const u32x4*>(vbase + (diagonal + lane) * a.v_token + d));
     if (__ballot(!finite) != 0) {
-      const float shift = m == kNegInf ? 0.0f : kShift - m;
+      const float shift = m == kNegInf ? 0.0f : a.shift - m;
 #pragma unroll
       for (int dt = 0; dt < ND; ++dt)
 #pragma unroll
@@ -430,6 +434,8 @@ hipError_t launch_attn_prompt(const awq_attn_prompt_args& g, hipStream_t st) {
   const int64_t tiles = (g.tokens >> (7 - a.heads_log2)) + g.seqs;  // (the numbers, see find_tile)
   a.tiles = static_cast<int32_t>(tiles);
   a.c = g.scale * kLog2e;
+  a.shift = g.dtype == AWQ_DT_F16 ? 12.0f : -6.0f - log2_up(g.tokens);
+  a.most = exp2f(a.shift + 10.0f);
   const int64_t blocks = ((tiles * g.q_heads >> a.heads_log2) + 7) / 8 * 8;  // (an uneven share leaves some idle)
   if (g.dtype == AWQ_DT_F16)
     return g.head_dim <= 64 ? launch_dp<F16, 64>(a, blocks, st) : launch_dp<F16, 128>(a, blocks, st);

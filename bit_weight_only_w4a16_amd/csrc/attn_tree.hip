@@ -39,9 +39,11 @@ constexpr int kStages = 2;       // of a wavefront's ring: one in use, one on it
 constexpr int kMinChunk = kStep * kWaves;  // positions per split: at least this many
 constexpr int kTableEntries = 1024;        // page numbers of a split staged in LDS
 constexpr int kMaxSplits = 64;
-// P carries a factor 2^kShift: with the maximum in use at most kSlack below the true one,
-// binary16 holds it, and probabilities down to 2^-21 of the maximum keep their digits
-constexpr float kShift = 7.0f, kSlack = 8.0f;
+// P carries a factor 2^shift, and the maximum in use is at most kSlack below the true one. In
+// binary16 that is 2^7: P stays below 2^15, and down to 2^-21 of the maximum keeps its digits.
+// bfloat16 has float32's exponents, and there it is small enough (2^-8 / the longest length) that
+// a row's P add up to less than 1: no sum of values of any size passes float32's largest.
+constexpr float kShift = 7.0f, kSlack = 8.0f;  // (binary16's shift)
 
 struct TreeArgs {
   const uint16_t *q, *k, *v;
@@ -55,6 +57,7 @@ struct TreeArgs {
   int32_t splits, row_blocks;
   uint32_t page_mul, page_shift;  // pos / page_size = pos * page_mul >> page_shift
   float c;  // scale * log2(e)
+  float shift;
 };
 
 // pos / page_size for 0 <= pos < 2^31 (page_mul = floor(2^page_shift / page_size) + 1 with
@@ -93,7 +96,7 @@ __device__ __forceinline__ uint32_t visible(uint64_t mask, int back, int left) {
 }
 
 // The factor that brings a partial result with maximum m and sum l to the maximum top (sums
-// and rows of every part carry 2^kShift). A
+// and rows of every part carry 2^shift). A
 // part that saw no finite score (m = -inf) has l = 0, or NaN if it saw a NaN, and passes
 // that on.
 __device__ __forceinline__ float scale_of(float m, float l, float top) {
@@ -297,7 +300,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
 #pragma unroll
       for (int d = 0; d < ND; ++d) acc[d] *= keep;
     }
-    const float off = m == kNegInf ? 0.0f : kShift - m;
+    const float off = m == kNegInf ? 0.0f : a.shift - m;
     u32x4 p;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
   if (left_out && col < rows) {
     const int t = col / a.group, hq = kv_head * a.group + col % a.group;
     add_keys<T, ND>(
-        a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, m == kNegInf ? 0.0f : kShift - m, last,
+        a.q + (s.first + t) * a.q_token + hq * a.q_head, a.head_dim, a.c, m == kNegInf ? 0.0f : a.shift - m, last,
         min(last + kStep, p1), 4 * g, 16,
         [&](int j, const uint16_t*& kr, const uint16_t*& vr) {
           const int64_t off = offset_of(j);
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : 2) attn_tree_rows_kernel(T
     u32x4 p[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float off = m[n] == kNegInf ? 0.0f : kShift - m[n];
+      const float off = m[n] == kNegInf ? 0.0f : a.shift - m[n];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : 2) attn_tree_rows_kernel(T
       const uint64_t bits = a.mask != nullptr ? a.mask[own] : (2ull << t) - 1;
       add_keys<T, ND>(
           a.q + own * a.q_token + (kv_head * a.group + r - t * a.group) * a.q_head, a.head_dim, a.c,
-          m[n] == kNegInf ? 0.0f : kShift - m[n], s0, min(s0 + 32, p1), 4 * (x >> 4), 16,
+          m[n] == kNegInf ? 0.0f : a.shift - m[n], s0, min(s0 + 32, p1), 4 * (x >> 4), 16,
           [&](int j, const uint16_t*& kr, const uint16_t*& vr) {
             const int64_t off = offset_of(j);
             kr = kbase + off;
@@ -884,6 +887,7 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& g, hipStream_t st) {
   a.group = g.q_heads / g.kv_heads;
   a.head_dim = g.head_dim;
   a.c = g.scale * kLog2e;
+  a.shift = g.dtype == AWQ_DT_F16 ? kShift : -kSlack - log2_up(a.max_len);
   const int64_t rows = static_cast<int64_t>(g.max_q) * a.group;
   const bool many = by_rows(rows, g.seqs, g.kv_heads, g.head_dim);
   a.row_blocks = static_cast<int32_t>(row_blocks(rows, g.seqs, g.kv_heads, g.head_dim));

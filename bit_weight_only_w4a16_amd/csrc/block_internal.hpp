@@ -18,6 +18,13 @@ hipError_t launch_attn_tree(const awq_attn_tree_args& a, hipStream_t st);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 
+// the least n with 2^n >= v, for v >= 1
+inline float log2_up(int64_t v) {
+  int n = 0;
+  while ((int64_t{1} << n) < v) ++n;
+  return static_cast<float>(n);
+}
+
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
 typedef float float2_t __attribute__((ext_vector_type(2)));

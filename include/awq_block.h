@@ -21,7 +21,9 @@
  *   - Query head h reads key / value head h / (Hq / Hkv).
  *   - Attention: what a row does not see never reaches it, infinities and NaN included. What it
  *     sees and is NaN makes the row NaN (a key) or that channel of it (a value); a visible
- *     infinity in a value gives infinity or, where its probability rounds to 0, NaN.
+ *     infinity in a value gives infinity or, where its probability rounds to 0, NaN. Sums of
+ *     finite values stay finite up to the type's largest; for that, bfloat16 values below
+ *     about 2^-75 lose digits.
  *   - A paged cache holds position i of a sequence in slot i % page_size of page
  *     block_table[b][i / page_size]; a slot index is page * page_size + slot.
  */

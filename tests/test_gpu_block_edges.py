@@ -201,3 +201,36 @@ def test_drafts_of_which_some_are_bad(dtype, bad, ctx):
         out = block.awq_attn_tree(q, kc, vc, table, i32(at_ctx), cumulative(drafts), 64, mask=words(masks)).cpu()
         assert not bool(torch.isfinite(out[hit]).any())
         ref.check(torch.where(hit, 0.0, out), torch.where(hit, 0.0, want), bound, f"shift {shift}")
+
+
+# ------------------------------------------------------------- values of any size in bfloat16
+
+def wide_values(g, n, d, gain):
+    v = torch.randn(n, 1, d, generator=g) * gain
+    return v.clamp(-3.38e38, 3.38e38).to(BF16)   # (the type's largest is 3.39e38)
+
+
+@pytest.mark.parametrize("gain", [1e-25, 1e25, 1e31, 1e37, 3e38])
+def test_prompt_values_of_any_size(gain):
+    """Rows whose maximum moves from key to key; the bound is relative to the values."""
+    g = torch.Generator().manual_seed(13)
+    for n, spread in ((400, 8.0), (1500, 0.0)):   # (spread 0: every key weighs the same)
+        q = (torch.randn(n, 1, 64, generator=g) * 6).to(BF16)
+        k = (torch.randn(n, 1, 64, generator=g) * torch.linspace(0.1 * spread, spread, n)[:, None, None]).to(BF16)
+        v = wide_values(g, n, 64, gain)
+        v[:, :, 5] = 3.38e38 if gain > 1e38 else v[:, :, 5]
+        out = block.awq_attn_prompt(q.to(DEV), k.to(DEV), v.to(DEV), cumulative([n]))
+        assert bool(torch.isfinite(out).all())
+        ref.check(out, *ref.prompt(q, k, v, [n]))
+
+
+@pytest.mark.parametrize("gain", [1e-25, 1e25, 1e31, 1e37, 3e38])
+@pytest.mark.parametrize("ctx,drafts,hq", [([50], [1], 4), ([50], [40], 4), ([5000], [2], 4), ([5000], [20], 4)])
+def test_tree_values_of_any_size(gain, ctx, drafts, hq):
+    q, kc, vc, table = tree_inputs(ctx, drafts, hq, 1, 128, 16, BF16, seed=5)
+    g = torch.Generator().manual_seed(6)
+    vc[:] = wide_values(g, vc.shape[0] * 16, 128, gain).view(-1, 1, 16, 128).to(DEV)
+    kc *= 3
+    out = block.awq_attn_tree(q, kc, vc, table, i32(ctx), cumulative(drafts), max(drafts))
+    assert bool(torch.isfinite(out).all())
+    ref.check(out, *ref.tree(q, kc, vc, table, ctx, drafts, None))
