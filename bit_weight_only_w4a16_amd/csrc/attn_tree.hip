@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.c, off));
-        const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i + 1], a.c, off));
-        l += e0 + e1;
-        p[2 * t + (i >> 1)] = T::pack2(e0, e1);
+        const uint32_t pair = T::pack2(__builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i], a.c, off)),
+                                       __builtin_amdgcn_exp2f(__builtin_fmaf(sc[t][i + 1], a.c, off)));
+        l = T::add2(pair, l);  // what is multiplied, as it was rounded
+        p[2 * t + (i >> 1)] = pair;
       }
 #pragma unroll
     for (int d = 0; d < ND; ++d) {
@@ -571,10 +571,10 @@ __global__ void __launch_bounds__(256, DP == 64 ? 4 : 2) attn_tree_rows_kernel(T
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          const float e0 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e], a.c, off));
-          const float e1 = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e + 1], a.c, off));
-          l[n] += e0 + e1;
-          p[n][2 * j + (e >> 1)] = T::pack2(e0, e1);
+          const uint32_t pair = T::pack2(__builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e], a.c, off)),
+                                         __builtin_amdgcn_exp2f(__builtin_fmaf(sc[n][j][e + 1], a.c, off)));
+          l[n] = T::add2(pair, l[n]);
+          p[n][2 * j + (e >> 1)] = pair;
         }
     }
 #pragma unroll

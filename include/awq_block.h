@@ -9,7 +9,9 @@
  * retained. In addition:
  *   - Index arrays (int32, int64, float32) need their elements' alignment only.
  *   - Elements are binary16 (AWQ_DT_F16) or bfloat16 (AWQ_DT_BF16); sums, softmax
- *     statistics and rotations are float32.
+ *     statistics and rotations are float32. Attention rounds probabilities to the element
+ *     type before they meet v (the matrix instructions' operands), and divides by the sum of
+ *     the rounded ones; outputs are rounded once.
  *   - Tokens are packed: x[token][head][d] with the head's D elements contiguous and the
  *     strides of the token and of the head (in elements) given, so that q, k and v may be
  *     views of one fused projection. Strides are multiples of 8 elements, a token's less

@@ -234,3 +234,26 @@ def test_tree_values_of_any_size(gain, ctx, drafts, hq):
     out = block.awq_attn_tree(q, kc, vc, table, i32(ctx), cumulative(drafts), max(drafts))
     assert bool(torch.isfinite(out).all())
     ref.check(out, *ref.tree(q, kc, vc, table, ctx, drafts, None))
+
+
+# ---------------------------------------------------------- the sum of what is multiplied
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("ctx,drafts,hq", [([300], [1], 4), ([300], [9], 4), ([6000], [1], 4)])
+def test_equal_values_come_out_as_they_are(dtype, ctx, drafts, hq):
+    """Every value row is the same, and beside a largest score in every 16 positions all are such
+    that the probabilities round up by most of half a step: the weights' sum has to be that of
+    the rounded ones."""
+    y = -torch.arange(1, 800, dtype=torch.float64).div(1024).to(dtype).double().unique()
+    p = torch.exp(y)
+    up = p.to(dtype).double() / p - 1
+    score = float(y[up.argmax()])
+    assert float(up.max()) > 0.8 * ref.U[dtype]
+    q, kc, vc, table = tree_inputs(ctx, drafts, hq, 1, 128, 16, dtype, seed=1)
+    q[:], kc[:] = 0, 0
+    q[..., 0], kc[..., 0] = 1, score
+    kc[:, :, 0, 0] = 0
+    value = randn(128, seed=2, dtype=dtype).to(DEV)
+    vc[:] = value
+    out = block.awq_attn_tree(q, kc, vc, table, i32(ctx), cumulative(drafts), max(drafts), scale=1.0)
+    assert torch.equal(out, value.expand_as(out))
