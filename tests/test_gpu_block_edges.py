@@ -257,3 +257,21 @@ def test_equal_values_come_out_as_they_are(dtype, ctx, drafts, hq):
     vc[:] = value
     out = block.awq_attn_tree(q, kc, vc, table, i32(ctx), cumulative(drafts), max(drafts), scale=1.0)
     assert torch.equal(out, value.expand_as(out))
+
+
+# ------------------------------------------- block tables much wider than the contexts in them
+
+@pytest.mark.parametrize("ctx,drafts", [([517], [1]), ([517, 0, 90, 2000], [3, 1, 12, 30])])
+def test_a_table_for_the_longest_context(ctx, drafts):
+    """As a captured decode step has one: 32768 positions, the entries past a sequence's pages
+    anything; the splits past its end leave nothing behind."""
+    q, kc, vc, narrow = tree_inputs(ctx, drafts, 8, 2, 128, 16, F16, seed=8)
+    table = torch.full((len(ctx), 2048), -7, dtype=torch.int32, device=DEV)
+    table[:, :narrow.shape[1]] = narrow
+    table[:, 1000:] = 1 << 30
+    assert splits(q, kc, table, max(drafts)) > splits(q, kc, narrow, max(drafts))
+    masks = tree_masks(drafts, 9)
+    need = block.awq_attn_tree_workspace_bytes(sum(drafts), len(ctx), 2048, 16, max(drafts), 8, 2, 128)
+    ws = torch.full((need // 4,), float("nan"), device=DEV).view(torch.uint8)
+    out = block.awq_attn_tree(q, kc, vc, table, i32(ctx), cumulative(drafts), max(drafts), mask=words(masks), ws=ws)
+    ref.check(out, *ref.tree(q, kc, vc, narrow, ctx, drafts, masks))
