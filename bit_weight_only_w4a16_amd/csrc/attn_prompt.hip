@@ -21,11 +21,11 @@
 //
 // Bound by the matrix instructions and the exponentials together: a tile's 16 + 16 products
 // and its 64 exponentials per lane take turns in a wavefront and overlap only between the two
-// wavefronts of a SIMD. One sequence of 8192 tokens, 32 heads on 8, D = 128: 551 us, 1.0
+// wavefronts of a SIMD. One sequence of 8192 tokens, 32 heads on 8, D = 128: 541-563 us, 1.0
 // PFLOP/s of the triangle's products (a large matrix product reaches 1.3); six ragged
-// prompts of 1 to 2048 tokens (bfloat16) 110-120 us, 0.70-0.76 PFLOP/s (the last tiles and the
-// diagonals); five of 1 to 120 tokens 8.3 us, of which the launch and the first tile's way from memory are
-// most. 64 keys and 128 rows leave 104 registers and 64 KiB of LDS, two workgroups per CU;
+// prompts of 1 to 2048 tokens (bfloat16) 107-110 us, 0.76-0.78 PFLOP/s (the last tiles and the
+// diagonals; both a quarter longer right after a pause); five of 1 to 120 tokens 8.0 us, of
+// which the launch and the first tile's way from memory are most. 64 keys and 128 rows leave 104 registers and 64 KiB of LDS, two workgroups per CU;
 // 256 rows were 1.5 % faster on the long sequence and 10 % slower on the ragged ones.
 #include "block_internal.hpp"
 
@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(256, 2) attn_prompt_kernel(PromptArgs a) {
     for (int i = 0; i < 16; ++i) broken |= acc[dt][i] != acc[dt][i];
   // Rows that came out NaN though their probabilities' sum is not (masked ones add exactly 0),
   // and an infinity or NaN among the values of the diagonal's tile, which some rows do not see:
-  // the products once more without that tile, whose values each row gets key by key. (Here
-  // and not in the loop: a look at the tile's values there cost 1 to 7 % of every call.)
+  // the products once more without that tile, whose values each row gets key by key. (Here and
+  // not in the loop: a look at the tile's values there cost every call 1 to 9 %.) 4096 tokens, 32
+  // heads, one NaN in the first value 0.4 ms, without it 0.17.
   if (__ballot(broken && row < len && l == l) != 0) {
     const int diagonal = (mine - 1) * kBK;
     bool finite = true;
@@ -399,7 +400,7 @@ hipError_t launch_dp(const PromptArgs& a, int64_t blocks, hipStream_t st) {
 
 // Heads of a workgroup (log2). Many short sequences: as many as divide the group, for each
 // workgroup then fills its rows and a group's keys are read once (32 query heads on 8, D =
-// 128, 16 tokens each: 64, 256, 1024 sequences take 14, 36, 136 us; one head at a time 23, 83,
+// 128, 16 tokens each: 64, 256, 1024 sequences take 13, 35, 135 us; one head at a time 23, 83,
 // 332). From 256 tokens on, and where one head at a time leaves workgroups' slots empty, one:
 // the batches measured then take the same within 1 % (1 x 16 tokens 5.9 us, with four heads
 // 6.7; 6 ragged prompts of 993 tokens on average 121, 123; 8192 tokens 548, 552).

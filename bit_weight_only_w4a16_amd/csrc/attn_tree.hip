@@ -1,10 +1,10 @@
 // Attention of the last (new or drafted) tokens of each sequence over its paged cache
 // (awq_attn_tree in awq_block.h). A handful of query rows read every cached key and value
 // once: large calls are bound by streaming the cache from memory (16 sequences of up to 32768
-// positions, 64 heads on 8, D = 128, single tokens: 1.33 GB in 237 us, 5.6 TB/s, more than a
+// positions, 64 heads on 8, D = 128, single tokens: 1.33 GB in 236 us, 5.6 TB/s, more than a
 // copy's reads and writes reach), small ones by the chain of a launch, the sequence, its pages
-// and its first step (one token over 517 positions, 32 heads: 9.2 us; over 16 to 128
-// positions 5-6 us).
+// and its first step (one token over 517 positions, 32 heads: 9.0 us; over 16 to 128
+// positions 5.0 us).
 //
 // The query rows that share a key / value head (tokens x heads of the group) are handled
 // together, so the cache is read once for all of them: up to 16 rows in one workgroup of
@@ -396,10 +396,10 @@ __global__ void __launch_bounds__(256, 1) attn_tree_kernel(TreeArgs a) {
 // the positions, so that a fragment of K or V read from LDS serves two row tiles. The
 // wavefronts keep their Q operands in registers and the two halves of the positions meet at
 // the end; 64 KiB of LDS let two workgroups share a CU. Eight sequences of 0 to 4096 positions
-// and 1 to 32 drafted tokens, 32 heads on 8 (58 MB of cache): 22.5 us and 5 us for the second
-// launch; 64 sequences of 512 positions with 16 tokens each 29 us, 5.2 TB/s. (A
+// and 1 to 32 drafted tokens, 32 heads on 8 (58 MB of cache): 21.7 us and 5 us for the second
+// launch; 64 sequences of 512 positions with 16 tokens each 27.5 us, 5.0 TB/s. (A
 // wavefront on 16 rows and all positions, with loads that the compiler waited for, took 35 and
-// 112 us where this takes 26 and 48: 8 and 32 sequences of 2048 positions, 16 tokens each.)
+// 112 us where this takes 24 and 45: 8 and 32 sequences of 2048 positions, 16 tokens each.)
 constexpr int kRowStep = 64;
 constexpr int kRowTiles = 2;  // of 16 rows, per wavefront
 
@@ -752,10 +752,10 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(TreeArgs a) {
 }
 
 // Which of the two kernels: 64 rows per workgroup for more than 16 rows (24 and 32 rows, 512
-// positions, 64 sequences, 8 key heads: 27 us; two tiles of 16 in the other kernel 34, 36), and
+// positions, 64 sequences, 8 key heads: 26, 27 us; two tiles of 16 in the other kernel 34, 36), and
 // for fewer where the other's workgroups, one per CU (two up to D = 64), would not all run at
-// once (4 and 16 rows: 256 sequences of 16 positions 23, 26 us, the other 30, 43; 64 of 512 26,
-// 26 and 27, 30; but 16 of 2048, which do, 31, 32 and 27, 29).
+// once (4 and 16 rows: 256 sequences of 16 positions 22, 24 us, the other 31, 40; 64 of 512 25,
+// 25 and 26, 28; 16 of 2048, which do, 27, 29 either way).
 bool by_rows(int64_t max_rows, int64_t seqs, int32_t kv_heads, int32_t head_dim) {
   return max_rows > 16 || seqs * kv_heads > (head_dim <= 64 ? 512 : 256);
 }

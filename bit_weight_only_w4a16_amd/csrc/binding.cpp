@@ -2,7 +2,7 @@
 // checks its tensors, forms the argument structure and calls the C entry point on PyTorch's
 // current stream. A decode step makes these calls for every layer, and their kernels take a
 // few microseconds: checked and marshalled in Python, a call costs 9 to 13 us of host time,
-// here 5 to 8 (MI355X host). block.py holds the signatures and the documentation.
+// here 5 to 9 (MI355X host). block.py holds the signatures and the documentation.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -296,7 +296,7 @@ PyObject* attn_tree(PyObject* const* in, Py_ssize_t n) {
   a.scale = in[8] == Py_None ? 1.0f / std::sqrt(static_cast<float>(a.head_dim)) : static_cast<float>(number(in[8]));
   at::Tensor out = output(in[9], "out", q);
   a.out = call.packed<void>(out, "out", a.o_token, a.o_head);
-  Owned made;  // until the launch: without the GIL another thread may have it replaced
+  Owned made;  // until the launch: under capture nothing else holds it
   if (ws == nullptr) {
     const size_t need = awq_attn_tree_workspace_bytes(a.tokens, a.seqs, a.table_width, a.page_size, a.max_q,
                                                       a.q_heads, a.kv_heads, a.head_dim);
