@@ -380,12 +380,13 @@ def scratch(need: int, index: int) -> torch.Tensor:
     uses on every call, so no initialisation is needed).
 
     While the current stream is captured into a graph: a new one from the graph's memory, so
-    that graphs captured on one stream may be replayed side by side. Else one that is cached
-    per device, stream and thread and grown on demand: calls that share it must be ordered,
-    and several launches of one call may use it, between which another thread's call could
-    launch its own on the same stream. One that a larger one replaces is kept, for a caller
-    may have captured a graph with it (each is at least twice the one before, so they come
-    to no more than the last)."""
+    that graphs captured on one stream may be replayed side by side (not those that share a
+    memory pool, which share all they allocate). Else one that is cached per device, stream
+    and thread and grown on demand: calls that share it must be ordered, and several launches
+    of one call may use it, between which another thread's call could launch its own on the
+    same stream. One that a larger one replaces is kept, for a caller may have captured a
+    graph with it (each is at least twice the one before, so they come to no more than the
+    last)."""
     if _capturing(index):
         return torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     key = (index, _stream(index), threading.get_ident())
