@@ -52,6 +52,8 @@ FILE_FLAGS = {
     "chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_tree.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+    "moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "ceilings.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }
 
@@ -82,9 +84,9 @@ def build(jobs: int = 8, verbose: bool = False, tuning_out: str | None = None) -
     if not srcs:
         raise RuntimeError("no HIP sources found")
     with cf.ThreadPoolExecutor(max_workers=max(1, min(jobs, len(srcs)))) as ex:
-        binding = ex.submit(_compile_binding, verbose) if tuning_out is None else None
+        binding = [ex.submit(_compile_binding, s, verbose) for s in BINDING_SRCS] if tuning_out is None else []
         objs = list(ex.map(lambda s: _compile(s, verbose, build_dir, extra), srcs))
-        binding_obj = binding.result() if binding is not None else None
+        binding_objs = [b.result() for b in binding]
     tmp = out + ".tmp"
     cmd = [hipcc(), "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
     if verbose:
@@ -94,13 +96,13 @@ def build(jobs: int = 8, verbose: bool = False, tuning_out: str | None = None) -
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, out)
     if tuning_out is None:
-        _link_binding(binding_obj, verbose)
+        _link_binding(binding_objs, verbose)
         build_probe(verbose)
         build_abi_check(verbose)
     return out
 
 
-BINDING_SRC = os.path.join(CSRC, "binding.cpp")
+BINDING_SRCS = [os.path.join(CSRC, f) for f in ("binding.cpp", "binding_ffn.cpp")]
 BINDING_LIB = os.path.join(PKG, "_block.so")
 
 
@@ -112,25 +114,25 @@ def _run(cmd: list, what: str, verbose: bool) -> None:
         raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
 
 
-def _compile_binding(verbose: bool = False) -> str:
-    """The Python extension module of block.py (host code only, against PyTorch's headers)."""
+def _compile_binding(src: str, verbose: bool = False) -> str:
+    """A source of the Python extension module (host code only, against PyTorch's headers)."""
     import sysconfig
 
     import torch
     from torch.utils.cpp_extension import include_paths
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
-    obj = os.path.join(BUILD, "binding.cpp.o")
+    obj = os.path.join(BUILD, os.path.basename(src) + ".o")
     includes = [*include_paths(), sysconfig.get_paths()["include"], os.path.join(rocm, "include")]
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-D__HIP_PLATFORM_AMD__",
           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-          *[f"-isystem{i}" for i in includes], "-Wall", "-c", BINDING_SRC, "-o", obj], "binding", verbose)
+          *[f"-isystem{i}" for i in includes], "-Wall", "-c", src, "-o", obj], "binding", verbose)
     return obj
 
 
-def _link_binding(obj: str, verbose: bool = False) -> str:
+def _link_binding(objs: list, verbose: bool = False) -> str:
     from torch.utils.cpp_extension import library_paths
     tmp = BINDING_LIB + ".tmp"
-    _run(["g++", "-shared", "-fPIC", obj, "-o", tmp, *[f"-L{p}" for p in library_paths()], "-ltorch_python",
+    _run(["g++", "-shared", "-fPIC", *objs, "-o", tmp, *[f"-L{p}" for p in library_paths()], "-ltorch_python",
           "-ltorch_cpu", "-lc10", "-L", PKG, "-lawq_gfx950", "-Wl,-rpath,$ORIGIN"], "binding link", verbose)
     os.replace(tmp, BINDING_LIB)
     return BINDING_LIB

@@ -1,0 +1,210 @@
+// The router of a mixture of experts: logits = x w^T, scores, the k best and their weights.
+//
+// Which expert comes k-th is a border: two sums in another order of float32 would now and then
+// choose differently. Products of two elements are exact in float64, and so are the sums to
+// about 1e-16, so the choice is the definition's. The matrix cores' float64 instruction forms
+// 16 tokens x 16 experts from four channels, one element of each operand in a lane, so every
+// element is widened once.
+//
+// Two launches: partial sums of 16 x 16 logits over slices of the channels (a token alone
+// would otherwise leave the card to a few wavefronts), then one wavefront or workgroup per
+// token that adds them and ranks the experts: an expert's place is the number of experts in
+// front of it, which all are counted at once, without a chain of k maxima.
+#include "ffn_internal.hpp"
+
+namespace awq {
+namespace {
+
+typedef double double4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kSliceWaves = 4;
+
+// Slices of the channels, one per workgroup of four wavefronts, so that about two workgroups per
+// CU run; a wavefront has at least 64 channels.
+int route_slices(int64_t tokens, int hidden, int experts) {
+  const int64_t tiles = (tokens + 15) / 16 * ((experts + 15) / 16);
+  int64_t slices = 512 / tiles;
+  const int64_t most = (hidden + 64 * kSliceWaves - 1) / (64 * kSliceWaves);
+  if (slices > most) slices = most;
+  return slices < 1 ? 1 : static_cast<int>(slices);
+}
+
+struct RouteArgs {
+  const uint16_t *x, *w;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  double* part;  // [slices][tokens][experts]
+  int64_t tokens, x_stride;
+  int hidden, experts, k, slices, score, renormalize;
+  float scale;
+};
+
+// grid: token tiles, expert tiles, slices
+template <typename T>
+__global__ void __launch_bounds__(64 * kSliceWaves) route_logits_kernel(RouteArgs a) {
+  __shared__ double red[kSliceWaves][16][16];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * 16 + r;
+  const int expert = blockIdx.y * 16 + r;
+  const uint16_t* x = a.x + (token < a.tokens ? token : 0) * a.x_stride;
+  const uint16_t* w = a.w + static_cast<int64_t>(expert < a.experts ? expert : 0) * a.hidden;
+  // steps of 32 channels dealt to all slices' wavefronts in turn
+  const int steps = (a.hidden + 31) / 32, waves = kSliceWaves * a.slices;
+  double4_t acc = {0.0, 0.0, 0.0, 0.0};
+  for (int s = static_cast<int>(blockIdx.z) * kSliceWaves + wave; s < steps; s += waves) {
+    const int c = 32 * s + 8 * p;
+    uint4 xv = make_uint4(0, 0, 0, 0), wv = xv;
+    if (c < a.hidden && token < a.tokens) xv = *reinterpret_cast<const uint4*>(x + c);
+    if (c < a.hidden && expert < a.experts) wv = *reinterpret_cast<const uint4*>(w + c);
+    float xf[8], wf[8];
+    widen<T>(xv, xf);
+    widen<T>(wv, wf);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(xf[e]), static_cast<double>(wf[e]), acc, 0, 0, 0);
+  }
+  // element i of lane l is row 4 i + l / 16, column l % 16
+#pragma unroll
+  for (int i = 0; i < 4; ++i) red[wave][4 * i + p][r] = acc[i];
+  __syncthreads();
+  const int m = threadIdx.x / 16, n = threadIdx.x % 16;
+  double sum = 0.0;
+#pragma unroll
+  for (int v = 0; v < kSliceWaves; ++v) sum += red[v][m][n];
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + m;
+  const int e = blockIdx.y * 16 + n;
+  if (t < a.tokens && e < a.experts) a.part[(blockIdx.z * a.tokens + t) * a.experts + e] = sum;
+}
+
+// An order of choices as whole numbers: larger is better, NaN stands behind -infinity.
+__device__ __forceinline__ uint64_t order(double v) {
+  if (v != v) return 1;
+  const int64_t b = __builtin_bit_cast(int64_t, v + 0.0);  // one zero
+  return static_cast<uint64_t>(b < 0 ? ~b : b | INT64_MIN);
+}
+
+// THREADS threads for each token, NE experts each: lane's experts t, t + THREADS, ..
+template <int THREADS, int NE>
+__global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
+  constexpr int TOKENS = 256 / THREADS, WAVES = THREADS / 64, MOST = THREADS * NE;
+  __shared__ uint64_t keys[TOKENS][MOST];
+  __shared__ double picked[TOKENS][32];
+  __shared__ double wave_top[TOKENS][WAVES], wave_add[TOKENS][WAVES];
+  const int mine = threadIdx.x / THREADS, t = threadIdx.x % THREADS;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * TOKENS + mine;
+  const bool live = token < a.tokens;
+  double p[NE];
+  double top = -__builtin_inf();
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    const int e = t + THREADS * i;
+    double l = 0.0;
+    if (live && e < a.experts) {
+      for (int s = 0; s < a.slices; ++s) l += a.part[(s * a.tokens + token) * a.experts + e];
+      const double bias = a.bias == nullptr ? 0.0 : static_cast<double>(a.bias[e]);
+      if (a.score == AWQ_SCORE_SIGMOID) l = 1.0 / (1.0 + exp(-l));
+      keys[mine][e] = order(l + bias);
+      top = fmax(top, l);
+    }
+    p[i] = l;
+  }
+  if (a.score == AWQ_SCORE_SOFTMAX) {
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) top = fmax(top, __shfl_xor(top, s));
+    if (WAVES > 1) {
+      if ((t & 63) == 0) wave_top[mine][t >> 6] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmax(top, wave_top[mine][w]);
+    }
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      if (t + THREADS * i >= a.experts) continue;
+      p[i] = exp(p[i] - top);
+      sum += p[i];
+    }
+#pragma unroll
+    for (int s = 32; s > 0; s >>= 1) sum += __shfl_xor(sum, s);
+    if (WAVES > 1) {
+      if ((t & 63) == 0) wave_add[mine][t >> 6] = sum;
+      __syncthreads();
+      sum = 0.0;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) sum += wave_add[mine][w];
+    }
+#pragma unroll
+    for (int i = 0; i < NE; ++i) p[i] /= sum;
+  }
+  __syncthreads();  // all keys
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      const int e = t + THREADS * i;
+      if (e >= a.experts) continue;
+      const uint64_t key = keys[mine][e];
+      int place = 0;
+      for (int o = 0; o < a.experts; ++o) {
+        const uint64_t other = keys[mine][o];
+        place += other > key || (other == key && o < e);
+      }
+      if (place < a.k) {
+        a.ids[token * a.k + place] = e;
+        picked[mine][place] = p[i];
+      }
+    }
+  }
+  __syncthreads();
+  if (!live || t >= a.k) return;
+  double sum = 1.0;
+  if (a.renormalize != 0) {
+    sum = 0.0;
+    for (int j = 0; j < a.k; ++j) sum += picked[mine][j];
+  }
+  const double v = picked[mine][t] * static_cast<double>(a.scale);
+  a.weights[token * a.k + t] = sum == 0.0 ? 0.0f : static_cast<float>(v / sum);
+}
+
+template <int THREADS, int NE>
+hipError_t launch_choose(const RouteArgs& a, hipStream_t st) {
+  constexpr int TOKENS = 256 / THREADS;
+  hipLaunchKernelGGL((route_choose_kernel<THREADS, NE>), dim3(static_cast<unsigned>((a.tokens + TOKENS - 1) / TOKENS)),
+                     dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t moe_route_workspace_bytes(int64_t tokens, int32_t hidden, int32_t experts) {
+  return static_cast<size_t>(8) * route_slices(tokens, hidden, experts) * tokens * experts;
+}
+
+hipError_t launch_moe_route(const awq_moe_route_args& p, hipStream_t st) {
+  RouteArgs a;
+  a.x = static_cast<const uint16_t*>(p.x);
+  a.w = static_cast<const uint16_t*>(p.w);
+  a.bias = p.bias;
+  a.ids = p.ids;
+  a.weights = p.weights;
+  a.part = static_cast<double*>(p.ws);
+  a.tokens = p.tokens;
+  a.x_stride = p.x_stride;
+  a.hidden = p.hidden;
+  a.experts = p.experts;
+  a.k = p.k;
+  a.slices = route_slices(p.tokens, p.hidden, p.experts);
+  a.score = p.score;
+  a.renormalize = p.renormalize;
+  a.scale = p.scale;
+  const dim3 grid(static_cast<unsigned>((p.tokens + 15) / 16), (p.experts + 15) / 16, a.slices);
+  hipLaunchKernelGGL((p.dtype == AWQ_DT_F16 ? &route_logits_kernel<F16> : &route_logits_kernel<BF16>), grid,
+                     dim3(64 * kSliceWaves), 0, st, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (p.experts <= 64) return launch_choose<64, 1>(a, st);
+  if (p.experts <= 256) return launch_choose<256, 1>(a, st);
+  return launch_choose<256, 4>(a, st);
+}
+
+}  // namespace awq
