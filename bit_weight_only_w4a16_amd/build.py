@@ -52,7 +52,6 @@ FILE_FLAGS = {
     "chain.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_prompt.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "attn_tree.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-    "gemm_i8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "moe.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
     "ceilings.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
 }

@@ -8,6 +8,9 @@
 // registers, and the wavefronts' sums meet in LDS.
 #include "ffn_internal.hpp"
 
+#include <math.h>
+#include <stdio.h>
+
 namespace awq {
 namespace {
 
@@ -19,6 +22,7 @@ struct I8Args {
   const uint16_t *bias, *mul, *residual;
   uint16_t* y;
   int64_t M, N, q_stride;
+  int32_t* part;  // [splits][M][N]: the sums of a split of the channels
   int K, units, act;
 };
 
@@ -105,8 +109,345 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
   }
 }
 
+// ------------------------------------------------------------------------------- tiles
+//
+// Workgroups of four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of
+// 64 channels. Operands go from memory straight into LDS, into a ring of three steps, of
+// which two are on their way or have landed ahead of use. The only barrier of a step
+// stands before its second half, whose operands are in registers already.
+// v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
+// runs of four outputs of one row.
+
+typedef int int16_t_ __attribute__((ext_vector_type(16)));
+
+template <typename T>
+__device__ __forceinline__ float8_t load8(const uint16_t* p) {
+  float f[8];
+  widen<T>(*reinterpret_cast<const uint4*>(p), f);
+  return float8_t{f[0], f[1], f[2], f[3], f[4], f[5], f[6], f[7]};
+}
+// the tail of eight consecutive outputs, v scaled and with its bias, f and r the factors and residuals
+template <typename T>
+__device__ __forceinline__ uint4 tail8(const I8Args& a, float8_t v, uint4 f, uint4 r) {
+  switch (a.act) {
+    case AWQ_ACT_RELU: v = activate8<AWQ_ACT_RELU>(v); break;
+    case AWQ_ACT_GELU: v = activate8<AWQ_ACT_GELU>(v); break;
+    case AWQ_ACT_GELU_TANH: v = activate8<AWQ_ACT_GELU_TANH>(v); break;
+    case AWQ_ACT_SILU: v = activate8<AWQ_ACT_SILU>(v); break;
+    default: break;
+  }
+  float w[8];
+  if (a.mul != nullptr) {
+    widen<T>(f, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= w[e];
+  }
+  if (a.residual != nullptr) {
+    widen<T>(r, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += w[e];
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = v[e];
+  return narrow<T>(w);
+}
+
+constexpr int kStep = 64;  // channels of a step
+// Steps in LDS. Three steps of 128 x 256 outputs leave room for two workgroups on a CU, one of
+// which multiplies while the other stores (four steps: 149 us instead of 135 at 2048 x 14336 x
+// 4096; tiles of 256 x 256, which have a CU to themselves: 155).
+constexpr int kRing = 3;
+
+template <typename T, int BM, int BN, bool SPLIT>
+__global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
+  constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 32, FN = TN / 32;
+  constexpr int STAGE = (BM + BN) * kStep, PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W, RING = kRing;
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave & 1, wn = wave >> 1, half = lane >> 5, l32 = lane & 31;
+
+  // blocks of an XCD are neighbours: bands of eight row tiles, down the rows first
+  const int mt = static_cast<int>((a.M + BM - 1) / BM), nt = static_cast<int>((a.N + BN - 1) / BN);
+  const int id = xcd_block(blockIdx.x, mt * nt);
+  const int band = id / (8 * nt), band_rows = min(8, mt - 8 * band), in_band = id - band * 8 * nt;
+  const int tile_m = 8 * band + in_band % band_rows, tile_n = in_band / band_rows;
+  const int64_t m0 = static_cast<int64_t>(tile_m) * BM;
+  const int n0 = tile_n * BN;
+  const int rows = static_cast<int>(min(a.M - m0, static_cast<int64_t>(BM)));
+  const uint32_t stride = static_cast<uint32_t>(a.q_stride);
+  const u32x4 rq = rsrc_words(a.q + m0 * a.q_stride, (rows - 1) * stride + a.K);
+  const int tiles = static_cast<int>((a.N + 15) / 16);
+  const u32x4 rw = rsrc_words(a.codes, static_cast<uint32_t>(tiles) * a.units * 1024u);
+  const uint32_t base = lds_offset(lds);
+
+  // steps of this workgroup's share of the channels
+  int first = 0, steps = a.units;
+  if (SPLIT) {
+    first = static_cast<int>(static_cast<int64_t>(a.units) * blockIdx.y / gridDim.y);
+    steps = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.y + 1) / gridDim.y) - first;
+  }
+
+  // 64 bytes of a row in LDS, their 16-byte pieces exchanged by the row's number (p ^ row / 2 % 4),
+  // so that eight rows' equal pieces lie in different banks; the exchange is made where a lane loads
+  const uint32_t lane_q = (lane >> 2) * stride + 16u * ((lane & 3) ^ ((lane >> 3) & 3));
+  auto issue_piece = [&](int step, int i) {  // 1 KiB each: 16 rows, or a unit of W
+    const uint32_t dst = base + (step % RING) * STAGE;
+    if (i < PIECES_A) {
+      const uint32_t piece = wave * PIECES_A + i;
+      load_to_lds(rq, lane_q + piece * 16u * stride + static_cast<uint32_t>(first + step) * kStep, dst + piece * 1024u);
+      return;
+    }
+    const int piece = wave * PIECES_W + i - PIECES_A, t = n0 / 16 + piece;
+    const uint32_t at = t < tiles ? (static_cast<uint32_t>(t) * a.units + first + step) * 1024u : kNoLoad;
+    load_to_lds(rw, at + 16u * lane, dst + BM * kStep + piece * 1024u);
+  };
+  // operands of half s of a step, in the order of their use: W's, then the rows'
+  int4_t fq[2][FM], fw[2][FN];
+  auto read_one = [&](int step, int s, int i) {
+    const unsigned char* stage = lds + (step % RING) * STAGE;
+    if (i < FN) {
+      const unsigned char* w = stage + BM * kStep + (wn * TN / 16 + (l32 >> 4)) * 1024 + 16 * ((lane & 15) + 16 * (2 * s + half));
+      fw[s][i] = *reinterpret_cast<const int4_t*>(w + i * 2048);
+    } else {
+      const unsigned char* q = stage + (wm * TM + l32) * kStep + 16 * ((2 * s + half) ^ ((lane >> 1) & 3));
+      fq[s][i - FN] = *reinterpret_cast<const int4_t*>(q + (i - FN) * 32 * kStep);
+    }
+  };
+  int16_t_ acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0;
+  // A half's products in runs of FN, and between the runs an equal part of the next half's LDS
+  // reads and of the loads of a step to come: a wavefront may have its SIMD to itself, and nothing
+  // else would fill the matrix cores' pauses. (Left to the compiler, both stand in front.)
+  auto products = [&](int s, bool reads, int read_step, bool loads, int load_step) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s][j], fq[s][i], acc[i][j], 0, 0, 0);
+      if (reads) {
+#pragma unroll
+        for (int r = (FM + FN) * i / FM; r < (FM + FN) * (i + 1) / FM; ++r) read_one(read_step, s ^ 1, r);
+      }
+      if (loads) {
+#pragma unroll
+        for (int l = PIECES * i / FM; l < PIECES * (i + 1) / FM; ++l) issue_piece(load_step, l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < RING; ++i)
+    if (i < steps) {
+#pragma unroll
+      for (int l = 0; l < PIECES; ++l) issue_piece(i, l);
+    }
+  // `ahead` steps behind the one that is waited for may be on their way
+  auto wait_step = [&](int ahead) {
+    if (ahead >= 2) {
+      wait_loads<2 * PIECES>();
+    } else if (ahead == 1) {
+      wait_loads<PIECES>();
+    } else {
+      wait_loads<0>();
+    }
+    lds_barrier();
+  };
+  wait_step(min(steps, RING) - 1);
+#pragma unroll
+  for (int r = 0; r < FM + FN; ++r) read_one(0, 0, r);
+  for (int i = 0; i < steps; ++i) {
+    products(0, true, i, false, 0);
+    // this step's operands are read, the next step's have landed
+    wait_step(min(steps - i, RING) - 2);
+    products(1, i + 1 < steps, i + 1, i + RING < steps, i + RING);
+  }
+
+  // element e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32
+  if constexpr (SPLIT) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int64_t m = m0 + wm * TM + 32 * i + l32;
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int n = n0 + wn * TN + 32 * j + 8 * g + 4 * half;
+          if (m < a.M && n < a.N)
+            *reinterpret_cast<int4_t*>(a.part + (blockIdx.y * a.M + m) * a.N + n) =
+                int4_t{acc[i][j][4 * g], acc[i][j][4 * g + 1], acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]};
+        }
+    }
+    return;
+  }
+  // 32 rows at a time through the wavefront's own LDS, so that a lane gets eight outputs of a row
+  // and sixteen (or eight, or four) lanes a whole line; rows are 4 floats apart from the banks'
+  // period. A lane's columns stay the same: their scales and biases are read once, and the
+  // factors and residuals of all 32 rows are on their way while the sums go through LDS.
+  constexpr int PITCH = TN + 4, LANES = TN / 8, RUNS = LANES / 2;
+  float* mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
+  const int c = 8 * (lane % LANES), n = n0 + wn * TN + c;
+  const bool in = n < a.N;
+  float8_t sw = {}, bias = {};
+  if (in) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sw[e] = a.scales[n + e];
+    if (a.bias != nullptr) bias = load8<T>(a.bias + n);
+  }
+  float sx[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t m = m0 + wm * TM + 32 * i + l32;
+    sx[i] = m < a.M ? a.scale[m] : 0.0f;
+  }
+  __syncthreads();  // all wavefronts have read their last operands
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int64_t top = m0 + wm * TM + 32 * i + lane / LANES;
+    uint4 f[RUNS], r[RUNS];
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const int64_t m = top + k * (64 / LANES), o = m * a.N + n;
+      f[k] = r[k] = make_uint4(0, 0, 0, 0);
+      if (a.mul != nullptr && in && m < a.M) f[k] = *reinterpret_cast<const uint4*>(a.mul + o);
+      if (a.residual != nullptr && in && m < a.M) r[k] = *reinterpret_cast<const uint4*>(a.residual + o);
+    }
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float4_t v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][j][4 * g + e]) * sx[i];
+        *reinterpret_cast<float4_t*>(mine + l32 * PITCH + 32 * j + 8 * g + 4 * half) = v;
+      }
+    wave_lds_fence();
+#pragma unroll
+    for (int k = 0; k < RUNS; ++k) {
+      const float* from = mine + (k * (64 / LANES) + lane / LANES) * PITCH + c;
+      const float4_t lo = *reinterpret_cast<const float4_t*>(from), hi = *reinterpret_cast<const float4_t*>(from + 4);
+      const int64_t m = top + k * (64 / LANES);
+      if (in && m < a.M)
+        *reinterpret_cast<uint4*>(a.y + m * a.N + n) =
+            tail8<T>(a, float8_t{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]} * sw + bias, f[k], r[k]);
+    }
+    wave_lds_fence();
+  }
+}
+
+// the sums of a split of the channels, eight outputs for each thread
+template <typename T>
+__global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
+  const int64_t runs = a.M * a.N / 8, all = a.M * a.N;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < runs; i += static_cast<int64_t>(gridDim.x) * 256) {
+    int4_t lo = {0, 0, 0, 0}, hi = lo;
+    for (int s = 0; s < splits; ++s) {
+      const int4_t* p = reinterpret_cast<const int4_t*>(a.part + s * all + 8 * i);
+      lo += p[0];
+      hi += p[1];
+    }
+    const int64_t m = 8 * i / a.N, n = 8 * i - m * a.N;
+    const float sx = a.scale[m];
+    float8_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = static_cast<float>(lo[e]) * sx * a.scales[n + e];
+      v[e + 4] = static_cast<float>(hi[e]) * sx * a.scales[n + 4 + e];
+    }
+    if (a.bias != nullptr) v += load8<T>(a.bias + n);
+    uint4 f = make_uint4(0, 0, 0, 0), r = f;
+    if (a.mul != nullptr) f = *reinterpret_cast<const uint4*>(a.mul + 8 * i);
+    if (a.residual != nullptr) r = *reinterpret_cast<const uint4*>(a.residual + 8 * i);
+    *reinterpret_cast<uint4*>(a.y + 8 * i) = tail8<T>(a, v, f, r);
+  }
+}
+
+// Which kernel a product takes: the one with the least time by an estimate in microseconds, whose
+// constants were fitted (by least squares of the logarithms, 10 % rms) to 1400 timings of all
+// kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. On
+// those the choice costs 2 % more than the best one on average, 34 % at worst (64 x 8192 x 1024).
+// A CU's blocks share its matrix cores (`work` each and step) and pass their steps not faster than
+// memory answers (`wait`, `fit` of them at a time).
+struct Tile {
+  int bm, bn, fit;
+  float work, wait, once;
+};
+constexpr Tile kTiles[] = {{64, 64, 6, 0.111f, 0.183f, 0.68f},
+                           {64, 128, 4, 0.152f, 0.205f, 1.21f},
+                           {128, 128, 3, 0.233f, 0.278f, 1.85f},
+                           {128, 256, 2, 0.390f, 0.426f, 3.47f}};
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 16};
+struct Choice {
+  int tile, splits;  // tile -1: i8_rows_kernel
+};
+Choice choose(int64_t M, int64_t N, int64_t K) {
+  if (const char* env = tuning_env("AWQ_I8_CFG")) {
+    int bm = 0, bn = 0, splits = 0;
+    if (sscanf(env, "%d,%d,%d", &bm, &bn, &splits) == 3) {
+      for (int t = 0; t < 4; ++t)
+        if (kTiles[t].bm == bm && kTiles[t].bn == bn) return {t, splits};
+      return {-1, 1};
+    }
+  }
+  constexpr float kCus = 256.0f;
+  const float units = static_cast<float>((K + kI8Unit - 1) / kI8Unit), m = static_cast<float>(M), n = static_cast<float>(N);
+  auto blocks = [](int64_t v, int64_t b) { return static_cast<float>((v + b - 1) / b); };
+  const int row_blocks = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  const float rounds = blocks(N, 16) * blocks(M, 16 * row_blocks) / kCus;
+  Choice best = {-1, 1};
+  float least = 2.4f + units / 8.0f * (rounds > 1.0f ? rounds : 1.0f) *
+                           (0.31f + 0.19f * (m / 16.0f < row_blocks ? m / 16.0f : static_cast<float>(row_blocks)));
+  for (int t = 0; t < 4; ++t)
+    for (int splits : kSplits) {
+      if (splits > 1 && units < 2.0f * splits) break;
+      const Tile& k = kTiles[t];
+      const float per_cu = ceilf(blocks(M, k.bm) * blocks(N, k.bn) * splits / kCus), steps = ceilf(units / splits);
+      const float waits = k.wait * ceilf(per_cu / k.fit), works = k.work * per_cu;
+      float time = 3.69f + steps * (waits > works ? waits : works) + k.once * per_cu;
+      if (splits > 1) time += 2.66f + (8.0f * splits + 2.0f) * m * n / 7.0e6f;
+      if (time < least) {
+        least = time;
+        best = {t, splits};
+      }
+    }
+  return best;
+}
+
+template <typename T, int BM, int BN>
+hipError_t launch_tiles(const I8Args& a, int splits, hipStream_t st) {
+  constexpr int STAGES = kRing * (BM + BN) * kStep, TAIL = 4 * 32 * (BN / 2 + 4) * 4, LDS = STAGES > TAIL ? STAGES : TAIL;
+  const unsigned blocks = static_cast<unsigned>((a.M + BM - 1) / BM * ((a.N + BN - 1) / BN));
+  auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
+    const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS, done);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(kernel, dim3(blocks, splits), dim3(256), LDS, st, a);
+    return hipGetLastError();
+  };
+  static std::atomic<uint64_t> whole{0}, split{0};
+  if (splits == 1) return go(&i8_tile_kernel<T, BM, BN, false>, whole);
+  hipError_t e = go(&i8_tile_kernel<T, BM, BN, true>, split);
+  if (e != hipSuccess) return e;
+  int64_t sums = (a.M * a.N / 8 + 255) / 256;
+  if (sums > 65536) sums = 65536;
+  hipLaunchKernelGGL((i8_sum_kernel<T>), dim3(static_cast<unsigned>(sums)), dim3(256), 0, st, a, splits);
+  return hipGetLastError();
+}
+
 template <typename T>
 hipError_t launch_as(const I8Args& a, hipStream_t st) {
+  const Choice c = choose(a.M, a.N, a.K);
+  switch (c.tile) {
+    case 0: return launch_tiles<T, 64, 64>(a, c.splits, st);
+    case 1: return launch_tiles<T, 64, 128>(a, c.splits, st);
+    case 2: return launch_tiles<T, 128, 128>(a, c.splits, st);
+    case 3: return launch_tiles<T, 128, 256>(a, c.splits, st);
+    default: break;
+  }
   const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
   auto go = [&](auto kernel, int rows) {
     // blocks of rows beyond a launch's y extent go in launches of their own
@@ -132,7 +473,10 @@ hipError_t launch_as(const I8Args& a, hipStream_t st) {
 
 }  // namespace
 
-size_t gemm_i8_workspace_bytes(int64_t, int64_t, int64_t) { return 0; }
+size_t gemm_i8_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  const Choice c = choose(M, N, K);
+  return c.splits == 1 ? 0 : static_cast<size_t>(4) * c.splits * M * N;
+}
 
 hipError_t launch_gemm_i8(const awq_gemm_i8_args& p, hipStream_t st) {
   const I8Layout l = make_i8_layout(p.N, p.K);
@@ -145,6 +489,7 @@ hipError_t launch_gemm_i8(const awq_gemm_i8_args& p, hipStream_t st) {
   a.mul = static_cast<const uint16_t*>(p.mul);
   a.residual = static_cast<const uint16_t*>(p.residual);
   a.y = static_cast<uint16_t*>(p.y);
+  a.part = static_cast<int32_t*>(p.ws);
   a.M = p.M;
   a.N = p.N;
   a.q_stride = p.q_stride;
