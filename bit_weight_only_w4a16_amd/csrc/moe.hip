@@ -6,23 +6,43 @@
 // Bound by memory: each expert that some token names is read once. Which experts those are is
 // known on the device alone, so the first launch has workgroups for as many experts as the
 // ids could name (those past the last named one end at once), and each finds its expert as the
-// n-th set bit of the bits that the ids set. In the second a workgroup owns 16 outputs of all
+// n-th set bit of the bits that the ids set. One workgroup of that launch writes the plan of the
+// second: the named experts and their tokens in order. There a workgroup owns 16 outputs of all
 // tokens and walks over the named experts' rows, its wavefronts taking equal runs of units, so
-// that its load does not depend on how many experts there are.
+// that its load does not depend on how many experts there are; with few outputs, several
+// workgroups share them, and the one that ends last adds their sums.
 //
-// Weights go from memory to registers, 1 KiB per load (awq_repack's units), are dequantized
-// exactly to binary16 and meet up to 16 tokens' rows in one matrix instruction. A wavefront keeps
-// its own sums; they are added in the wavefronts' order, so results do not vary.
+// Weights go from memory to registers, 1 KiB per load (awq_repack's units), several units ahead of
+// their use; they are dequantized exactly to binary16 and meet up to 16 tokens' rows in one matrix
+// instruction. Every sum has its place and order: results do not vary.
 #include "ffn_internal.hpp"
+
+#include <type_traits>
 
 namespace awq {
 namespace {
 
-constexpr int kMostExperts = 1024, kMoeWaves = 8;
+constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX_K;
+constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kAhead = 4;                       // units of a wavefront on their way, in the first launch
+constexpr int kAheadW = 8, kAheadX = 4;         // in the second: of weights, and of rows
+constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
 
 struct Layers {  // a stack of packed layers
   const uint8_t* base;
-  int64_t bytes, scales_off, zeros_off;  // zeros_off -1: symmetric
+  int64_t bytes;
+  uint32_t scales_off, zeros_off;
+};
+
+// What the first launch tells the second (in the workspace).
+struct Plan {
+  int32_t* total;    // named experts
+  int32_t* experts;  // [pairs]: which, ascending
+  int32_t* first;    // [pairs + 1]: where an expert's tokens begin in the next two
+  int32_t* pair;     // [pairs]: token * k + j
+  float* weight;     // [pairs]
+  int32_t* ended;    // [tiles]: workgroups that have written their sums
+  float* part;       // [splits][tiles][tokens * 16]
 };
 
 struct MoeArgs {
@@ -31,18 +51,22 @@ struct MoeArgs {
   const float* weights;
   Layers gate, up, down;
   uint16_t* mid;  // [tokens * k][ffn]
+  Plan plan;
   uint16_t* y;
   int64_t x_stride, residual_stride, y_stride, inv_in_stride, inv_down_stride;
   int tokens, hidden, ffn, experts, k, sets, act;
 };
 
-// The experts that the ids name, as bits in LDS; all threads of a workgroup take part.
-__device__ __forceinline__ void find_named(const MoeArgs& a, uint32_t* bits) {
-  for (int i = threadIdx.x; i < kMostExperts / 32; i += blockDim.x) bits[i] = 0;
+// The ids in LDS (-1 where they name no expert), and the experts that they name as bits; all
+// threads of a workgroup take part.
+__device__ __forceinline__ void find_named(const MoeArgs& a, int* ids, uint32_t* bits) {
+  if (threadIdx.x < kMostExperts / 32) bits[threadIdx.x] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < a.tokens * a.k; i += blockDim.x) {
     const int e = a.ids[i];
-    if (e >= 0 && e < a.experts) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    const bool named = e >= 0 && e < a.experts;
+    ids[i] = named ? e : -1;
+    if (named) atomicOr(&bits[e >> 5], 1u << (e & 31));
   }
   __syncthreads();
 }
@@ -69,46 +93,44 @@ __device__ __forceinline__ Named count_named(const uint32_t* bits) {
 }
 
 // The tokens that name expert e, as bits (token t is lane t's); for lane t, the first j with
-// ids[t][j] == e and the sum of the weights of all such j.
+// ids[t][j] == e.
 struct Rows {
   uint64_t tokens;
   int pair;
-  float weight;
 };
-__device__ __forceinline__ Rows rows_of(const MoeArgs& a, int e) {
+__device__ __forceinline__ Rows rows_of(const MoeArgs& a, const int* ids, int e) {
   const int t = threadIdx.x & 63;
-  Rows r = {0, -1, 0.0f};
-  if (t < a.tokens) {
-    for (int j = a.k - 1; j >= 0; --j) {
-      if (a.ids[t * a.k + j] != e) continue;
-      r.pair = t * a.k + j;
-      r.weight += a.weights[t * a.k + j];
-    }
-  }
+  Rows r = {0, -1};
+  if (t < a.tokens)
+    for (int j = a.k - 1; j >= 0; --j)
+      if (ids[t * a.k + j] == e) r.pair = t * a.k + j;
   r.tokens = __ballot(r.pair >= 0);
   return r;
 }
 
-// One unit's words, scale and zero word of this lane.
+// One unit's words, scale and zero word of this lane; nothing is read where `skip` is kNoLoad.
 struct Piece {
   uint4 c;
-  uint16_t s;
-  uint32_t z;
+  uint32_t s, z;
 };
+struct Reader {  // a layer's regions of one tile of 16 outputs
+  __amdgpu_buffer_rsrc_t all;
+  uint32_t codes, scales, zeros;  // offsets of unit 0
+};
+__device__ __forceinline__ Reader reader(const Layers& l, int e, int tile, int units, int sets) {
+  const uint32_t first = static_cast<uint32_t>(tile) * units;
+  return {make_rsrc(l.base + e * l.bytes, static_cast<uint32_t>(l.bytes)), first * kUnitBytes,
+          l.scales_off + first * (2 * kTileN * sets), l.zeros_off + first * (8 * sets)};
+}
 template <bool ASYM>
-__device__ __forceinline__ Piece load_piece(const Layers& l, int64_t layer, int64_t unit, int sets, int lane) {
-  const int r = lane & 15, set = lane_set(lane >> 4, sets);
-  const uint8_t* base = l.base + layer * l.bytes;
+__device__ __forceinline__ Piece load_piece(const Reader& r, int unit, int sets, int lane, uint32_t skip) {
+  const uint32_t set = lane_set(lane >> 4, sets), u = static_cast<uint32_t>(unit);
   Piece p;
-  typedef unsigned int u4 __attribute__((ext_vector_type(4)));
-  const u4 c = __builtin_nontemporal_load(reinterpret_cast<const u4*>(base + unit * kUnitBytes) + lane);
-  p.c = make_uint4(c[0], c[1], c[2], c[3]);
-  p.s = reinterpret_cast<const uint16_t*>(base + l.scales_off)[(unit * sets + set) * kTileN + r];
-  p.z = ASYM ? reinterpret_cast<const uint32_t*>(base + l.zeros_off)[(unit * sets + set) * 2 + (r >> 3)] : 0u;
+  p.c = buf_load16_stream(r.all, 16u * lane + skip, r.codes + u * kUnitBytes);
+  p.s = buf_load2(r.all, 2u * (kTileN * set + (lane & 15)) + skip, r.scales + u * (2 * kTileN * sets));
+  p.z = ASYM ? buf_load4(r.all, 4u * (2 * set + ((lane & 15) >> 3)) + skip, r.zeros + u * (8 * sets)) : 0u;
   return p;
 }
-
-// acc += rows (four operands of 8 channels each) . the unit's weights
 struct Dequant {
   half2_t scale;
   uint32_t nz1024, nz64;
@@ -116,178 +138,383 @@ struct Dequant {
 template <bool ASYM>
 __device__ __forceinline__ Dequant constants(const Piece& p, int lane) {
   const uint32_t z = ASYM ? (p.z >> (4 * (lane & 7))) & 15u : 8u;
-  return {as_h2(p.s | static_cast<uint32_t>(p.s) << 16), neg_off1024(z), neg_off64(z)};
+  return {as_h2(p.s | p.s << 16), neg_off1024(z), neg_off64(z)};
 }
 __device__ __forceinline__ half8_t weights8(const Piece& p, int i, const Dequant& d) {
   half2_t q[4];
   dequant_word(i == 0 ? p.c.x : i == 1 ? p.c.y : i == 2 ? p.c.z : p.c.w, d.nz1024, d.nz64, d.scale, q);
   return half8_t{q[0].x, q[0].y, q[1].x, q[1].y, q[2].x, q[2].y, q[3].x, q[3].y};
 }
+__device__ __forceinline__ half8_t load_half8(const uint16_t* p) {
+  return __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(p));
+}
 
-// grid: tiles of 16 ffn outputs, experts that may be named
-template <bool ASYM>
-__global__ void __launch_bounds__(64 * kMoeWaves) moe_up_kernel(MoeArgs a) {
+// The plan, by one workgroup. Where an expert's tokens stand among each other depends on the
+// order of the atomics, what is computed for each of them does not.
+__device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, const uint32_t* bits, const Named& named,
+                                           int tiles) {
+  __shared__ int before[kMostExperts / 32];
+  __shared__ int begin[kMostExperts], taken[kMostExperts];
+  const int lane = threadIdx.x & 63, pairs = a.tokens * a.k;
+  if (threadIdx.x < kMostExperts / 32) {
+    before[lane] = named.before;
+    uint32_t word = named.word;
+    for (int at = named.before; word != 0; ++at, word &= word - 1) a.plan.experts[at] = 32 * lane + __builtin_ctz(word);
+  }
+  for (int i = threadIdx.x; i < named.total; i += blockDim.x) taken[i] = 0;
+  for (int i = threadIdx.x; i < tiles; i += blockDim.x) a.plan.ended[i] = 0;
+  __syncthreads();
+  // a pair's expert by its place among the named ones, -1 where an earlier j of the token names it
+  auto place = [&](int i) {
+    const int e = ids[i];
+    if (e < 0) return -1;
+    for (int j = i / a.k * a.k; j < i; ++j)
+      if (ids[j] == e) return -1;
+    return before[e >> 5] + static_cast<int>(__popc(bits[e >> 5] & ((1u << (e & 31)) - 1)));
+  };
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    const int at = place(i);
+    if (at >= 0) atomicAdd(&taken[at], 1);
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {  // begin[i] = the sum of taken before i
+    int base = 0;
+    for (int i0 = 0; i0 < named.total; i0 += 64) {
+      const int mine = i0 + lane < named.total ? taken[i0 + lane] : 0;
+      int upto = mine;
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1) {
+        const int other = __shfl_up(upto, s);
+        if (lane >= s) upto += other;
+      }
+      if (i0 + lane < named.total) begin[i0 + lane] = base + upto - mine;
+      base += __shfl(upto, 63);
+    }
+    if (lane == 0) {
+      a.plan.first[named.total] = base;
+      *a.plan.total = named.total;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < named.total; i += blockDim.x) {
+    a.plan.first[i] = begin[i];
+    taken[i] = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
+    const int at = place(i);
+    if (at < 0) continue;
+    const int to = begin[at] + atomicAdd(&taken[at], 1);
+    float weight = a.weights[i];
+    for (int j = i + 1; j < (i / a.k + 1) * a.k; ++j)
+      if (ids[j] == ids[i]) weight += a.weights[j];
+    a.plan.pair[to] = i;
+    a.plan.weight[to] = weight;
+  }
+}
+
+// Wavefronts own 16 ffn outputs, SHARE of them the same ones with every SHARE-th unit each.
+// grid: the outputs' workgroups and one for the plan, experts that may be named
+template <bool ASYM, int SHARE, int CHUNKS>
+__global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
+  constexpr int TILES = kUpWaves / SHARE;
   __shared__ uint32_t bits[kMostExperts / 32];
+  __shared__ int ids[kMostPairs];
   __shared__ int row_pair[64];
-  __shared__ float red[kMoeWaves][2][16][16];
+  __shared__ float4_t red[SHARE == 1 ? 1 : kUpWaves][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int r = lane & 15, p = lane >> 4;
-  find_named(a, bits);
+  const int r = lane & 15, p = lane >> 4, part = wave % SHARE;
+  const int tiles = a.ffn / kTileN, slot = blockIdx.y;
+  const bool plans = blockIdx.x == gridDim.x - 1;
+  if (plans && slot != 0) return;
+  find_named(a, ids, bits);
   const Named named = count_named(bits);
-  const int slot = blockIdx.y;
+  if (plans) {
+    write_plan(a, ids, bits, named, a.hidden / kTileN);
+    return;
+  }
   if (slot >= named.total) return;
   const uint64_t holds = __ballot(named.before <= slot && slot < named.before + __popc(named.word));
   const int word_at = __builtin_ctzll(holds);
   uint32_t word = __shfl(named.word, word_at);
   for (int skip = slot - __shfl(named.before, word_at); skip > 0; --skip) word &= word - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * word_at + __builtin_ctz(word));
-  const Rows rows = rows_of(a, e);
-  const int count = __popcll(rows.tokens);
+
+  const int tile = blockIdx.x * TILES + wave / SHARE;  // past the last one: nothing is loaded or stored
+  const int units = tile < tiles ? a.hidden / kGroup : 0;
+  const Reader rg = reader(a.gate, e, tile, units, a.sets), ru = reader(a.up, e, tile, units, a.sets);
+  Piece pg[kAhead], pu[kAhead];
+  auto load = [&](int i, int unit) {
+    const uint32_t skip = unit < units ? 0u : kNoLoad;
+    pg[i] = load_piece<ASYM>(rg, unit, a.sets, lane, skip);
+    pu[i] = load_piece<ASYM>(ru, unit, a.sets, lane, skip);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) load(i, part + SHARE * i);
+
+  const Rows rows = rows_of(a, ids, e);
+  const int count = __popcll(rows.tokens), chunks = (count + 15) / 16;
   if (wave == 0 && rows.pair >= 0) row_pair[__popcll(rows.tokens & ((uint64_t{1} << lane) - 1))] = rows.pair;
   __syncthreads();
-
-  const int64_t tile = blockIdx.x;
-  const int units = a.hidden / kGroup;
+  // rows past the last repeat it; their results are dropped
+  const uint16_t* x[CHUNKS];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) x[c] = a.x + row_pair[min(16 * c + r, count - 1)] / a.k * a.x_stride + 32 * p;
   const uint16_t* inv = a.inv_in == nullptr ? nullptr : a.inv_in + e * a.inv_in_stride + 32 * p;
-  for (int m0 = 0; m0 < count; m0 += 16) {
-    const bool live = m0 + r < count;
-    const uint16_t* x = a.x + (live ? row_pair[m0 + r] / a.k : 0) * a.x_stride + 32 * p;
-    float4_t g = {0.0f, 0.0f, 0.0f, 0.0f}, u = g;
-    if (wave < units) {
-      Piece pg = load_piece<ASYM>(a.gate, e, tile * units + wave, a.sets, lane);
-      Piece pu = load_piece<ASYM>(a.up, e, tile * units + wave, a.sets, lane);
-      for (int at = wave; at < units; at += kMoeWaves) {
-        const Piece cg = pg, cu = pu;
-        if (at + kMoeWaves < units) {
-          pg = load_piece<ASYM>(a.gate, e, tile * units + at + kMoeWaves, a.sets, lane);
-          pu = load_piece<ASYM>(a.up, e, tile * units + at + kMoeWaves, a.sets, lane);
-        }
-        uint4 xv[4];
+  float4_t g[CHUNKS], u[CHUNKS];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) g[c] = u[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  for (int at0 = part; at0 < units; at0 += SHARE * kAhead) {
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int at = at0 + SHARE * n;
+      if (at >= units) break;
+      const Dequant dg = constants<ASYM>(pg[n], lane), du = constants<ASYM>(pu[n], lane);
+      half8_t xf[4], wg[4], wu[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        xf[i] = load_half8(x[0] + at * kGroup + 8 * i);
+        wg[i] = weights8(pg[n], i, dg);
+        wu[i] = weights8(pu[n], i, du);
+      }
+      load(n, at + SHARE * kAhead);
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        if (c >= chunks) break;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          xv[i] = make_uint4(0, 0, 0, 0);
-          if (live) xv[i] = *reinterpret_cast<const uint4*>(x + at * kGroup + 8 * i);
-        }
-        if (inv != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            xv[i] = scale_x8(xv[i], *reinterpret_cast<const uint4*>(inv + at * kGroup + 8 * i));
-        }
-        const Dequant dg = constants<ASYM>(cg, lane), du = constants<ASYM>(cu, lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const half8_t xf = __builtin_bit_cast(half8_t, xv[i]);
-          g = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, weights8(cg, i, dg), g, 0, 0, 0);
-          u = __builtin_amdgcn_mfma_f32_16x16x32_f16(xf, weights8(cu, i, du), u, 0, 0, 0);
+          if (c > 0) xf[i] = load_half8(x[c] + at * kGroup + 8 * i);
+          const half8_t f = inv == nullptr ? xf[i] : xf[i] * load_half8(inv + at * kGroup + 8 * i);
+          g[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, wg[i], g[c], 0, 0, 0);
+          u[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, wu[i], u[c], 0, 0, 0);
         }
       }
     }
-    __syncthreads();  // the sums of the rows before these have been read
+  }
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    if (c >= chunks) break;
+    if constexpr (SHARE > 1) {
+      if (c > 0) __syncthreads();  // the sums of the rows before these have been read
+      red[wave][0][lane] = g[c];
+      red[wave][1][lane] = u[c];
+      __syncthreads();
+      if (part != 0) continue;
+#pragma unroll
+      for (int w = 1; w < SHARE; ++w) {
+        g[c] += red[wave + w][0][lane];
+        u[c] += red[wave + w][1][lane];
+      }
+    }
+    if (tile >= tiles) continue;
+    const int f = tile * kTileN + r;
+    const float scale = a.inv_down == nullptr ? 1.0f : f16_to_f32(a.inv_down[e * a.inv_down_stride + f]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      red[wave][0][4 * p + j][r] = g[j];
-      red[wave][1][4 * p + j][r] = u[j];
-    }
-    __syncthreads();
-    const int m = threadIdx.x / 16, n = threadIdx.x % 16;
-    if (m < 16 && m0 + m < count) {
-      float sg = 0.0f, su = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kMoeWaves; ++w) {
-        sg += red[w][0][m][n];
-        su += red[w][1][m][n];
-      }
-      const int f = static_cast<int>(tile) * kTileN + n;
-      float v = activate(sg, a.act) * su;
-      if (a.inv_down != nullptr) v *= f16_to_f32(a.inv_down[e * a.inv_down_stride + f]);
-      a.mid[static_cast<int64_t>(row_pair[m0 + m]) * a.ffn + f] =
-          __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+      const int m = 16 * c + 4 * p + j;
+      if (m >= count) continue;
+      float v = activate(g[c][j], a.act) * u[c][j];
+      if (a.inv_down != nullptr) v *= scale;
+      a.mid[static_cast<int64_t>(row_pair[m]) * a.ffn + f] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
     }
   }
 }
 
-// grid: tiles of 16 hidden outputs. Dynamic LDS: [waves][tokens][16] float32.
+// grid: tiles of 16 hidden outputs, splits of the named experts' units. Dynamic LDS:
+// [waves][tokens][16] float32.
 template <bool ASYM>
-__global__ void __launch_bounds__(64 * kMoeWaves) moe_down_kernel(MoeArgs a) {
-  __shared__ uint32_t bits[kMostExperts / 32];
-  __shared__ uint16_t named_list[kMostExperts];
-  __shared__ int row_pair[kMoeWaves][64];
-  __shared__ float row_weight[kMoeWaves][64];
+__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
+  __shared__ int experts[kMostExperts], first[kMostExperts + 1];
+  __shared__ int row_pair[kMostPairs];
+  __shared__ float row_weight[kMostPairs];
+  __shared__ int last_one;
   extern __shared__ float sums[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, p = lane >> 4;
+  const int tile = blockIdx.x, tiles = gridDim.x, pairs = a.tokens * a.k;
   float* mine = sums + wave * a.tokens * 16;
   for (int i = lane; i < a.tokens * 16; i += 64) mine[i] = 0.0f;
-  find_named(a, bits);
-  const Named named = count_named(bits);
-  if (wave == 0) {
-    uint32_t word = named.word;
-    for (int at = named.before; word != 0; ++at, word &= word - 1)
-      named_list[at] = static_cast<uint16_t>(32 * lane + __builtin_ctz(word));
+  const int total = *a.plan.total;
+  for (int i = threadIdx.x; i <= pairs; i += 64 * kDownWaves) {
+    // what lies behind the last named expert (of kMostExperts at most) is not used
+    if (i <= kMostExperts) first[i] = a.plan.first[i];
+    if (i < kMostExperts && i < pairs) experts[i] = a.plan.experts[i];
+    if (i < pairs) {
+      row_pair[i] = a.plan.pair[i];
+      row_weight[i] = a.plan.weight[i];
+    }
   }
   __syncthreads();
 
-  const int64_t tile = blockIdx.x;
-  const int units = a.ffn / kGroup, all = __builtin_amdgcn_readfirstlane(named.total) * units;
-  int at = static_cast<int>(static_cast<int64_t>(all) * wave / kMoeWaves);
-  const int end = static_cast<int>(static_cast<int64_t>(all) * (wave + 1) / kMoeWaves);
-  while (at < end) {
-    const int slot = at / units, e = __builtin_amdgcn_readfirstlane(named_list[slot]);
-    const int first = at - slot * units, last = min(units, end - slot * units);
-    at = slot * units + last;
-    const Rows rows = rows_of(a, e);
-    const int count = __popcll(rows.tokens);
-    wave_lds_fence();  // the rows of the expert before have been read
-    if (rows.pair >= 0) {
-      const int row = __popcll(rows.tokens & ((uint64_t{1} << lane) - 1));
-      row_pair[wave][row] = rows.pair;
-      row_weight[wave][row] = rows.weight;
+  // this wavefront's run of the named experts' units
+  const int units = a.ffn / kGroup, all = total * units, waves = kDownWaves * gridDim.y;
+  const int number = blockIdx.y * kDownWaves + wave;
+  const int begin = static_cast<int>(static_cast<int64_t>(all) * number / waves);
+  const int end = static_cast<int>(static_cast<int64_t>(all) * (number + 1) / waves);
+  struct Cursor {
+    int slot, unit;
+  };
+  auto next = [&](Cursor& c) {
+    if (++c.unit == units) {
+      c.unit = 0;
+      ++c.slot;
     }
-    wave_lds_fence();
-    for (int m0 = 0; m0 < count; m0 += 16) {
-      const bool live = m0 + r < count;
-      const uint16_t* x = a.mid + static_cast<int64_t>(live ? row_pair[wave][m0 + r] : 0) * a.ffn + 32 * p;
-      float4_t d = {0.0f, 0.0f, 0.0f, 0.0f};
-      Piece next = load_piece<ASYM>(a.down, e, tile * units + first, a.sets, lane);
-      for (int u = first; u < last; ++u) {
-        const Piece c = next;
-        if (u + 1 < last) next = load_piece<ASYM>(a.down, e, tile * units + u + 1, a.sets, lane);
-        const Dequant dq = constants<ASYM>(c, lane);
+  };
+  Piece pw[kAheadW];
+  half8_t px[kAheadX][4];  // of the expert's first 16 rows
+  auto load_w = [&](Piece& w, const Cursor& c, int at) {
+    const bool real = at < end;
+    const int e = __builtin_amdgcn_readfirstlane(experts[real ? c.slot : 0]);
+    w = load_piece<ASYM>(reader(a.down, e, tile, units, a.sets), real ? c.unit : 0, a.sets, lane, real ? 0u : kNoLoad);
+  };
+  auto load_x = [&](half8_t (&x)[4], const Cursor& c, int at) {
+    const bool real = at < end;
+    const int slot = real ? c.slot : 0, row = min(first[slot] + r, first[slot + 1] - 1);
+    const uint16_t* from = a.mid + static_cast<int64_t>(row_pair[row]) * a.ffn + (real ? c.unit : 0) * kGroup + 32 * p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = load_half8(from + 8 * i);
+  };
+  if (begin < end) {
+    Cursor now = {begin / units, begin % units}, ahead_w = now, ahead_x = now;
+#pragma unroll
+    for (int i = 0; i < kAheadW; ++i) {
+      load_w(pw[i], ahead_w, begin + i);
+      next(ahead_w);
+    }
+#pragma unroll
+    for (int i = 0; i < kAheadX; ++i) {
+      load_x(px[i], ahead_x, begin + i);
+      next(ahead_x);
+    }
+    float4_t d[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) d[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int at0 = begin; at0 < end; at0 += kAheadW) {
+#pragma unroll
+      for (int n = 0; n < kAheadW; ++n) {
+        const int at = at0 + n;
+        if (at >= end) break;
+        const int row0 = first[now.slot], count = __builtin_amdgcn_readfirstlane(first[now.slot + 1] - row0);
+        const Dequant dq = constants<ASYM>(pw[n], lane);
+        half8_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint4 xv = make_uint4(0, 0, 0, 0);
-          if (live) xv = *reinterpret_cast<const uint4*>(x + u * kGroup + 8 * i);
-          d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8_t, xv), weights8(c, i, dq), d, 0, 0, 0);
+          w[i] = weights8(pw[n], i, dq);
+          d[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % kAheadX][i], w[i], d[0], 0, 0, 0);
         }
-      }
+        load_w(pw[n], ahead_w, at + kAheadW);
+        next(ahead_w);
+        load_x(px[n % kAheadX], ahead_x, at + kAheadX);
+        next(ahead_x);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = m0 + 4 * p + j;
-        if (m < count) mine[row_pair[wave][m] / a.k * 16 + r] += row_weight[wave][m] * d[j];
+        for (int c = 1; c < kChunks; ++c) {
+          if (16 * c >= count) break;
+          const uint16_t* x = a.mid + static_cast<int64_t>(row_pair[row0 + min(16 * c + r, count - 1)]) * a.ffn +
+                              now.unit * kGroup + 32 * p;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(load_half8(x + 8 * i), w[i], d[c], 0, 0, 0);
+        }
+        if (now.unit == units - 1 || at + 1 == end) {  // this wavefront's share of the expert is complete
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            if (16 * c >= count) break;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int m = 16 * c + 4 * p + j;
+              if (m < count) mine[row_pair[row0 + m] / a.k * 16 + r] += row_weight[row0 + m] * d[c][j];
+            }
+            d[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+          }
+          wave_lds_fence();
+        }
+        next(now);
       }
-      wave_lds_fence();
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.tokens * 16; i += 64 * kMoeWaves) {
-    const int t = i / 16, n = static_cast<int>(tile) * 16 + i % 16;
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kMoeWaves; ++w) v += sums[w * a.tokens * 16 + i];
+  const int outputs = a.tokens * 16;
+  auto store = [&](int i, float v) {
+    const int t = i / 16, n = tile * 16 + i % 16;
     if (a.residual != nullptr) v += f16_to_f32(a.residual[t * a.residual_stride + n]);
     a.y[t * a.y_stride + n] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+  };
+  auto sum = [&](int i) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kDownWaves; ++w) v += sums[w * outputs + i];
+    return v;
+  };
+  if (gridDim.y == 1) {
+    for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves) store(i, sum(i));
+    return;
   }
+  // The last workgroup of a tile adds all parts, in their order. They go through the memory that
+  // all XCDs see, one by one: an exchange has been seen by all when its result is there, and the
+  // barrier waits for it (a fence writes back all that an XCD's cache holds, in every workgroup:
+  // 57 us instead of 9 for 23 MB of weights).
+  uint32_t seen = 0;
+  for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves)
+    seen |= __hip_atomic_exchange(reinterpret_cast<uint32_t*>(a.plan.part) +
+                                      (static_cast<int64_t>(blockIdx.y) * tiles + tile) * outputs + i,
+                                  __builtin_bit_cast(uint32_t, sum(i)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("" : : "v"(seen) : "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last_one = __hip_atomic_fetch_add(&a.plan.ended[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+               static_cast<int>(gridDim.y) - 1;
+  __syncthreads();
+  if (!last_one) return;
+  for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves) {
+    float v = 0.0f;
+    for (int s = 0; s < static_cast<int>(gridDim.y); ++s)
+      v += __hip_atomic_load(a.plan.part + (static_cast<int64_t>(s) * tiles + tile) * outputs + i, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+    store(i, v);
+  }
+}
+
+// Workgroups that share 16 outputs in the second launch, so that at least one runs on each CU.
+int down_splits(int hidden) {
+  const int tiles = hidden / kTileN;
+  const int splits = (256 + tiles - 1) / tiles;
+  return splits > 16 ? 16 : splits;
 }
 
 Layers make_layers(const void* base, int64_t N, int64_t K, int32_t group, int32_t fmt) {
   const PackedLayout l = make_layout(N, K, group, fmt);
-  return {static_cast<const uint8_t*>(base), l.total_bytes, l.scales_off, l.zeros_off};
+  return {static_cast<const uint8_t*>(base), l.total_bytes, static_cast<uint32_t>(l.scales_off),
+          static_cast<uint32_t>(l.zeros_off < 0 ? 0 : l.zeros_off)};
+}
+
+// The workspace: mid, then the plan. Returns its size.
+size_t lay_out(int64_t tokens, int hidden, int ffn, int k, void* ws, uint16_t** mid, Plan* plan) {
+  const size_t pairs = static_cast<size_t>(tokens) * k, tiles = hidden / kTileN;
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 15) / 16 * 16;
+    return static_cast<char*>(ws) + here;
+  };
+  uint16_t* m = reinterpret_cast<uint16_t*>(take(2 * pairs * ffn));
+  Plan p;
+  p.total = reinterpret_cast<int32_t*>(take(4));
+  p.experts = reinterpret_cast<int32_t*>(take(4 * pairs));
+  p.first = reinterpret_cast<int32_t*>(take(4 * (pairs + 1)));
+  p.pair = reinterpret_cast<int32_t*>(take(4 * pairs));
+  p.weight = reinterpret_cast<float*>(take(4 * pairs));
+  p.ended = reinterpret_cast<int32_t*>(take(4 * tiles));
+  const int splits = down_splits(hidden);
+  p.part = reinterpret_cast<float*>(take(splits == 1 ? 0 : 4 * splits * tiles * tokens * 16));
+  if (mid != nullptr) *mid = m;
+  if (plan != nullptr) *plan = p;
+  return at;
 }
 
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t tokens, int32_t, int32_t ffn, int32_t k) {
-  return static_cast<size_t>(2) * tokens * k * ffn;
+size_t moe_workspace_bytes(int64_t tokens, int32_t hidden, int32_t ffn, int32_t k) {
+  return lay_out(tokens, hidden, ffn, k, nullptr, nullptr, nullptr);
 }
 
 hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
@@ -301,7 +528,7 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   a.gate = make_layers(p.gate, p.ffn, p.hidden, p.group, p.fmt);
   a.up = make_layers(p.up, p.ffn, p.hidden, p.group, p.fmt);
   a.down = make_layers(p.down, p.hidden, p.ffn, p.group, p.fmt);
-  a.mid = static_cast<uint16_t*>(p.ws);
+  lay_out(p.tokens, p.hidden, p.ffn, p.k, p.ws, &a.mid, &a.plan);
   a.y = p.y;
   a.x_stride = p.x_stride;
   a.residual_stride = p.residual_stride;
@@ -318,12 +545,25 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   const int64_t pairs = p.tokens * p.k;
   const int slots = static_cast<int>(pairs < p.experts ? pairs : p.experts);
   const bool asym = p.fmt == AWQ_FMT_ASYM;
-  hipLaunchKernelGGL((asym ? &moe_up_kernel<true> : &moe_up_kernel<false>), dim3(p.ffn / kTileN, slots),
-                     dim3(64 * kMoeWaves), 0, st, a);
+  // wavefronts that share 16 outputs, so that at least about 1024 run
+  const int outputs = p.ffn / kTileN, all = outputs * slots;
+  auto up = [&](auto kernel, int share) {
+    const unsigned groups = static_cast<unsigned>((outputs * share + kUpWaves - 1) / kUpWaves);
+    hipLaunchKernelGGL(kernel, dim3(groups + 1, slots), dim3(64 * kUpWaves), 0, st, a);
+  };
+  auto up_chunks = [&](auto wide, auto narrow, int share) { a.tokens > 16 ? up(wide, share) : up(narrow, share); };
+  auto up_fmt = [&](auto fmt) {
+    constexpr bool ASYM = decltype(fmt)::value;
+    if (all >= 1024) return up_chunks(&moe_up_kernel<ASYM, 1, kChunks>, &moe_up_kernel<ASYM, 1, 1>, 1);
+    if (all >= 512) return up_chunks(&moe_up_kernel<ASYM, 2, kChunks>, &moe_up_kernel<ASYM, 2, 1>, 2);
+    return up_chunks(&moe_up_kernel<ASYM, 4, kChunks>, &moe_up_kernel<ASYM, 4, 1>, 4);
+  };
+  asym ? up_fmt(std::true_type{}) : up_fmt(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((asym ? &moe_down_kernel<true> : &moe_down_kernel<false>), dim3(p.hidden / kTileN),
-                     dim3(64 * kMoeWaves), static_cast<size_t>(4) * kMoeWaves * a.tokens * 16, st, a);
+  hipLaunchKernelGGL((asym ? &moe_down_kernel<true> : &moe_down_kernel<false>),
+                     dim3(p.hidden / kTileN, down_splits(p.hidden)), dim3(64 * kDownWaves),
+                     static_cast<size_t>(4) * kDownWaves * a.tokens * 16, st, a);
   return hipGetLastError();
 }
 
