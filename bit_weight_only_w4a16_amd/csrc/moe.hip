@@ -24,8 +24,10 @@ namespace {
 
 constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX_K;
 constexpr int kUpWaves = 4, kDownWaves = 8;
-constexpr int kAhead = 4;                       // units of a wavefront on their way, in the first launch
-constexpr int kAheadW = 8, kAheadX = 4;         // in the second: of weights, and of rows
+// Units of a wavefront on their way: in the first launch by its number of tiles (two layers'
+// weights each), in the second of weights and of rows.
+constexpr int up_ahead(int wide) { return wide == 4 ? 2 : wide == 2 ? 3 : 4; }
+constexpr int kAheadW = 8, kAheadX = 4;
 constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
 
 struct Layers {  // a stack of packed layers
@@ -213,15 +215,17 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
   }
 }
 
-// Wavefronts own 16 ffn outputs, SHARE of them the same ones with every SHARE-th unit each.
+// Wavefronts own WIDE tiles of 16 ffn outputs, SHARE wavefronts the same ones with every SHARE-th
+// unit each. The rows' operands of a unit serve all of a wavefront's tiles (with one tile each, the
+// rows' loads took a fifth to a quarter of the time).
 // grid: the outputs' workgroups and one for the plan, experts that may be named
-template <bool ASYM, int SHARE, int CHUNKS>
+template <bool ASYM, int WIDE, int SHARE, int CHUNKS>
 __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
-  constexpr int TILES = kUpWaves / SHARE;
+  constexpr int TILES = WIDE * kUpWaves / SHARE, AHEAD = up_ahead(WIDE);
   __shared__ uint32_t bits[kMostExperts / 32];
   __shared__ int ids[kMostPairs];
   __shared__ int row_pair[64];
-  __shared__ float4_t red[SHARE == 1 ? 1 : kUpWaves][2][64];
+  __shared__ float4_t red[SHARE == 1 ? 1 : kUpWaves][WIDE][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, p = lane >> 4, part = wave % SHARE;
   const int tiles = a.ffn / kTileN, slot = blockIdx.y;
@@ -240,17 +244,24 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   for (int skip = slot - __shfl(named.before, word_at); skip > 0; --skip) word &= word - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * word_at + __builtin_ctz(word));
 
-  const int tile = blockIdx.x * TILES + wave / SHARE;  // past the last one: nothing is loaded or stored
-  const int units = tile < tiles ? a.hidden / kGroup : 0;
-  const Reader rg = reader(a.gate, e, tile, units, a.sets), ru = reader(a.up, e, tile, units, a.sets);
-  Piece pg[kAhead], pu[kAhead];
+  const int units = a.hidden / kGroup, tile0 = blockIdx.x * TILES + wave / SHARE * WIDE;
+  Reader rg[WIDE], ru[WIDE];  // of a tile past the last one, the last one's: its results are dropped
+#pragma unroll
+  for (int t = 0; t < WIDE; ++t) {
+    rg[t] = reader(a.gate, e, min(tile0 + t, tiles - 1), units, a.sets);
+    ru[t] = reader(a.up, e, min(tile0 + t, tiles - 1), units, a.sets);
+  }
+  Piece pg[AHEAD][WIDE], pu[AHEAD][WIDE];
   auto load = [&](int i, int unit) {
     const uint32_t skip = unit < units ? 0u : kNoLoad;
-    pg[i] = load_piece<ASYM>(rg, unit, a.sets, lane, skip);
-    pu[i] = load_piece<ASYM>(ru, unit, a.sets, lane, skip);
+#pragma unroll
+    for (int t = 0; t < WIDE; ++t) {
+      pg[i][t] = load_piece<ASYM>(rg[t], unit, a.sets, lane, skip);
+      pu[i][t] = load_piece<ASYM>(ru[t], unit, a.sets, lane, skip);
+    }
   };
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) load(i, part + SHARE * i);
+  for (int i = 0; i < AHEAD; ++i) load(i, part + SHARE * i);
 
   const Rows rows = rows_of(a, ids, e);
   const int count = __popcll(rows.tokens), chunks = (count + 15) / 16;
@@ -261,35 +272,46 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) x[c] = a.x + row_pair[min(16 * c + r, count - 1)] / a.k * a.x_stride + 32 * p;
   const uint16_t* inv = a.inv_in == nullptr ? nullptr : a.inv_in + e * a.inv_in_stride + 32 * p;
-  float4_t g[CHUNKS], u[CHUNKS];
+  auto load_x = [&](const uint16_t* from, int unit, half8_t (&f)[4]) {
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) g[c] = u[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) {
+      f[i] = load_half8(from + unit * kGroup + 8 * i);
+      if (inv != nullptr) f[i] *= load_half8(inv + unit * kGroup + 8 * i);
+    }
+  };
+  float4_t g[CHUNKS][WIDE], u[CHUNKS][WIDE];
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+    for (int t = 0; t < WIDE; ++t) g[c][t] = u[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int at0 = part; at0 < units; at0 += SHARE * kAhead) {
+  for (int at0 = part; at0 < units; at0 += SHARE * AHEAD) {
 #pragma unroll
-    for (int n = 0; n < kAhead; ++n) {
+    for (int n = 0; n < AHEAD; ++n) {
       const int at = at0 + SHARE * n;
       if (at >= units) break;
-      const Dequant dg = constants<ASYM>(pg[n], lane), du = constants<ASYM>(pu[n], lane);
-      half8_t xf[4], wg[4], wu[4];
+      half8_t f[CHUNKS][4];
+      load_x(x[0], at, f[0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        xf[i] = load_half8(x[0] + at * kGroup + 8 * i);
-        wg[i] = weights8(pg[n], i, dg);
-        wu[i] = weights8(pu[n], i, du);
-      }
-      load(n, at + SHARE * kAhead);
+      for (int c = 1; c < CHUNKS; ++c)
+        if (c < chunks) load_x(x[c], at, f[c]);
 #pragma unroll
-      for (int c = 0; c < CHUNKS; ++c) {
-        if (c >= chunks) break;
+      for (int t = 0; t < WIDE; ++t) {
+        const Dequant dg = constants<ASYM>(pg[n][t], lane), du = constants<ASYM>(pu[n][t], lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          if (c > 0) xf[i] = load_half8(x[c] + at * kGroup + 8 * i);
-          const half8_t f = inv == nullptr ? xf[i] : xf[i] * load_half8(inv + at * kGroup + 8 * i);
-          g[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, wg[i], g[c], 0, 0, 0);
-          u[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, wu[i], u[c], 0, 0, 0);
+          const half8_t wg = weights8(pg[n][t], i, dg), wu = weights8(pu[n][t], i, du);
+          g[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wg, g[0][t], 0, 0, 0);
+          u[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wu, u[0][t], 0, 0, 0);
+#pragma unroll
+          for (int c = 1; c < CHUNKS; ++c) {
+            if (c >= chunks) break;
+            g[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wg, g[c][t], 0, 0, 0);
+            u[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wu, u[c][t], 0, 0, 0);
+          }
         }
       }
+      load(n, at + SHARE * AHEAD);
     }
   }
 #pragma unroll
@@ -297,26 +319,37 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
     if (c >= chunks) break;
     if constexpr (SHARE > 1) {
       if (c > 0) __syncthreads();  // the sums of the rows before these have been read
-      red[wave][0][lane] = g[c];
-      red[wave][1][lane] = u[c];
-      __syncthreads();
-      if (part != 0) continue;
 #pragma unroll
-      for (int w = 1; w < SHARE; ++w) {
-        g[c] += red[wave + w][0][lane];
-        u[c] += red[wave + w][1][lane];
+      for (int t = 0; t < WIDE; ++t) {
+        red[wave][t][0][lane] = g[c][t];
+        red[wave][t][1][lane] = u[c][t];
       }
+      __syncthreads();
     }
-    if (tile >= tiles) continue;
-    const int f = tile * kTileN + r;
-    const float scale = a.inv_down == nullptr ? 1.0f : f16_to_f32(a.inv_down[e * a.inv_down_stride + f]);
+    // the wavefronts that share tiles divide them among themselves
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = 16 * c + 4 * p + j;
-      if (m >= count) continue;
-      float v = activate(g[c][j], a.act) * u[c][j];
-      if (a.inv_down != nullptr) v *= scale;
-      a.mid[static_cast<int64_t>(row_pair[m]) * a.ffn + f] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+    for (int t = 0; t < WIDE; ++t) {
+      if (t % SHARE != part || tile0 + t >= tiles) continue;
+      float4_t sg = g[c][t], su = u[c][t];
+      if constexpr (SHARE > 1) {
+        const int w0 = wave - part;
+        sg = red[w0][t][0][lane];
+        su = red[w0][t][1][lane];
+#pragma unroll
+        for (int w = 1; w < SHARE; ++w) {
+          sg += red[w0 + w][t][0][lane];
+          su += red[w0 + w][t][1][lane];
+        }
+      }
+      const int out = (tile0 + t) * kTileN + r;
+      const float scale = a.inv_down == nullptr ? 1.0f : f16_to_f32(a.inv_down[e * a.inv_down_stride + out]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int m = 16 * c + 4 * p + j;
+        if (m >= count) continue;
+        const float v = activate(sg[j], a.act) * su[j] * scale;
+        a.mid[static_cast<int64_t>(row_pair[m]) * a.ffn + out] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+      }
     }
   }
 }
@@ -545,18 +578,23 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   const int64_t pairs = p.tokens * p.k;
   const int slots = static_cast<int>(pairs < p.experts ? pairs : p.experts);
   const bool asym = p.fmt == AWQ_FMT_ASYM;
-  // wavefronts that share 16 outputs, so that at least about 1024 run
-  const int outputs = p.ffn / kTileN, all = outputs * slots;
-  auto up = [&](auto kernel, int share) {
-    const unsigned groups = static_cast<unsigned>((outputs * share + kUpWaves - 1) / kUpWaves);
+  // As many tiles for a wavefront as leave about 1024 wavefronts; up to four wavefronts share
+  // tiles. More than 16 rows for an expert take twice the registers for each tile.
+  const int tiles = p.ffn / kTileN, all = tiles * slots;
+  auto up = [&](auto kernel, int per_group) {
+    const unsigned groups = static_cast<unsigned>((tiles + per_group - 1) / per_group);
     hipLaunchKernelGGL(kernel, dim3(groups + 1, slots), dim3(64 * kUpWaves), 0, st, a);
   };
-  auto up_chunks = [&](auto wide, auto narrow, int share) { a.tokens > 16 ? up(wide, share) : up(narrow, share); };
   auto up_fmt = [&](auto fmt) {
     constexpr bool ASYM = decltype(fmt)::value;
-    if (all >= 1024) return up_chunks(&moe_up_kernel<ASYM, 1, kChunks>, &moe_up_kernel<ASYM, 1, 1>, 1);
-    if (all >= 512) return up_chunks(&moe_up_kernel<ASYM, 2, kChunks>, &moe_up_kernel<ASYM, 2, 1>, 2);
-    return up_chunks(&moe_up_kernel<ASYM, 4, kChunks>, &moe_up_kernel<ASYM, 4, 1>, 4);
+    if (a.tokens <= 16) {
+      if (all >= 1024) return up(&moe_up_kernel<ASYM, 4, 4, 1>, 4);
+      if (all >= 512) return up(&moe_up_kernel<ASYM, 2, 4, 1>, 2);
+      return up(&moe_up_kernel<ASYM, 1, 4, 1>, 1);
+    }
+    if (all >= 1024) return up(&moe_up_kernel<ASYM, 2, 2, kChunks>, 4);
+    if (all >= 512) return up(&moe_up_kernel<ASYM, 2, 4, kChunks>, 2);
+    return up(&moe_up_kernel<ASYM, 1, 4, kChunks>, 1);
   };
   asym ? up_fmt(std::true_type{}) : up_fmt(std::false_type{});
   const hipError_t e = hipGetLastError();
