@@ -23,11 +23,11 @@ namespace awq {
 namespace {
 
 constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX_K;
-constexpr int kUpWaves = 4, kDownWaves = 8;
+constexpr int kUpWaves = 4;
 // Units of a wavefront on their way: in the first launch by its number of tiles (two layers'
-// weights each), in the second of weights and of rows.
+// weights each), in the second of weights and, half as many, of rows.
 constexpr int up_ahead(int wide) { return wide == 4 ? 2 : wide == 2 ? 3 : 4; }
-constexpr int kAheadW = 8, kAheadX = 4;
+constexpr int kAheadW = 4, kAheadX = 2;
 constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
 
 struct Layers {  // a stack of packed layers
@@ -354,10 +354,11 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   }
 }
 
-// grid: tiles of 16 hidden outputs, splits of the named experts' units. Dynamic LDS:
-// [waves][tokens][16] float32.
-template <bool ASYM>
-__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
+// Workgroups own WIDE tiles of 16 hidden outputs. grid: those, splits of the named experts' units.
+// Dynamic LDS: [waves][tokens][16 WIDE] float32.
+template <bool ASYM, int WIDE, int WAVES, int CHUNKS>
+__global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
+  constexpr int OUT = 16 * WIDE;
   __shared__ int experts[kMostExperts], first[kMostExperts + 1];
   __shared__ int row_pair[kMostPairs];
   __shared__ float row_weight[kMostPairs];
@@ -365,11 +366,11 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
   extern __shared__ float sums[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, p = lane >> 4;
-  const int tile = blockIdx.x, tiles = gridDim.x, pairs = a.tokens * a.k;
-  float* mine = sums + wave * a.tokens * 16;
-  for (int i = lane; i < a.tokens * 16; i += 64) mine[i] = 0.0f;
+  const int group = blockIdx.x, groups = gridDim.x, pairs = a.tokens * a.k;
+  float* mine = sums + wave * a.tokens * OUT;
+  for (int i = lane; i < a.tokens * OUT; i += 64) mine[i] = 0.0f;
   const int total = *a.plan.total;
-  for (int i = threadIdx.x; i <= pairs; i += 64 * kDownWaves) {
+  for (int i = threadIdx.x; i <= pairs; i += 64 * WAVES) {
     // what lies behind the last named expert (of kMostExperts at most) is not used
     if (i <= kMostExperts) first[i] = a.plan.first[i];
     if (i < kMostExperts && i < pairs) experts[i] = a.plan.experts[i];
@@ -381,8 +382,8 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
   __syncthreads();
 
   // this wavefront's run of the named experts' units
-  const int units = a.ffn / kGroup, all = total * units, waves = kDownWaves * gridDim.y;
-  const int number = blockIdx.y * kDownWaves + wave;
+  const int units = a.ffn / kGroup, all = total * units, waves = WAVES * gridDim.y;
+  const int number = blockIdx.y * WAVES + wave;
   const int begin = static_cast<int>(static_cast<int64_t>(all) * number / waves);
   const int end = static_cast<int>(static_cast<int64_t>(all) * (number + 1) / waves);
   struct Cursor {
@@ -394,12 +395,15 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
       ++c.slot;
     }
   };
-  Piece pw[kAheadW];
+  Piece pw[kAheadW][WIDE];
   half8_t px[kAheadX][4];  // of the expert's first 16 rows
-  auto load_w = [&](Piece& w, const Cursor& c, int at) {
+  auto load_w = [&](Piece (&w)[WIDE], const Cursor& c, int at) {
     const bool real = at < end;
     const int e = __builtin_amdgcn_readfirstlane(experts[real ? c.slot : 0]);
-    w = load_piece<ASYM>(reader(a.down, e, tile, units, a.sets), real ? c.unit : 0, a.sets, lane, real ? 0u : kNoLoad);
+#pragma unroll
+    for (int t = 0; t < WIDE; ++t)
+      w[t] = load_piece<ASYM>(reader(a.down, e, WIDE * group + t, units, a.sets), real ? c.unit : 0, a.sets, lane,
+                              real ? 0u : kNoLoad);
   };
   auto load_x = [&](half8_t (&x)[4], const Cursor& c, int at) {
     const bool real = at < end;
@@ -420,44 +424,57 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
       load_x(px[i], ahead_x, begin + i);
       next(ahead_x);
     }
-    float4_t d[kChunks];
+    float4_t d[CHUNKS][WIDE];
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) d[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int t = 0; t < WIDE; ++t) d[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
     for (int at0 = begin; at0 < end; at0 += kAheadW) {
 #pragma unroll
       for (int n = 0; n < kAheadW; ++n) {
         const int at = at0 + n;
         if (at >= end) break;
         const int row0 = first[now.slot], count = __builtin_amdgcn_readfirstlane(first[now.slot + 1] - row0);
-        const Dequant dq = constants<ASYM>(pw[n], lane);
-        half8_t w[4];
+        half8_t w[WIDE][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[i] = weights8(pw[n], i, dq);
-          d[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % kAheadX][i], w[i], d[0], 0, 0, 0);
+        for (int t = 0; t < WIDE; ++t) {
+          const Dequant dq = constants<ASYM>(pw[n][t], lane);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[t][i] = weights8(pw[n][t], i, dq);
+            d[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % kAheadX][i], w[t][i], d[0][t], 0, 0, 0);
+          }
         }
         load_w(pw[n], ahead_w, at + kAheadW);
         next(ahead_w);
         load_x(px[n % kAheadX], ahead_x, at + kAheadX);
         next(ahead_x);
 #pragma unroll
-        for (int c = 1; c < kChunks; ++c) {
+        for (int c = 1; c < CHUNKS; ++c) {
           if (16 * c >= count) break;
           const uint16_t* x = a.mid + static_cast<int64_t>(row_pair[row0 + min(16 * c + r, count - 1)]) * a.ffn +
                               now.unit * kGroup + 32 * p;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(load_half8(x + 8 * i), w[i], d[c], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            const half8_t f = load_half8(x + 8 * i);
+#pragma unroll
+            for (int t = 0; t < WIDE; ++t) d[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, w[t][i], d[c][t], 0, 0, 0);
+          }
         }
         if (now.unit == units - 1 || at + 1 == end) {  // this wavefront's share of the expert is complete
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
+          for (int c = 0; c < CHUNKS; ++c) {
             if (16 * c >= count) break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int m = 16 * c + 4 * p + j;
-              if (m < count) mine[row_pair[row0 + m] / a.k * 16 + r] += row_weight[row0 + m] * d[c][j];
+              if (m >= count) continue;
+              float* to = mine + row_pair[row0 + m] / a.k * OUT + r;
+#pragma unroll
+              for (int t = 0; t < WIDE; ++t) to[16 * t] += row_weight[row0 + m] * d[c][t][j];
             }
-            d[c] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < WIDE; ++t) d[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
           }
           wave_lds_fence();
         }
@@ -466,52 +483,60 @@ __global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
     }
   }
   __syncthreads();
-  const int outputs = a.tokens * 16;
+  const int outputs = a.tokens * OUT;
   auto store = [&](int i, float v) {
-    const int t = i / 16, n = tile * 16 + i % 16;
+    const int t = i / OUT, n = group * OUT + i % OUT;
     if (a.residual != nullptr) v += f16_to_f32(a.residual[t * a.residual_stride + n]);
     a.y[t * a.y_stride + n] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
   };
   auto sum = [&](int i) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kDownWaves; ++w) v += sums[w * outputs + i];
+    for (int w = 0; w < WAVES; ++w) v += sums[w * outputs + i];
     return v;
   };
   if (gridDim.y == 1) {
-    for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves) store(i, sum(i));
+    for (int i = threadIdx.x; i < outputs; i += 64 * WAVES) store(i, sum(i));
     return;
   }
-  // The last workgroup of a tile adds all parts, in their order. They go through the memory that
+  // The last workgroup of a group of outputs adds all parts, in their order. They go through the memory that
   // all XCDs see, one by one: an exchange has been seen by all when its result is there, and the
   // barrier waits for it (a fence writes back all that an XCD's cache holds, in every workgroup:
   // 57 us instead of 9 for 23 MB of weights).
   uint32_t seen = 0;
-  for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves)
+  for (int i = threadIdx.x; i < outputs; i += 64 * WAVES)
     seen |= __hip_atomic_exchange(reinterpret_cast<uint32_t*>(a.plan.part) +
-                                      (static_cast<int64_t>(blockIdx.y) * tiles + tile) * outputs + i,
+                                      (static_cast<int64_t>(blockIdx.y) * groups + group) * outputs + i,
                                   __builtin_bit_cast(uint32_t, sum(i)), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   asm volatile("" : : "v"(seen) : "memory");
   __syncthreads();
   if (threadIdx.x == 0)
-    last_one = __hip_atomic_fetch_add(&a.plan.ended[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+    last_one = __hip_atomic_fetch_add(&a.plan.ended[group], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                static_cast<int>(gridDim.y) - 1;
   __syncthreads();
   if (!last_one) return;
-  for (int i = threadIdx.x; i < outputs; i += 64 * kDownWaves) {
+  for (int i = threadIdx.x; i < outputs; i += 64 * WAVES) {
     float v = 0.0f;
     for (int s = 0; s < static_cast<int>(gridDim.y); ++s)
-      v += __hip_atomic_load(a.plan.part + (static_cast<int64_t>(s) * tiles + tile) * outputs + i, __ATOMIC_RELAXED,
+      v += __hip_atomic_load(a.plan.part + (static_cast<int64_t>(s) * groups + group) * outputs + i, __ATOMIC_RELAXED,
                              __HIP_MEMORY_SCOPE_AGENT);
     store(i, v);
   }
 }
 
-// Workgroups that share 16 outputs in the second launch, so that at least one runs on each CU.
-int down_splits(int hidden) {
-  const int tiles = hidden / kTileN;
-  const int splits = (256 + tiles - 1) / tiles;
-  return splits > 16 ? 16 : splits;
+// The second launch. More than 16 tokens: two tiles for each wavefront, whose rows' loads are most
+// of what it does, and eight wavefronts with the registers for that (48 tokens over 64 experts:
+// 76 -> 64 us for its part); else sixteen wavefronts with one. Workgroups share outputs so that at
+// least one runs on each CU.
+struct Down {
+  int wide, waves, splits;
+};
+Down down_for(int64_t tokens, int hidden) {
+  Down d = {tokens > 16 ? 2 : 1, tokens > 16 ? 8 : 16, 1};
+  const int groups = hidden / (kTileN * d.wide);
+  d.splits = (256 + groups - 1) / groups;
+  if (d.splits > 16) d.splits = 16;
+  return d;
 }
 
 Layers make_layers(const void* base, int64_t N, int64_t K, int32_t group, int32_t fmt) {
@@ -537,7 +562,7 @@ size_t lay_out(int64_t tokens, int hidden, int ffn, int k, void* ws, uint16_t** 
   p.pair = reinterpret_cast<int32_t*>(take(4 * pairs));
   p.weight = reinterpret_cast<float*>(take(4 * pairs));
   p.ended = reinterpret_cast<int32_t*>(take(4 * tiles));
-  const int splits = down_splits(hidden);
+  const int splits = down_for(tokens, hidden).splits;
   p.part = reinterpret_cast<float*>(take(splits == 1 ? 0 : 4 * splits * tiles * tokens * 16));
   if (mid != nullptr) *mid = m;
   if (plan != nullptr) *plan = p;
@@ -599,10 +624,20 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   asym ? up_fmt(std::true_type{}) : up_fmt(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((asym ? &moe_down_kernel<true> : &moe_down_kernel<false>),
-                     dim3(p.hidden / kTileN, down_splits(p.hidden)), dim3(64 * kDownWaves),
-                     static_cast<size_t>(4) * kDownWaves * a.tokens * 16, st, a);
-  return hipGetLastError();
+  const Down d = down_for(p.tokens, p.hidden);
+  auto down = [&](auto kernel, std::atomic<uint64_t>& done) {
+    const hipError_t limit = ensure_lds_limit(reinterpret_cast<const void*>(kernel),
+                                              4 * d.waves * AWQ_MOE_MAX_TOKENS * 16 * d.wide, done);
+    if (limit != hipSuccess) return limit;
+    hipLaunchKernelGGL(kernel, dim3(p.hidden / (kTileN * d.wide), d.splits), dim3(64 * d.waves),
+                       static_cast<size_t>(4) * d.waves * a.tokens * 16 * d.wide, st, a);
+    return hipGetLastError();
+  };
+  static std::atomic<uint64_t> done[4];
+  if (a.tokens <= 16)
+    return asym ? down(&moe_down_kernel<true, 1, 16, 1>, done[0]) : down(&moe_down_kernel<false, 1, 16, 1>, done[1]);
+  return asym ? down(&moe_down_kernel<true, 2, 8, kChunks>, done[2])
+              : down(&moe_down_kernel<false, 2, 8, kChunks>, done[3]);
 }
 
 }  // namespace awq
