@@ -26,7 +26,7 @@ constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX
 constexpr int kUpWaves = 4;
 // Units of a wavefront on their way: in the first launch by its number of tiles (two layers'
 // weights each), in the second of weights and, half as many, of rows.
-constexpr int up_ahead(int wide) { return wide == 4 ? 2 : wide == 2 ? 3 : 4; }
+constexpr int up_ahead(int wide) { return wide == 1 ? 4 : 2; }
 constexpr int kAheadW = 4, kAheadX = 2;
 constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
 

@@ -17,15 +17,19 @@ namespace {
 
 typedef double double4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kSliceWaves = 4;
+constexpr int kSliceWaves = 4, kRouteAhead = 2;
 
-// Slices of the channels, one per workgroup of four wavefronts, so that about two workgroups per
-// CU run; a wavefront has at least 64 channels.
+// Slices of the channels, one per workgroup of four wavefronts, so that about four workgroups per
+// CU run; a wavefront has at least 32 channels. (One workgroup per CU left each float64
+// instruction waiting for its operands: 517 tokens x 128 experts x 4096 31 us instead of 19.)
+int route_wide(int64_t tokens) { return tokens > 16 ? 2 : 1; }  // tiles of 16 tokens for a wavefront
 int route_slices(int64_t tokens, int hidden, int experts) {
-  const int64_t tiles = (tokens + 15) / 16 * ((experts + 15) / 16);
-  int64_t slices = 512 / tiles;
-  const int64_t most = (hidden + 64 * kSliceWaves - 1) / (64 * kSliceWaves);
+  const int rows = 16 * route_wide(tokens);
+  const int64_t tiles = (tokens + rows - 1) / rows * ((experts + 15) / 16);
+  int64_t slices = (1024 + tiles / 2) / tiles;
+  const int64_t most = (hidden + 32 * kSliceWaves - 1) / (32 * kSliceWaves);
   if (slices > most) slices = most;
+  if (slices > 32) slices = 32;
   return slices < 1 ? 1 : static_cast<int>(slices);
 }
 
@@ -40,41 +44,76 @@ struct RouteArgs {
   float scale;
 };
 
-// grid: token tiles, expert tiles, slices
-template <typename T>
+// grid: token tiles, expert tiles, slices. A wavefront's WIDE token tiles share an expert's operands,
+// and their sums are chains of their own.
+template <typename T, int WIDE>
 __global__ void __launch_bounds__(64 * kSliceWaves) route_logits_kernel(RouteArgs a) {
-  __shared__ double red[kSliceWaves][16][16];
+  __shared__ double red[kSliceWaves][16 * WIDE][16];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, p = lane >> 4;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * 16 + r;
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * (16 * WIDE);
   const int expert = blockIdx.y * 16 + r;
-  const uint16_t* x = a.x + (token < a.tokens ? token : 0) * a.x_stride;
   const uint16_t* w = a.w + static_cast<int64_t>(expert < a.experts ? expert : 0) * a.hidden;
+  const bool has_w = expert < a.experts;
+  const uint16_t* x[WIDE];
+  bool has_x[WIDE];
+#pragma unroll
+  for (int t = 0; t < WIDE; ++t) {
+    const int64_t token = token0 + 16 * t + r;
+    has_x[t] = token < a.tokens;
+    x[t] = a.x + (has_x[t] ? token : 0) * a.x_stride;
+  }
   // steps of 32 channels dealt to all slices' wavefronts in turn
   const int steps = (a.hidden + 31) / 32, waves = kSliceWaves * a.slices;
-  double4_t acc = {0.0, 0.0, 0.0, 0.0};
-  for (int s = static_cast<int>(blockIdx.z) * kSliceWaves + wave; s < steps; s += waves) {
-    const int c = 32 * s + 8 * p;
-    uint4 xv = make_uint4(0, 0, 0, 0), wv = xv;
-    if (c < a.hidden && token < a.tokens) xv = *reinterpret_cast<const uint4*>(x + c);
-    if (c < a.hidden && expert < a.experts) wv = *reinterpret_cast<const uint4*>(w + c);
-    float xf[8], wf[8];
-    widen<T>(xv, xf);
-    widen<T>(wv, wf);
+  double4_t acc[WIDE];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(xf[e]), static_cast<double>(wf[e]), acc, 0, 0, 0);
+  for (int t = 0; t < WIDE; ++t) acc[t] = double4_t{0.0, 0.0, 0.0, 0.0};
+  uint4 xv[kRouteAhead][WIDE], wv[kRouteAhead];
+  auto load = [&](int i, int s) {  // zeros behind the last channel
+    const int c = 32 * s + 8 * p;
+    wv[i] = make_uint4(0, 0, 0, 0);
+    if (c < a.hidden && has_w) wv[i] = *reinterpret_cast<const uint4*>(w + c);
+#pragma unroll
+    for (int t = 0; t < WIDE; ++t) {
+      xv[i][t] = make_uint4(0, 0, 0, 0);
+      if (c < a.hidden && has_x[t]) xv[i][t] = *reinterpret_cast<const uint4*>(x[t] + c);
+    }
+  };
+  const int s0 = static_cast<int>(blockIdx.z) * kSliceWaves + wave;
+#pragma unroll
+  for (int i = 0; i < kRouteAhead; ++i) load(i, s0 + i * waves);
+  for (int s = s0; s < steps; s += kRouteAhead * waves) {
+#pragma unroll
+    for (int i = 0; i < kRouteAhead; ++i) {
+      float xf[WIDE][8], wf[8];
+      widen<T>(wv[i], wf);
+#pragma unroll
+      for (int t = 0; t < WIDE; ++t) widen<T>(xv[i][t], xf[t]);
+      load(i, s + (i + kRouteAhead) * waves);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double we = static_cast<double>(wf[e]);
+#pragma unroll
+        for (int t = 0; t < WIDE; ++t)
+          acc[t] = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(xf[t][e]), we, acc[t], 0, 0, 0);
+      }
+    }
   }
   // element i of lane l is row 4 i + l / 16, column l % 16
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[wave][4 * i + p][r] = acc[i];
-  __syncthreads();
-  const int m = threadIdx.x / 16, n = threadIdx.x % 16;
-  double sum = 0.0;
+  for (int t = 0; t < WIDE; ++t)
 #pragma unroll
-  for (int v = 0; v < kSliceWaves; ++v) sum += red[v][m][n];
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * 16 + m;
-  const int e = blockIdx.y * 16 + n;
-  if (t < a.tokens && e < a.experts) a.part[(blockIdx.z * a.tokens + t) * a.experts + e] = sum;
+    for (int i = 0; i < 4; ++i) red[wave][16 * t + 4 * i + p][r] = acc[t][i];
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < WIDE; ++t) {
+    const int m = 16 * t + threadIdx.x / 16, n = threadIdx.x % 16;
+    double sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < kSliceWaves; ++v) sum += red[v][m][n];
+    const int64_t token = token0 + m;
+    const int e = blockIdx.y * 16 + n;
+    if (token < a.tokens && e < a.experts) a.part[(blockIdx.z * a.tokens + token) * a.experts + e] = sum;
+  }
 }
 
 // An order of choices as whole numbers: larger is better, NaN stands behind -infinity.
@@ -101,7 +140,15 @@ __global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
     const int e = t + THREADS * i;
     double l = 0.0;
     if (live && e < a.experts) {
-      for (int s = 0; s < a.slices; ++s) l += a.part[(s * a.tokens + token) * a.experts + e];
+      const double* part = a.part + token * a.experts + e;
+      const int64_t slice = a.tokens * a.experts;
+      for (int s = 0; s < a.slices; s += 8) {  // eight at a time on their way
+        double v[8];
+#pragma unroll
+        for (int o = 0; o < 8; ++o) v[o] = part[min(s + o, a.slices - 1) * slice];
+#pragma unroll
+        for (int o = 0; o < 8; ++o) l += s + o < a.slices ? v[o] : 0.0;
+      }
       const double bias = a.bias == nullptr ? 0.0 : static_cast<double>(a.bias[e]);
       if (a.score == AWQ_SCORE_SIGMOID) l = 1.0 / (1.0 + exp(-l));
       keys[mine][e] = order(l + bias);
@@ -145,6 +192,7 @@ __global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
       if (e >= a.experts) continue;
       const uint64_t key = keys[mine][e];
       int place = 0;
+#pragma unroll 4
       for (int o = 0; o < a.experts; ++o) {
         const uint64_t other = keys[mine][o];
         place += other > key || (other == key && o < e);
@@ -197,12 +245,16 @@ hipError_t launch_moe_route(const awq_moe_route_args& p, hipStream_t st) {
   a.score = p.score;
   a.renormalize = p.renormalize;
   a.scale = p.scale;
-  const dim3 grid(static_cast<unsigned>((p.tokens + 15) / 16), (p.experts + 15) / 16, a.slices);
-  hipLaunchKernelGGL((p.dtype == AWQ_DT_F16 ? &route_logits_kernel<F16> : &route_logits_kernel<BF16>), grid,
-                     dim3(64 * kSliceWaves), 0, st, a);
+  const int wide = route_wide(p.tokens);
+  const dim3 grid(static_cast<unsigned>((p.tokens + 16 * wide - 1) / (16 * wide)), (p.experts + 15) / 16, a.slices);
+  const bool f16 = p.dtype == AWQ_DT_F16;
+  const auto logits = wide == 1 ? f16 ? &route_logits_kernel<F16, 1> : &route_logits_kernel<BF16, 1>
+                                : f16 ? &route_logits_kernel<F16, 2> : &route_logits_kernel<BF16, 2>;
+  hipLaunchKernelGGL(logits, grid, dim3(64 * kSliceWaves), 0, st, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (p.experts <= 64) return launch_choose<64, 1>(a, st);
+  if (p.experts <= 128) return launch_choose<128, 1>(a, st);
   if (p.experts <= 256) return launch_choose<256, 1>(a, st);
   return launch_choose<256, 4>(a, st);
 }
