@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // ------------------------------------------------------------------------------- tiles
 //
 // Workgroups of four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of
-// 64 channels. Operands go from memory straight into LDS, into a ring of three steps, of
-// which two are on their way or have landed ahead of use. The only barrier of a step
+// 64 channels. Operands go from memory straight into LDS, into a ring of three or four
+// steps, of which all but one are on their way or have landed ahead of use. The only barrier of a step
 // stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
 // runs of four outputs of one row.
@@ -155,13 +155,28 @@ __device__ __forceinline__ uint4 tail8(const I8Args& a, float8_t v, uint4 f, uin
 constexpr int kStep = 64;  // channels of a step
 // Steps in LDS. Three steps of 128 x 256 outputs leave room for two workgroups on a CU, one of
 // which multiplies while the other stores (four steps: 149 us instead of 135 at 2048 x 14336 x
-// 4096; tiles of 256 x 256, which have a CU to themselves: 155).
-constexpr int kRing = 3;
+// 4096; tiles of 256 x 256, which have a CU to themselves: 155). Smaller tiles have less to do in a
+// step and take four (64 x 128 at 333 x 4096 x 11008: 41 us with three, 32 with four, 33 with six).
+constexpr int ring(int bm, int bn) { return bm * bn > 16384 ? 3 : 4; }
+
+// Waits until at most `ahead` <= MOST steps of PIECES loads each are on their way.
+template <int MOST, int PIECES>
+__device__ __forceinline__ void wait_steps(int ahead) {
+  if constexpr (MOST == 0) {
+    wait_loads<0>();
+  } else {
+    if (ahead >= MOST) {
+      wait_loads<MOST * PIECES>();
+    } else {
+      wait_steps<MOST - 1, PIECES>(ahead);
+    }
+  }
+}
 
 template <typename T, int BM, int BN, bool SPLIT>
 __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 32, FN = TN / 32;
-  constexpr int STAGE = (BM + BN) * kStep, PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W, RING = kRing;
+  constexpr int STAGE = (BM + BN) * kStep, PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W, RING = ring(BM, BN);
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave & 1, wn = wave >> 1, half = lane >> 5, l32 = lane & 31;
@@ -190,8 +205,8 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   // 64 bytes of a row in LDS, their 16-byte pieces exchanged by the row's number (p ^ row / 2 % 4),
   // so that eight rows' equal pieces lie in different banks; the exchange is made where a lane loads
   const uint32_t lane_q = (lane >> 2) * stride + 16u * ((lane & 3) ^ ((lane >> 3) & 3));
-  auto issue_piece = [&](int step, int i) {  // 1 KiB each: 16 rows, or a unit of W
-    const uint32_t dst = base + (step % RING) * STAGE;
+  auto issue_piece = [&](int slot, int step, int i) {  // 1 KiB each: 16 rows, or a unit of W
+    const uint32_t dst = base + slot * STAGE;
     if (i < PIECES_A) {
       const uint32_t piece = wave * PIECES_A + i;
       load_to_lds(rq, lane_q + piece * 16u * stride + static_cast<uint32_t>(first + step) * kStep, dst + piece * 1024u);
@@ -203,8 +218,8 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   };
   // operands of half s of a step, in the order of their use: W's, then the rows'
   int4_t fq[2][FM], fw[2][FN];
-  auto read_one = [&](int step, int s, int i) {
-    const unsigned char* stage = lds + (step % RING) * STAGE;
+  auto read_one = [&](int slot, int s, int i) {
+    const unsigned char* stage = lds + slot * STAGE;
     if (i < FN) {
       const unsigned char* w = stage + BM * kStep + (wn * TN / 16 + (l32 >> 4)) * 1024 + 16 * ((lane & 15) + 16 * (2 * s + half));
       fw[s][i] = *reinterpret_cast<const int4_t*>(w + i * 2048);
@@ -223,7 +238,7 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   // A half's products in runs of FN, and between the runs an equal part of the next half's LDS
   // reads and of the loads of a step to come: a wavefront may have its SIMD to itself, and nothing
   // else would fill the matrix cores' pauses. (Left to the compiler, both stand in front.)
-  auto products = [&](int s, bool reads, int read_step, bool loads, int load_step) {
+  auto products = [&](int s, bool reads, int read_slot, bool loads, int load_slot, int load_step) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -231,11 +246,11 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s][j], fq[s][i], acc[i][j], 0, 0, 0);
       if (reads) {
 #pragma unroll
-        for (int r = (FM + FN) * i / FM; r < (FM + FN) * (i + 1) / FM; ++r) read_one(read_step, s ^ 1, r);
+        for (int r = (FM + FN) * i / FM; r < (FM + FN) * (i + 1) / FM; ++r) read_one(read_slot, s ^ 1, r);
       }
       if (loads) {
 #pragma unroll
-        for (int l = PIECES * i / FM; l < PIECES * (i + 1) / FM; ++l) issue_piece(load_step, l);
+        for (int l = PIECES * i / FM; l < PIECES * (i + 1) / FM; ++l) issue_piece(load_slot, load_step, l);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -245,27 +260,26 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   for (int i = 0; i < RING; ++i)
     if (i < steps) {
 #pragma unroll
-      for (int l = 0; l < PIECES; ++l) issue_piece(i, l);
+      for (int l = 0; l < PIECES; ++l) issue_piece(i, i, l);
     }
   // `ahead` steps behind the one that is waited for may be on their way
   auto wait_step = [&](int ahead) {
-    if (ahead >= 2) {
-      wait_loads<2 * PIECES>();
-    } else if (ahead == 1) {
-      wait_loads<PIECES>();
-    } else {
-      wait_loads<0>();
-    }
+    wait_steps<RING - 1, PIECES>(ahead);
     lds_barrier();
   };
   wait_step(min(steps, RING) - 1);
 #pragma unroll
   for (int r = 0; r < FM + FN; ++r) read_one(0, 0, r);
-  for (int i = 0; i < steps; ++i) {
-    products(0, true, i, false, 0);
-    // this step's operands are read, the next step's have landed
-    wait_step(min(steps - i, RING) - 2);
-    products(1, i + 1 < steps, i + 1, i + RING < steps, i + RING);
+  for (int i0 = 0; i0 < steps; i0 += RING) {
+#pragma unroll
+    for (int n = 0; n < RING; ++n) {  // the steps' places in the ring are constants
+      const int i = i0 + n;
+      if (i >= steps) break;
+      products(0, true, n, false, 0, 0);
+      // this step's operands are read, the next step's have landed
+      wait_step(min(steps - i, RING) - 2);
+      products(1, i + 1 < steps, (n + 1) % RING, i + RING < steps, n, i + RING);
+    }
   }
 
   // element e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32
@@ -346,10 +360,19 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
   const int64_t runs = a.M * a.N / 8, all = a.M * a.N;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < runs; i += static_cast<int64_t>(gridDim.x) * 256) {
     int4_t lo = {0, 0, 0, 0}, hi = lo;
-    for (int s = 0; s < splits; ++s) {
-      const int4_t* p = reinterpret_cast<const int4_t*>(a.part + s * all + 8 * i);
-      lo += p[0];
-      hi += p[1];
+    for (int s = 0; s < splits; s += 4) {  // four at a time on their way
+      int4_t v[4][2];
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        const int4_t* p = reinterpret_cast<const int4_t*>(a.part + min(s + o, splits - 1) * all + 8 * i);
+        v[o][0] = p[0];
+        v[o][1] = p[1];
+      }
+#pragma unroll
+      for (int o = 0; o < 4; ++o) {
+        lo += s + o < splits ? v[o][0] : int4_t{0, 0, 0, 0};
+        hi += s + o < splits ? v[o][1] : int4_t{0, 0, 0, 0};
+      }
     }
     const int64_t m = 8 * i / a.N, n = 8 * i - m * a.N;
     const float sx = a.scale[m];
@@ -368,19 +391,19 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
 }
 
 // Which kernel a product takes: the one with the least time by an estimate in microseconds, whose
-// constants were fitted (by least squares of the logarithms, 10 % rms) to 1400 timings of all
+// constants were fitted (by least squares of the logarithms, 9 % rms) to 1300 timings of all
 // kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. On
-// those the choice costs 2 % more than the best one on average, 34 % at worst (64 x 8192 x 1024).
+// those the choice costs 1.1 % more than the best one on average, 25 % at worst (33 x 8192 x 1024).
 // A CU's blocks share its matrix cores (`work` each and step) and pass their steps not faster than
 // memory answers (`wait`, `fit` of them at a time).
 struct Tile {
   int bm, bn, fit;
   float work, wait, once;
 };
-constexpr Tile kTiles[] = {{64, 64, 6, 0.111f, 0.183f, 0.68f},
-                           {64, 128, 4, 0.152f, 0.205f, 1.21f},
-                           {128, 128, 3, 0.233f, 0.278f, 1.85f},
-                           {128, 256, 2, 0.390f, 0.426f, 3.47f}};
+constexpr Tile kTiles[] = {{64, 64, 5, 0.106f, 0.129f, 0.55f},
+                           {64, 128, 3, 0.145f, 0.150f, 1.11f},
+                           {128, 128, 2, 0.215f, 0.235f, 1.97f},
+                           {128, 256, 2, 0.352f, 0.380f, 3.34f}};
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 16};
 struct Choice {
   int tile, splits;  // tile -1: i8_rows_kernel
@@ -394,6 +417,8 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
       return {-1, 1};
     }
   }
+  // few rows: 14336 x 4096 of one row 10.8 us, the best tiles 12.5; 8192 x 14336 of four 19.4 and 24.6
+  if (M <= 8) return {-1, 1};
   constexpr float kCus = 256.0f;
   const float units = static_cast<float>((K + kI8Unit - 1) / kI8Unit), m = static_cast<float>(M), n = static_cast<float>(N);
   auto blocks = [](int64_t v, int64_t b) { return static_cast<float>((v + b - 1) / b); };
@@ -408,8 +433,8 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
       const Tile& k = kTiles[t];
       const float per_cu = ceilf(blocks(M, k.bm) * blocks(N, k.bn) * splits / kCus), steps = ceilf(units / splits);
       const float waits = k.wait * ceilf(per_cu / k.fit), works = k.work * per_cu;
-      float time = 3.69f + steps * (waits > works ? waits : works) + k.once * per_cu;
-      if (splits > 1) time += 2.66f + (8.0f * splits + 2.0f) * m * n / 7.0e6f;
+      float time = 3.06f + steps * (waits > works ? waits : works) + k.once * per_cu;
+      if (splits > 1) time += 1.82f + 0.10f * splits + (8.0f * splits + 2.0f) * m * n / 6.5e6f;
       if (time < least) {
         least = time;
         best = {t, splits};
@@ -420,7 +445,7 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
 
 template <typename T, int BM, int BN>
 hipError_t launch_tiles(const I8Args& a, int splits, hipStream_t st) {
-  constexpr int STAGES = kRing * (BM + BN) * kStep, TAIL = 4 * 32 * (BN / 2 + 4) * 4, LDS = STAGES > TAIL ? STAGES : TAIL;
+  constexpr int STAGES = ring(BM, BN) * (BM + BN) * kStep, TAIL = 4 * 32 * (BN / 2 + 4) * 4, LDS = STAGES > TAIL ? STAGES : TAIL;
   const unsigned blocks = static_cast<unsigned>((a.M + BM - 1) / BM * ((a.N + BN - 1) / BN));
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
     const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS, done);
