@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   __shared__ float4_t red[SHARE == 1 ? 1 : kUpWaves][WIDE][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int r = lane & 15, p = lane >> 4, part = wave % SHARE;
-  const int tiles = a.ffn / kTileN, slot = blockIdx.y;
+  const int slot = blockIdx.y;
   const bool plans = blockIdx.x == gridDim.x - 1;
   if (plans && slot != 0) return;
   find_named(a, ids, bits);
@@ -245,11 +245,11 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   const int e = __builtin_amdgcn_readfirstlane(32 * word_at + __builtin_ctz(word));
 
   const int units = a.hidden / kGroup, tile0 = blockIdx.x * TILES + wave / SHARE * WIDE;
-  Reader rg[WIDE], ru[WIDE];  // of a tile past the last one, the last one's: its results are dropped
+  Reader rg[WIDE], ru[WIDE];
 #pragma unroll
   for (int t = 0; t < WIDE; ++t) {
-    rg[t] = reader(a.gate, e, min(tile0 + t, tiles - 1), units, a.sets);
-    ru[t] = reader(a.up, e, min(tile0 + t, tiles - 1), units, a.sets);
+    rg[t] = reader(a.gate, e, tile0 + t, units, a.sets);
+    ru[t] = reader(a.up, e, tile0 + t, units, a.sets);
   }
   Piece pg[AHEAD][WIDE], pu[AHEAD][WIDE];
   auto load = [&](int i, int unit) {
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
     // the wavefronts that share tiles divide them among themselves
 #pragma unroll
     for (int t = 0; t < WIDE; ++t) {
-      if (t % SHARE != part || tile0 + t >= tiles) continue;
+      if (t % SHARE != part) continue;
       float4_t sg = g[c][t], su = u[c][t];
       if constexpr (SHARE > 1) {
         const int w0 = wave - part;
@@ -607,8 +607,8 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   // tiles. More than 16 rows for an expert take twice the registers for each tile.
   const int tiles = p.ffn / kTileN, all = tiles * slots;
   auto up = [&](auto kernel, int per_group) {
-    const unsigned groups = static_cast<unsigned>((tiles + per_group - 1) / per_group);
-    hipLaunchKernelGGL(kernel, dim3(groups + 1, slots), dim3(64 * kUpWaves), 0, st, a);
+    // tiles come in eights
+    hipLaunchKernelGGL(kernel, dim3(tiles / per_group + 1, slots), dim3(64 * kUpWaves), 0, st, a);
   };
   auto up_fmt = [&](auto fmt) {
     constexpr bool ASYM = decltype(fmt)::value;

@@ -4,9 +4,9 @@
 //   h = T(x + residual);  v = h w r,  r = 1 / sqrt(mean(h^2) + eps);  s = max|v| / 127,
 //   q = rint(v / s)
 //
-// A row is read once and stays in registers: its square sum and max|h w| come from one
-// reduction (r > 0, so max|v| = r max|h w|, to the same rounding), and every output is
-// written from there. Memory is the only bound of long inputs.
+// A row is read once and stays in registers; its sum of squares, and for 8-bit rows max|v| after
+// it, come from reductions over the row's threads, and every output is written from there. Memory
+// is the only bound of long inputs.
 #include "ffn_internal.hpp"
 
 namespace awq {
@@ -26,28 +26,20 @@ struct RowsArgs {
   float eps;
 };
 
-// The sum over a row's THREADS threads of `sum`, and the largest `top`.
-template <int THREADS>
-__device__ __forceinline__ void row_reduce(float& sum, uint32_t& top, uint2* shared) {
+// `v` combined over a row's THREADS threads, left in all of them.
+template <int THREADS, typename V, typename Op>
+__device__ __forceinline__ V row_reduce(V v, V* shared, Op op) {
 #pragma unroll
-  for (int s = 32; s > 0; s >>= 1) {
-    sum += __shfl_xor(sum, s);
-    top = umax(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), s)));
-  }
+  for (int s = 32; s > 0; s >>= 1) v = op(v, __shfl_xor(v, s));
   if constexpr (THREADS > 64) {
-    constexpr int WAVES = THREADS / 64;
     __syncthreads();  // an earlier reduction's values have been read
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = make_uint2(__builtin_bit_cast(uint32_t, sum), top);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
     __syncthreads();
-    sum = 0.0f;
-    top = 0;
+    v = shared[0];
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) {
-      const uint32_t part = shared[w].x;
-      sum += __builtin_bit_cast(float, part);
-      top = umax(top, shared[w].y);
-    }
+    for (int w = 1; w < THREADS / 64; ++w) v = op(v, shared[w]);
   }
+  return v;
 }
 
 // A value of which the compiler knows nothing from here on.
@@ -57,7 +49,8 @@ __device__ __forceinline__ void hide(uint4& v) { asm volatile("" : "+v"(v.x), "+
 template <typename T, int THREADS, int NV, bool NORM>
 __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(RowsArgs a) {
   constexpr int BLOCK = THREADS < 256 ? 256 : THREADS, ROWS = BLOCK / THREADS;
-  __shared__ uint2 shared[BLOCK / 64];
+  __shared__ float sums[BLOCK / 64];
+  __shared__ uint32_t tops[BLOCK / 64];
   const int t = threadIdx.x % THREADS;
   const int runs = a.width / 8;
   for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THREADS; row < a.tokens;
@@ -86,57 +79,59 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(Row
         if (a.h != nullptr && t + THREADS * i < runs) *reinterpret_cast<uint4*>(a.h + row * a.h_stride + at) = h[i];
       }
     }
-    float sum = 0.0f, down = 1.0f;
-    uint32_t top = 0;
-    // f = h, v = h w, both times `down`
-    auto weighted = [&](int i, float* f, float* v) {
-      widen<T>(h[i], f);
-      if (NORM) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= down;
-      }
-      widen<T>(w[i], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= f[e];
-    };
-    auto reduce = [&] {
-      sum = 0.0f;
-      top = 0;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float f[8], v[8];
-        weighted(i, f, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (NORM) sum = __builtin_fmaf(f[e], f[e], sum);
-          top = umax(top, magnitude(v[e]));
-        }
-        __builtin_amdgcn_sched_barrier(0);  // one run's float32 values at a time
-      }
-      row_reduce<THREADS>(sum, top, shared);
-      // the compiler would keep all float32 values for the outputs: twice the registers
+    // the compiler would keep all float32 values from one pass over the registers to the next:
+    // twice the registers
+    auto hide_all = [&] {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         hide(h[i]);
         hide(w[i]);
       }
     };
-    reduce();
-    float r = 1.0f;
+    float down = 1.0f, r = 1.0f;
     if (NORM) {
-      float eps = a.eps;
+      auto squares = [&] {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float f[8];
+          widen<T>(h[i], f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            f[e] *= down;
+            sum = __builtin_fmaf(f[e], f[e], sum);
+          }
+        }
+        hide_all();
+        return row_reduce<THREADS>(sum, sums, [](float a, float b) { return a + b; });
+      };
+      float sum = squares(), eps = a.eps;
       if (sum == __builtin_inff()) {
         down = kDown;
         eps *= kDown * kDown;
-        reduce();
+        sum = squares();
       }
       r = 1.0f / sqrtf(sum / static_cast<float>(a.width) + eps);
     }
+    auto values = [&](int i, float* v) {
+      float f[8];
+      widen<T>(h[i], v);
+      widen<T>(w[i], f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (NORM ? v[e] * down * r : v[e]) * f[e];
+    };
     RowScale s = {0.0f, 0.0f};
     if (a.q != nullptr) {
-      // a NaN sum (NaN or two infinities apart) and max|v| past the type's range go the same way
-      const float most = __builtin_bit_cast(float, top) * r;
-      s = row_scale(top >= 0x7F800000u ? top : magnitude(most));
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float v[8];
+        values(i, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = umax(top, magnitude(v[e]));
+      }
+      hide_all();
+      s = row_scale(row_reduce<THREADS>(top, tops, [](uint32_t a, uint32_t b) { return umax(a, b); }));
       if (t == 0) a.scale[row] = s.scale;
     }
 #pragma unroll
@@ -144,10 +139,8 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(Row
       __builtin_amdgcn_sched_barrier(0);
       const int at = 8 * (t + THREADS * i);
       if (t + THREADS * i >= runs) continue;
-      float f[8], v[8];
-      weighted(i, f, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= r;
+      float v[8];
+      values(i, v);
       if (NORM && a.y != nullptr) *reinterpret_cast<uint4*>(a.y + row * a.y_stride + at) = narrow<T>(v);
       if (a.q != nullptr)
         *reinterpret_cast<uint2*>(a.q + row * a.q_stride + at) =

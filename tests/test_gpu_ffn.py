@@ -134,6 +134,13 @@ def test_rows_that_are_not_ordinary(dtype):
     over = v[1].abs() >= big * (1 + ref.U[dtype])
     y = got.y.cpu()
     assert bool(torch.isinf(y[over]).all())
+    if dtype == BF16:   # products of value and weight alone would pass float32
+        x2 = randn(3, width, seed=4, dtype=dtype) * 2.0 ** torch.tensor([[40], [100], [-60]], device=DEV).to(dtype)
+        w2 = randn(width, seed=5, dtype=dtype) * 2.0 ** 100
+        _, v, off = ref.norm(x2, w2, 1e-5)
+        got = int8.awq_rms_norm(x2, w2, i8=True)
+        ref.check(got.y, v, off + ref.U[dtype] * v.abs() + ref.TINY[dtype])
+        ref.check_rows8(got.q, got.scale, v, off)
     q, s = int8.awq_quant_i8(x)
     assert s.cpu()[0] == 0 and bool(torch.isnan(s.cpu()[2:4]).all()) and bool((q[[0, 2, 3]] == 0).all())
     v = ref.cpu64(x[[1, 4, 6, 7]])
@@ -388,7 +395,8 @@ def choices(tokens, k, experts, seed):
 @pytest.mark.parametrize("tokens,hidden,ffn,experts,k,group,fmt", [
     (1, 128, 128, 1, 1, 128, 0), (1, 1024, 384, 8, 2, 128, 0), (2, 256, 1408, 5, 3, 64, 1), (5, 384, 256, 40, 6, 32, 0),
     (16, 512, 512, 4, 2, 128, 1), (17, 256, 384, 3, 3, 128, 0), (33, 640, 128, 2, 2, 64, 0), (64, 256, 256, 70, 8, 128, 0),
-    (64, 128, 256, 1, 1, 128, 1), (3, 2048, 256, 6, 2, 256, 0),
+    (64, 128, 256, 1, 1, 128, 1), (9, 256, 640, 16, 4, 128, 0), (12, 128, 1152, 16, 6, 128, 1), (20, 128, 640, 16, 4, 64, 0),
+    (40, 4096, 128, 2, 1, 128, 0), (16, 4224, 128, 2, 2, 128, 1), (3, 2048, 256, 6, 2, 256, 0),
 ])
 @pytest.mark.parametrize("act,extra", [("silu", False), ("gelu", True)])
 def test_moe(tokens, hidden, ffn, experts, k, group, fmt, act, extra):
@@ -428,6 +436,18 @@ def test_moe_ids_of_every_kind():
     assert moe.awq_moe(x[:0], ids[:0], weights[:0], *packed, ffn).shape == (0, hidden)
 
 
+def test_moe_with_the_most_of_everything():
+    """64 tokens of 32 experts each out of 1024: more experts named than a wavefront has lanes."""
+    some, dense = experts4(8, 128, 128, 128, 0, seed=31)
+    which = torch.arange(1024, device=DEV) % 8
+    packed = [p[which].contiguous() for p in some]
+    x, (ids, weights) = randn(64, 128, seed=32), choices(64, 32, 1024, seed=33)
+    y = moe.awq_moe(x, ids, weights, *packed, 128)
+    want, bound = ref.moe(x, ids % 8, weights, *dense)
+    ref.check(y, want, bound)
+    assert same(y, moe.awq_moe(x, ids, weights, *packed, 128))
+
+
 def test_moe_strides_in_place_and_what_is_not_finite():
     hidden, ffn, experts = 256, 256, 4
     packed, _ = experts4(experts, hidden, ffn, 128, 0, seed=11)
@@ -450,9 +470,12 @@ def test_moe_strides_in_place_and_what_is_not_finite():
     y = moe.awq_moe(bad, ids, weights, *packed, ffn, residual=r)
     keep = [0, 1, 3, 5]
     assert same(y[keep], want[keep]) and bool(torch.isnan(y[2]).all()) and not bool(torch.isfinite(y[4]).all())
-    # weights of 0, and a row of them NaN
+    # weights of 0, and one that is NaN
     none = torch.zeros_like(weights)
     assert bool((moe.awq_moe(x, ids, none, *packed, ffn) == 0).all())
+    none[1, 0] = float("nan")
+    y = moe.awq_moe(x, ids, none, *packed, ffn)
+    assert bool(torch.isnan(y[1]).all()) and bool((y[[0, 2, 3, 4, 5]] == 0).all())
 
 
 def test_moe_refuses_wrong_stacks():
