@@ -111,8 +111,9 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 
 // ------------------------------------------------------------------------------- tiles
 //
-// Workgroups of four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of
-// 64 channels. Operands go from memory straight into LDS, into a ring of three or four
+// Four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of 64 channels; with
+// TEAMS = 2 a workgroup has two such teams, which take turns with the steps and add up their sums
+// at the end (few tiles leave a SIMD one wavefront, whose every step waits for LDS and the barrier). Operands go from memory straight into LDS, into a ring of three or four
 // steps, of which all but one are on their way or have landed ahead of use. The only barrier of a step
 // stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
@@ -173,12 +174,14 @@ __device__ __forceinline__ void wait_steps(int ahead) {
   }
 }
 
-template <typename T, int BM, int BN, bool SPLIT>
-__global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
+template <typename T, int BM, int BN, int TEAMS, bool SPLIT>
+__global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 32, FN = TN / 32;
-  constexpr int STAGE = (BM + BN) * kStep, PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W, RING = ring(BM, BN);
+  constexpr int STAGE = (BM + BN) * kStep, RING = ring(BM, BN);
+  constexpr int PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W;  // a wavefront's loads of a step
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int number = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = number & 3, team = number >> 2;
   const int wm = wave & 1, wn = wave >> 1, half = lane >> 5, l32 = lane & 31;
 
   // blocks of an XCD are neighbours: bands of eight row tiles, down the rows first
@@ -193,33 +196,36 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   const u32x4 rq = rsrc_words(a.q + m0 * a.q_stride, (rows - 1) * stride + a.K);
   const int tiles = static_cast<int>((a.N + 15) / 16);
   const u32x4 rw = rsrc_words(a.codes, static_cast<uint32_t>(tiles) * a.units * 1024u);
-  const uint32_t base = lds_offset(lds);
+  const unsigned char* mine_lds = lds + team * RING * STAGE;
+  const uint32_t base = lds_offset(mine_lds);
 
-  // steps of this workgroup's share of the channels
-  int first = 0, steps = a.units;
+  // units of this workgroup's share of the channels; a team's last step may lie past them (zeros)
+  int first = 0, end = a.units;
   if (SPLIT) {
     first = static_cast<int>(static_cast<int64_t>(a.units) * blockIdx.y / gridDim.y);
-    steps = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.y + 1) / gridDim.y) - first;
+    end = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.y + 1) / gridDim.y);
   }
+  const int steps = (end - first + TEAMS - 1) / TEAMS;
 
   // 64 bytes of a row in LDS, their 16-byte pieces exchanged by the row's number (p ^ row / 2 % 4),
   // so that eight rows' equal pieces lie in different banks; the exchange is made where a lane loads
   const uint32_t lane_q = (lane >> 2) * stride + 16u * ((lane & 3) ^ ((lane >> 3) & 3));
   auto issue_piece = [&](int slot, int step, int i) {  // 1 KiB each: 16 rows, or a unit of W
     const uint32_t dst = base + slot * STAGE;
+    const int unit = first + TEAMS * step + team;
     if (i < PIECES_A) {
       const uint32_t piece = wave * PIECES_A + i;
-      load_to_lds(rq, lane_q + piece * 16u * stride + static_cast<uint32_t>(first + step) * kStep, dst + piece * 1024u);
+      load_to_lds(rq, lane_q + piece * 16u * stride + static_cast<uint32_t>(unit) * kStep, dst + piece * 1024u);
       return;
     }
     const int piece = wave * PIECES_W + i - PIECES_A, t = n0 / 16 + piece;
-    const uint32_t at = t < tiles ? (static_cast<uint32_t>(t) * a.units + first + step) * 1024u : kNoLoad;
+    const uint32_t at = t < tiles && (TEAMS == 1 || unit < end) ? (static_cast<uint32_t>(t) * a.units + unit) * 1024u : kNoLoad;
     load_to_lds(rw, at + 16u * lane, dst + BM * kStep + piece * 1024u);
   };
   // operands of half s of a step, in the order of their use: W's, then the rows'
   int4_t fq[2][FM], fw[2][FN];
   auto read_one = [&](int slot, int s, int i) {
-    const unsigned char* stage = lds + slot * STAGE;
+    const unsigned char* stage = mine_lds + slot * STAGE;
     if (i < FN) {
       const unsigned char* w = stage + BM * kStep + (wn * TN / 16 + (l32 >> 4)) * 1024 + 16 * ((lane & 15) + 16 * (2 * s + half));
       fw[s][i] = *reinterpret_cast<const int4_t*>(w + i * 2048);
@@ -282,6 +288,23 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
     }
   }
 
+  constexpr int PITCH = TN + 4;
+  if constexpr (TEAMS > 1) {  // behind the place of the output's transposition
+    int16_t_* sums = reinterpret_cast<int16_t_*>(lds + 4 * 32 * PITCH * 4) + wave * FM * FN * 64 + lane;
+    __syncthreads();  // all wavefronts have read their last operands
+    if (team == 1) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sums[(i * FN + j) * 64] = acc[i][j];
+    }
+    __syncthreads();
+    if (team == 1) return;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] += sums[(i * FN + j) * 64];
+  }
   // element e of lane l: output 8 (e / 4) + 4 (l / 32) + e % 4 of row l % 32
   if constexpr (SPLIT) {
 #pragma unroll
@@ -303,7 +326,7 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
   // and sixteen (or eight, or four) lanes a whole line; rows are 4 floats apart from the banks'
   // period. A lane's columns stay the same: their scales and biases are read once, and the
   // factors and residuals of all 32 rows are on their way while the sums go through LDS.
-  constexpr int PITCH = TN + 4, LANES = TN / 8, RUNS = LANES / 2;
+  constexpr int LANES = TN / 8, RUNS = LANES / 2;
   float* mine = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
   const int c = 8 * (lane % LANES), n = n0 + wn * TN + c;
   const bool in = n < a.N;
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(256, 2) i8_tile_kernel(I8Args a) {
     const int64_t m = m0 + wm * TM + 32 * i + l32;
     sx[i] = m < a.M ? a.scale[m] : 0.0f;
   }
-  __syncthreads();  // all wavefronts have read their last operands
+  if constexpr (TEAMS == 1) __syncthreads();  // all wavefronts have read their last operands
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t top = m0 + wm * TM + 32 * i + lane / LANES;
@@ -391,29 +414,32 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
 }
 
 // Which kernel a product takes: the one with the least time by an estimate in microseconds, whose
-// constants were fitted (by least squares of the logarithms, 9 % rms) to 1300 timings of all
+// constants were fitted (by least squares of the logarithms, 10 % rms) to 2400 timings of all
 // kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. On
-// those the choice costs 1.1 % more than the best one on average, 25 % at worst (33 x 8192 x 1024).
+// those the choice costs 1.6 % more than the best one on average, 26 % at worst (33 x 8192 x 1024).
 // A CU's blocks share its matrix cores (`work` each and step) and pass their steps not faster than
-// memory answers (`wait`, `fit` of them at a time).
+// memory answers (`wait`, `fit` of them at a time). Two teams win where 64 x 64 tiles leave CUs to
+// spare (200 x 4096 x 4096: 10.9 us, one team 12.9); with larger tiles they gained 2 % at most.
 struct Tile {
-  int bm, bn, fit;
+  int bm, bn, teams, fit;
   float work, wait, once;
 };
-constexpr Tile kTiles[] = {{64, 64, 5, 0.106f, 0.129f, 0.55f},
-                           {64, 128, 3, 0.145f, 0.150f, 1.11f},
-                           {128, 128, 2, 0.215f, 0.235f, 1.97f},
-                           {128, 256, 2, 0.352f, 0.380f, 3.34f}};
+constexpr Tile kTiles[] = {{64, 64, 1, 5, 0.106f, 0.131f, 0.52f},
+                           {64, 128, 1, 3, 0.153f, 0.143f, 0.97f},
+                           {128, 128, 1, 2, 0.215f, 0.231f, 1.69f},
+                           {128, 256, 1, 2, 0.345f, 0.370f, 3.12f},
+                           {64, 64, 2, 2, 0.191f, 0.178f, 1.11f}};
+constexpr int kKinds = sizeof(kTiles) / sizeof(kTiles[0]);
 constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 16};
 struct Choice {
   int tile, splits;  // tile -1: i8_rows_kernel
 };
 Choice choose(int64_t M, int64_t N, int64_t K) {
   if (const char* env = tuning_env("AWQ_I8_CFG")) {
-    int bm = 0, bn = 0, splits = 0;
-    if (sscanf(env, "%d,%d,%d", &bm, &bn, &splits) == 3) {
-      for (int t = 0; t < 4; ++t)
-        if (kTiles[t].bm == bm && kTiles[t].bn == bn) return {t, splits};
+    int bm = 0, bn = 0, splits = 0, teams = 1;
+    if (sscanf(env, "%d,%d,%d,%d", &bm, &bn, &splits, &teams) >= 3) {
+      for (int t = 0; t < kKinds; ++t)
+        if (kTiles[t].bm == bm && kTiles[t].bn == bn && kTiles[t].teams == teams) return {t, splits};
       return {-1, 1};
     }
   }
@@ -427,14 +453,14 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
   Choice best = {-1, 1};
   float least = 2.4f + units / 8.0f * (rounds > 1.0f ? rounds : 1.0f) *
                            (0.31f + 0.19f * (m / 16.0f < row_blocks ? m / 16.0f : static_cast<float>(row_blocks)));
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < kKinds; ++t)
     for (int splits : kSplits) {
-      if (splits > 1 && units < 2.0f * splits) break;
       const Tile& k = kTiles[t];
-      const float per_cu = ceilf(blocks(M, k.bm) * blocks(N, k.bn) * splits / kCus), steps = ceilf(units / splits);
+      if (splits > 1 && units < 2.0f * splits * k.teams) break;
+      const float per_cu = ceilf(blocks(M, k.bm) * blocks(N, k.bn) * splits / kCus), steps = ceilf(units / (splits * k.teams));
       const float waits = k.wait * ceilf(per_cu / k.fit), works = k.work * per_cu;
-      float time = 3.06f + steps * (waits > works ? waits : works) + k.once * per_cu;
-      if (splits > 1) time += 1.82f + 0.10f * splits + (8.0f * splits + 2.0f) * m * n / 6.5e6f;
+      float time = 2.87f + steps * (waits > works ? waits : works) + k.once * per_cu;
+      if (splits > 1) time += 1.86f + 0.11f * splits + (8.0f * splits + 2.0f) * m * n / 5.4e6f;
       if (time < least) {
         least = time;
         best = {t, splits};
@@ -443,19 +469,21 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-template <typename T, int BM, int BN>
+template <typename T, int BM, int BN, int TEAMS>
 hipError_t launch_tiles(const I8Args& a, int splits, hipStream_t st) {
-  constexpr int STAGES = ring(BM, BN) * (BM + BN) * kStep, TAIL = 4 * 32 * (BN / 2 + 4) * 4, LDS = STAGES > TAIL ? STAGES : TAIL;
+  constexpr int STAGES = TEAMS * ring(BM, BN) * (BM + BN) * kStep;
+  constexpr int TAIL = 4 * 32 * (BN / 2 + 4) * 4 + (TEAMS > 1 ? BM * BN * 4 : 0), LDS = STAGES > TAIL ? STAGES : TAIL;
+  static_assert(LDS <= 163840, "a CU's LDS");
   const unsigned blocks = static_cast<unsigned>((a.M + BM - 1) / BM * ((a.N + BN - 1) / BN));
   auto go = [&](auto kernel, std::atomic<uint64_t>& done) {
     const hipError_t e = ensure_lds_limit(reinterpret_cast<const void*>(kernel), LDS, done);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(kernel, dim3(blocks, splits), dim3(256), LDS, st, a);
+    hipLaunchKernelGGL(kernel, dim3(blocks, splits), dim3(256 * TEAMS), LDS, st, a);
     return hipGetLastError();
   };
   static std::atomic<uint64_t> whole{0}, split{0};
-  if (splits == 1) return go(&i8_tile_kernel<T, BM, BN, false>, whole);
-  hipError_t e = go(&i8_tile_kernel<T, BM, BN, true>, split);
+  if (splits == 1) return go(&i8_tile_kernel<T, BM, BN, TEAMS, false>, whole);
+  hipError_t e = go(&i8_tile_kernel<T, BM, BN, TEAMS, true>, split);
   if (e != hipSuccess) return e;
   int64_t sums = (a.M * a.N / 8 + 255) / 256;
   if (sums > 65536) sums = 65536;
@@ -467,10 +495,11 @@ template <typename T>
 hipError_t launch_as(const I8Args& a, hipStream_t st) {
   const Choice c = choose(a.M, a.N, a.K);
   switch (c.tile) {
-    case 0: return launch_tiles<T, 64, 64>(a, c.splits, st);
-    case 1: return launch_tiles<T, 64, 128>(a, c.splits, st);
-    case 2: return launch_tiles<T, 128, 128>(a, c.splits, st);
-    case 3: return launch_tiles<T, 128, 256>(a, c.splits, st);
+    case 0: return launch_tiles<T, 64, 64, 1>(a, c.splits, st);
+    case 1: return launch_tiles<T, 64, 128, 1>(a, c.splits, st);
+    case 2: return launch_tiles<T, 128, 128, 1>(a, c.splits, st);
+    case 3: return launch_tiles<T, 128, 256, 1>(a, c.splits, st);
+    case 4: return launch_tiles<T, 64, 64, 2>(a, c.splits, st);
     default: break;
   }
   const unsigned tiles = static_cast<unsigned>((a.N + 15) / 16);
