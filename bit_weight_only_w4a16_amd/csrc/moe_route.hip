@@ -9,7 +9,8 @@
 // Two launches: partial sums of 16 x 16 logits over slices of the channels (a token alone
 // would otherwise leave the card to a few wavefronts), then one wavefront or workgroup per
 // token that adds them and ranks the experts: an expert's place is the number of experts in
-// front of it, which all are counted at once, without a chain of k maxima.
+// front of it, which all are counted at once, without a chain of k maxima. A few tokens with a small
+// router take one launch.
 #include "ffn_internal.hpp"
 
 namespace awq {
@@ -123,15 +124,15 @@ __device__ __forceinline__ uint64_t order(double v) {
   return static_cast<uint64_t>(b < 0 ? ~b : b | INT64_MIN);
 }
 
-// THREADS threads for each token, NE experts each: lane's experts t, t + THREADS, ..
-template <int THREADS, int NE>
-__global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
-  constexpr int TOKENS = 256 / THREADS, WAVES = THREADS / 64, MOST = THREADS * NE;
+// THREADS threads for each of a workgroup's TOKENS tokens, NE experts each (t, t + THREADS, ..), whose
+// logits logit(e) gives. All threads of the workgroup call it.
+template <int THREADS, int NE, int TOKENS, typename Logit>
+__device__ __forceinline__ void choose(const RouteArgs& a, int64_t token, Logit logit) {
+  constexpr int WAVES = THREADS / 64, MOST = THREADS * NE;
   __shared__ uint64_t keys[TOKENS][MOST];
-  __shared__ double picked[TOKENS][32];
+  __shared__ double picked[TOKENS][AWQ_MOE_MAX_K];
   __shared__ double wave_top[TOKENS][WAVES], wave_add[TOKENS][WAVES];
   const int mine = threadIdx.x / THREADS, t = threadIdx.x % THREADS;
-  const int64_t token = static_cast<int64_t>(blockIdx.x) * TOKENS + mine;
   const bool live = token < a.tokens;
   double p[NE];
   double top = -__builtin_inf();
@@ -140,15 +141,7 @@ __global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
     const int e = t + THREADS * i;
     double l = 0.0;
     if (live && e < a.experts) {
-      const double* part = a.part + token * a.experts + e;
-      const int64_t slice = a.tokens * a.experts;
-      for (int s = 0; s < a.slices; s += 8) {  // eight at a time on their way
-        double v[8];
-#pragma unroll
-        for (int o = 0; o < 8; ++o) v[o] = part[min(s + o, a.slices - 1) * slice];
-#pragma unroll
-        for (int o = 0; o < 8; ++o) l += s + o < a.slices ? v[o] : 0.0;
-      }
+      l = logit(e);
       const double bias = a.bias == nullptr ? 0.0 : static_cast<double>(a.bias[e]);
       if (a.score == AWQ_SCORE_SIGMOID) l = 1.0 / (1.0 + exp(-l));
       keys[mine][e] = order(l + bias);
@@ -215,6 +208,70 @@ __global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
 }
 
 template <int THREADS, int NE>
+__global__ void __launch_bounds__(256) route_choose_kernel(RouteArgs a) {
+  constexpr int TOKENS = 256 / THREADS;
+  const int64_t token = static_cast<int64_t>(blockIdx.x) * TOKENS + threadIdx.x / THREADS;
+  choose<THREADS, NE, TOKENS>(a, token, [&](int e) {
+    const double* part = a.part + token * a.experts + e;
+    const int64_t slice = a.tokens * a.experts;
+    double l = 0.0;
+    for (int s = 0; s < a.slices; s += 8) {  // eight at a time on their way
+      double v[8];
+#pragma unroll
+      for (int o = 0; o < 8; ++o) v[o] = part[min(s + o, a.slices - 1) * slice];
+#pragma unroll
+      for (int o = 0; o < 8; ++o) l += s + o < a.slices ? v[o] : 0.0;
+    }
+    return l;
+  });
+}
+
+// A token or a few with a small router: everything in one workgroup and one launch. A wavefront takes
+// a run of the channels of one expert (wavefronts share experts while there are fewer of them), one
+// channel of each token in a lane's sums; the matrix cores' chains of dependent float64 products
+// would take longer here (90 ns each).
+constexpr int kSmallTokens = 4, kSmallExperts = 64, kSmallWaves = 16;
+bool is_small(int64_t tokens, int hidden, int experts) {
+  return tokens <= kSmallTokens && experts <= kSmallExperts && static_cast<int64_t>(experts) * hidden <= 65536;
+}
+template <typename T>
+__global__ void __launch_bounds__(64 * kSmallWaves) route_small_kernel(RouteArgs a) {
+  __shared__ double part[kSmallTokens][kSmallExperts][kSmallWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int share = a.experts >= kSmallWaves ? 1 : kSmallWaves / a.experts;  // wavefronts of an expert
+  const int tokens = static_cast<int>(a.tokens);
+  for (int e = wave / share; e < a.experts; e += kSmallWaves / share) {
+    double sum[kSmallTokens] = {0.0, 0.0, 0.0, 0.0};
+    for (int c = 8 * (64 * (wave % share) + lane); c < a.hidden; c += 512 * share) {
+      float w[8];
+      widen<T>(*reinterpret_cast<const uint4*>(a.w + static_cast<int64_t>(e) * a.hidden + c), w);
+#pragma unroll
+      for (int t = 0; t < kSmallTokens; ++t) {
+        if (t >= tokens) break;
+        float x[8];
+        widen<T>(*reinterpret_cast<const uint4*>(a.x + t * a.x_stride + c), x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          sum[t] = __builtin_fma(static_cast<double>(x[i]), static_cast<double>(w[i]), sum[t]);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kSmallTokens; ++t) {
+      if (t >= tokens) break;
+#pragma unroll
+      for (int s = 32; s > 0; s >>= 1) sum[t] += __shfl_xor(sum[t], s);
+      if (lane == 0) part[t][e][wave % share] = sum[t];
+    }
+  }
+  __syncthreads();
+  choose<64, 1, kSmallWaves>(a, wave, [&](int e) {
+    double l = 0.0;
+    for (int s = 0; s < share; ++s) l += part[wave][e][s];
+    return l;
+  });
+}
+
+template <int THREADS, int NE>
 hipError_t launch_choose(const RouteArgs& a, hipStream_t st) {
   constexpr int TOKENS = 256 / THREADS;
   hipLaunchKernelGGL((route_choose_kernel<THREADS, NE>), dim3(static_cast<unsigned>((a.tokens + TOKENS - 1) / TOKENS)),
@@ -225,6 +282,7 @@ hipError_t launch_choose(const RouteArgs& a, hipStream_t st) {
 }  // namespace
 
 size_t moe_route_workspace_bytes(int64_t tokens, int32_t hidden, int32_t experts) {
+  if (is_small(tokens, hidden, experts)) return 0;
   return static_cast<size_t>(8) * route_slices(tokens, hidden, experts) * tokens * experts;
 }
 
@@ -245,6 +303,11 @@ hipError_t launch_moe_route(const awq_moe_route_args& p, hipStream_t st) {
   a.score = p.score;
   a.renormalize = p.renormalize;
   a.scale = p.scale;
+  if (is_small(p.tokens, p.hidden, p.experts)) {
+    hipLaunchKernelGGL((p.dtype == AWQ_DT_F16 ? &route_small_kernel<F16> : &route_small_kernel<BF16>), dim3(1),
+                       dim3(64 * kSmallWaves), 0, st, a);
+    return hipGetLastError();
+  }
   const int wide = route_wide(p.tokens);
   const dim3 grid(static_cast<unsigned>((p.tokens + 16 * wide - 1) / (16 * wide)), (p.experts + 15) / 16, a.slices);
   const bool f16 = p.dtype == AWQ_DT_F16;

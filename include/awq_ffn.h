@@ -137,7 +137,8 @@ int awq_gemm_i8(const awq_gemm_i8_args* args, hipStream_t stream);
  * With a bias the softmax's choice is logit + bias too. k <= E <= 1024, k <= 32, tokens <=
  * 2^20, hidden a multiple of 8 up to 65536; x's rows x_stride elements apart (a multiple of
  * 8), w contiguous.
- * ws: device, awq_moe_route_workspace_bytes() bytes, overwritten.
+ * ws: device, awq_moe_route_workspace_bytes() bytes, overwritten; may be NULL with ws_bytes == 0
+ * where that is 0 (a few tokens with a small router).
  */
 typedef struct awq_moe_route_args {
   const void* x;     /* [tokens][hidden] */

@@ -137,7 +137,7 @@ def test_gemm_i8_asks_for_its_workspace(lib):
             assert call(lib.awq_gemm_i8, c_abi.GemmI8Args(**{**d, "ws": None, "ws_bytes": 0})) == WORKSPACE
 
 
-ROUTE = dict(x=P, w=P, bias=P, ids=P, weights=P, ws=P, ws_bytes=1 << 40, tokens=4, x_stride=256, hidden=256, experts=16,
+ROUTE = dict(x=P, w=P, bias=P, ids=P, weights=P, ws=P, ws_bytes=1 << 40, tokens=40, x_stride=256, hidden=256, experts=16,
              k=2, dtype=0, score=0, renormalize=1, scale=1.0)
 
 
@@ -153,6 +153,14 @@ ROUTE = dict(x=P, w=P, bias=P, ids=P, weights=P, ws=P, ws_bytes=1 << 40, tokens=
 ])
 def test_route_refusals(lib, change, code):
     assert call(lib.awq_moe_route, c_abi.MoeRouteArgs(**{**ROUTE, **change})) == code
+
+
+def test_route_workspace_sizes(lib):
+    f = moe.awq_moe_route_workspace_bytes
+    assert f(0, 256, 16) == f(-1, 256, 16) == f(4, 252, 16) == f(4, 256, 2000) == 0
+    assert f(4, 4096, 16) == 0 and f(5, 4096, 16) > 0 and f(4, 4104, 16) > 0 and f(1, 8, 65) > 0
+    # a float64 for each token and expert, of each slice of the channels
+    assert f(517, 4096, 128) % (517 * 128 * 8) == 0
 
 
 MOE = dict(x=P, ids=P, weights=P, gate=P, up=P, down=P, inv_in=P, inv_down=P, residual=P, y=P, ws=P, ws_bytes=1 << 40,

@@ -310,7 +310,8 @@ def test_int8_linear():
 @TYPES
 @pytest.mark.parametrize("tokens,hidden,experts,k", [
     (1, 8, 1, 1), (1, 4096, 8, 2), (2, 64, 3, 3), (7, 1000, 17, 4), (16, 2048, 64, 8), (17, 512, 65, 8), (33, 4104, 60, 6),
-    (5, 328, 256, 8), (3, 256, 257, 32), (40, 136, 1024, 32), (517, 256, 128, 8),
+    (5, 328, 256, 8), (3, 256, 257, 32), (40, 136, 1024, 32), (517, 256, 128, 8), (4, 4096, 16, 8), (4, 1024, 64, 32),
+    (3, 24, 5, 2), (4, 5000, 13, 3), (1, 65536, 1, 1), (2, 520, 33, 6),
 ])
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route(dtype, tokens, hidden, experts, k, score):
