@@ -24,10 +24,6 @@ namespace {
 
 constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX_K;
 constexpr int kUpWaves = 4;
-// Units of a wavefront on their way: in the first launch by its number of tiles (two layers'
-// weights each), in the second of weights and, half as many, of rows.
-constexpr int up_ahead(int wide) { return wide == 1 ? 4 : 2; }
-constexpr int kAheadW = 4, kAheadX = 2;
 constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
 
 struct Layers {  // a stack of packed layers
@@ -221,7 +217,7 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
 // grid: the outputs' workgroups and one for the plan, experts that may be named
 template <bool ASYM, int WIDE, int SHARE, int CHUNKS>
 __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
-  constexpr int TILES = WIDE * kUpWaves / SHARE, AHEAD = up_ahead(WIDE);
+  constexpr int TILES = WIDE * kUpWaves / SHARE;
   __shared__ uint32_t bits[kMostExperts / 32];
   __shared__ int ids[kMostPairs];
   __shared__ int row_pair[64];
@@ -251,17 +247,16 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
     rg[t] = reader(a.gate, e, tile0 + t, units, a.sets);
     ru[t] = reader(a.up, e, tile0 + t, units, a.sets);
   }
-  Piece pg[AHEAD][WIDE], pu[AHEAD][WIDE];
-  auto load = [&](int i, int unit) {
+  Piece pg[WIDE], pu[WIDE];
+  auto load = [&](int unit) {
     const uint32_t skip = unit < units ? 0u : kNoLoad;
 #pragma unroll
     for (int t = 0; t < WIDE; ++t) {
-      pg[i][t] = load_piece<ASYM>(rg[t], unit, a.sets, lane, skip);
-      pu[i][t] = load_piece<ASYM>(ru[t], unit, a.sets, lane, skip);
+      pg[t] = load_piece<ASYM>(rg[t], unit, a.sets, lane, skip);
+      pu[t] = load_piece<ASYM>(ru[t], unit, a.sets, lane, skip);
     }
   };
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load(i, part + SHARE * i);
+  load(part);
 
   const Rows rows = rows_of(a, ids, e);
   const int count = __popcll(rows.tokens), chunks = (count + 15) / 16;
@@ -285,34 +280,31 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
 #pragma unroll
     for (int t = 0; t < WIDE; ++t) g[c][t] = u[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int at0 = part; at0 < units; at0 += SHARE * AHEAD) {
+  // One unit ahead: four wavefronts on a SIMD hide more than two whose registers hold more units
+  // (one token through two of eight experts, this launch: 25 us, with two units ahead 27, three 32).
+  for (int at = part; at < units; at += SHARE) {
+    half8_t f[CHUNKS][4];
+    load_x(x[0], at, f[0]);
 #pragma unroll
-    for (int n = 0; n < AHEAD; ++n) {
-      const int at = at0 + SHARE * n;
-      if (at >= units) break;
-      half8_t f[CHUNKS][4];
-      load_x(x[0], at, f[0]);
+    for (int c = 1; c < CHUNKS; ++c)
+      if (c < chunks) load_x(x[c], at, f[c]);
 #pragma unroll
-      for (int c = 1; c < CHUNKS; ++c)
-        if (c < chunks) load_x(x[c], at, f[c]);
+    for (int t = 0; t < WIDE; ++t) {
+      const Dequant dg = constants<ASYM>(pg[t], lane), du = constants<ASYM>(pu[t], lane);
 #pragma unroll
-      for (int t = 0; t < WIDE; ++t) {
-        const Dequant dg = constants<ASYM>(pg[n][t], lane), du = constants<ASYM>(pu[n][t], lane);
+      for (int i = 0; i < 4; ++i) {
+        const half8_t wg = weights8(pg[t], i, dg), wu = weights8(pu[t], i, du);
+        g[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wg, g[0][t], 0, 0, 0);
+        u[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wu, u[0][t], 0, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const half8_t wg = weights8(pg[n][t], i, dg), wu = weights8(pu[n][t], i, du);
-          g[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wg, g[0][t], 0, 0, 0);
-          u[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wu, u[0][t], 0, 0, 0);
-#pragma unroll
-          for (int c = 1; c < CHUNKS; ++c) {
-            if (c >= chunks) break;
-            g[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wg, g[c][t], 0, 0, 0);
-            u[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wu, u[c][t], 0, 0, 0);
-          }
+        for (int c = 1; c < CHUNKS; ++c) {
+          if (c >= chunks) break;
+          g[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wg, g[c][t], 0, 0, 0);
+          u[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wu, u[c][t], 0, 0, 0);
         }
       }
-      load(n, at + SHARE * AHEAD);
     }
+    load(at + SHARE);
   }
 #pragma unroll
   for (int c = 0; c < CHUNKS; ++c) {
@@ -354,9 +346,10 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   }
 }
 
-// Workgroups own WIDE tiles of 16 hidden outputs. grid: those, splits of the named experts' units.
+// Workgroups own WIDE tiles of 16 hidden outputs; a wavefront asks for weights AHEAD_W units ahead and
+// for rows AHEAD_X. grid: the outputs' workgroups, splits of the named experts' units.
 // Dynamic LDS: [waves][tokens][16 WIDE] float32.
-template <bool ASYM, int WIDE, int WAVES, int CHUNKS>
+template <bool ASYM, int WIDE, int WAVES, int CHUNKS, int AHEAD_W, int AHEAD_X>
 __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   constexpr int OUT = 16 * WIDE;
   __shared__ int experts[kMostExperts], first[kMostExperts + 1];
@@ -395,8 +388,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
       ++c.slot;
     }
   };
-  Piece pw[kAheadW][WIDE];
-  half8_t px[kAheadX][4];  // of the expert's first 16 rows
+  Piece pw[AHEAD_W][WIDE];
+  half8_t px[AHEAD_X][4];  // of the expert's first 16 rows
   auto load_w = [&](Piece (&w)[WIDE], const Cursor& c, int at) {
     const bool real = at < end;
     const int e = __builtin_amdgcn_readfirstlane(experts[real ? c.slot : 0]);
@@ -415,12 +408,12 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   if (begin < end) {
     Cursor now = {begin / units, begin % units}, ahead_w = now, ahead_x = now;
 #pragma unroll
-    for (int i = 0; i < kAheadW; ++i) {
+    for (int i = 0; i < AHEAD_W; ++i) {
       load_w(pw[i], ahead_w, begin + i);
       next(ahead_w);
     }
 #pragma unroll
-    for (int i = 0; i < kAheadX; ++i) {
+    for (int i = 0; i < AHEAD_X; ++i) {
       load_x(px[i], ahead_x, begin + i);
       next(ahead_x);
     }
@@ -429,9 +422,9 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
       for (int t = 0; t < WIDE; ++t) d[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int at0 = begin; at0 < end; at0 += kAheadW) {
+    for (int at0 = begin; at0 < end; at0 += AHEAD_W) {
 #pragma unroll
-      for (int n = 0; n < kAheadW; ++n) {
+      for (int n = 0; n < AHEAD_W; ++n) {
         const int at = at0 + n;
         if (at >= end) break;
         const int row0 = first[now.slot], count = __builtin_amdgcn_readfirstlane(first[now.slot + 1] - row0);
@@ -442,12 +435,12 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             w[t][i] = weights8(pw[n][t], i, dq);
-            d[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % kAheadX][i], w[t][i], d[0][t], 0, 0, 0);
+            d[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % AHEAD_X][i], w[t][i], d[0][t], 0, 0, 0);
           }
         }
-        load_w(pw[n], ahead_w, at + kAheadW);
+        load_w(pw[n], ahead_w, at + AHEAD_W);
         next(ahead_w);
-        load_x(px[n % kAheadX], ahead_x, at + kAheadX);
+        load_x(px[n % AHEAD_X], ahead_x, at + AHEAD_X);
         next(ahead_x);
 #pragma unroll
         for (int c = 1; c < CHUNKS; ++c) {
@@ -526,7 +519,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
 
 // The second launch. More than 16 tokens: two tiles for each wavefront, whose rows' loads are most
 // of what it does, and eight wavefronts with the registers for that (48 tokens over 64 experts:
-// 76 -> 64 us for its part); else sixteen wavefronts with one. Workgroups share outputs so that at
+// 76 -> 64 us for its part); else sixteen wavefronts with one and few units ahead (one token through two of
+// eight experts 20 us; eight wavefronts with eight units ahead 24). Workgroups share outputs so that at
 // least one runs on each CU.
 struct Down {
   int wide, waves, splits;
@@ -613,7 +607,6 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   auto up_fmt = [&](auto fmt) {
     constexpr bool ASYM = decltype(fmt)::value;
     if (a.tokens <= 16) {
-      if (all >= 1024) return up(&moe_up_kernel<ASYM, 4, 4, 1>, 4);
       if (all >= 512) return up(&moe_up_kernel<ASYM, 2, 4, 1>, 2);
       return up(&moe_up_kernel<ASYM, 1, 4, 1>, 1);
     }
@@ -635,9 +628,10 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   };
   static std::atomic<uint64_t> done[4];
   if (a.tokens <= 16)
-    return asym ? down(&moe_down_kernel<true, 1, 16, 1>, done[0]) : down(&moe_down_kernel<false, 1, 16, 1>, done[1]);
-  return asym ? down(&moe_down_kernel<true, 2, 8, kChunks>, done[2])
-              : down(&moe_down_kernel<false, 2, 8, kChunks>, done[3]);
+    return asym ? down(&moe_down_kernel<true, 1, 16, 1, 2, 1>, done[0])
+                : down(&moe_down_kernel<false, 1, 16, 1, 2, 1>, done[1]);
+  return asym ? down(&moe_down_kernel<true, 2, 8, kChunks, 4, 2>, done[2])
+              : down(&moe_down_kernel<false, 2, 8, kChunks, 4, 2>, done[3]);
 }
 
 }  // namespace awq
