@@ -23,8 +23,12 @@ namespace awq {
 namespace {
 
 constexpr int kMostExperts = 1024, kMostPairs = AWQ_MOE_MAX_TOKENS * AWQ_MOE_MAX_K;
-constexpr int kUpWaves = 4;
-constexpr int kChunks = AWQ_MOE_MAX_TOKENS / 16;
+constexpr int kUpWaves = 4, kDownWaves = 16, kDownWide = 2, kAheadW = 2;
+// Rows of an expert that a wavefront has sums for at a time: chunks of 16, one for up to 16 tokens,
+// else two (four, for 64 tokens, left two wavefronts on a SIMD); an expert of more tokens is read
+// again for them.
+constexpr int kChunks = 2;
+constexpr int kMostRuns = kMostExperts + kMostPairs / (16 * kChunks);
 
 struct Layers {  // a stack of packed layers
   const uint8_t* base;
@@ -34,9 +38,9 @@ struct Layers {  // a stack of packed layers
 
 // What the first launch tells the second (in the workspace).
 struct Plan {
-  int32_t* total;    // named experts
-  int32_t* experts;  // [pairs]: which, ascending
-  int32_t* first;    // [pairs + 1]: where an expert's tokens begin in the next two
+  int32_t* total;    // runs: a named expert with up to 16 CHUNKS of its tokens
+  int32_t* experts;  // [pairs]: a run's expert, ascending
+  int32_t* first;    // [pairs + 1]: where a run's tokens begin in the next two
   int32_t* pair;     // [pairs]: token * k + j
   float* weight;     // [pairs]
   int32_t* ended;    // [tiles]: workgroups that have written their sums
@@ -150,14 +154,14 @@ __device__ __forceinline__ half8_t load_half8(const uint16_t* p) {
 // The plan, by one workgroup. Where an expert's tokens stand among each other depends on the
 // order of the atomics, what is computed for each of them does not.
 __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, const uint32_t* bits, const Named& named,
-                                           int tiles) {
+                                           int tiles, int most_rows) {
   __shared__ int before[kMostExperts / 32];
-  __shared__ int begin[kMostExperts], taken[kMostExperts];
+  __shared__ int who[kMostExperts], begin[kMostExperts], taken[kMostExperts];
   const int lane = threadIdx.x & 63, pairs = a.tokens * a.k;
   if (threadIdx.x < kMostExperts / 32) {
     before[lane] = named.before;
     uint32_t word = named.word;
-    for (int at = named.before; word != 0; ++at, word &= word - 1) a.plan.experts[at] = 32 * lane + __builtin_ctz(word);
+    for (int at = named.before; word != 0; ++at, word &= word - 1) who[at] = 32 * lane + __builtin_ctz(word);
   }
   for (int i = threadIdx.x; i < named.total; i += blockDim.x) taken[i] = 0;
   for (int i = threadIdx.x; i < tiles; i += blockDim.x) a.plan.ended[i] = 0;
@@ -175,29 +179,34 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
     if (at >= 0) atomicAdd(&taken[at], 1);
   }
   __syncthreads();
-  if (threadIdx.x < 64) {  // begin[i] = the sum of taken before i
+  if (threadIdx.x < 64) {  // sums over the experts before one: of tokens (low half) and of runs
     int base = 0;
     for (int i0 = 0; i0 < named.total; i0 += 64) {
-      const int mine = i0 + lane < named.total ? taken[i0 + lane] : 0;
+      const int rows = i0 + lane < named.total ? taken[i0 + lane] : 0;
+      const int runs = (rows + most_rows - 1) / most_rows, mine = rows | runs << 16;
       int upto = mine;
 #pragma unroll
       for (int s = 1; s < 64; s <<= 1) {
         const int other = __shfl_up(upto, s);
         if (lane >= s) upto += other;
       }
-      if (i0 + lane < named.total) begin[i0 + lane] = base + upto - mine;
+      const int from = base + upto - mine;
+      if (i0 + lane < named.total) {
+        begin[i0 + lane] = from & 0xFFFF;
+        for (int n = 0; n < runs; ++n) {
+          a.plan.experts[(from >> 16) + n] = who[i0 + lane];
+          a.plan.first[(from >> 16) + n] = (from & 0xFFFF) + n * most_rows;
+        }
+      }
       base += __shfl(upto, 63);
     }
     if (lane == 0) {
-      a.plan.first[named.total] = base;
-      *a.plan.total = named.total;
+      a.plan.first[base >> 16] = base & 0xFFFF;
+      *a.plan.total = base >> 16;
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < named.total; i += blockDim.x) {
-    a.plan.first[i] = begin[i];
-    taken[i] = 0;
-  }
+  for (int i = threadIdx.x; i < named.total; i += blockDim.x) taken[i] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
     const int at = place(i);
@@ -211,26 +220,24 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
   }
 }
 
-// Wavefronts own WIDE tiles of 16 ffn outputs, SHARE wavefronts the same ones with every SHARE-th
-// unit each. The rows' operands of a unit serve all of a wavefront's tiles (with one tile each, the
-// rows' loads took a fifth to a quarter of the time).
-// grid: the outputs' workgroups and one for the plan, experts that may be named
-template <bool ASYM, int WIDE, int SHARE, int CHUNKS>
+// A workgroup owns WIDE tiles of 16 ffn outputs of one expert; its four wavefronts take every fourth
+// unit each, and a unit's rows serve all tiles (with one tile each, the rows' loads took a fifth to a
+// quarter of the time). grid: the outputs' workgroups and one for the plan, experts that may be named
+template <bool ASYM, int WIDE, int CHUNKS>
 __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
-  constexpr int TILES = WIDE * kUpWaves / SHARE;
   __shared__ uint32_t bits[kMostExperts / 32];
   __shared__ int ids[kMostPairs];
   __shared__ int row_pair[64];
-  __shared__ float4_t red[SHARE == 1 ? 1 : kUpWaves][WIDE][2][64];
+  __shared__ float4_t red[kUpWaves][WIDE][2][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int r = lane & 15, p = lane >> 4, part = wave % SHARE;
+  const int r = lane & 15, p = lane >> 4;
   const int slot = blockIdx.y;
   const bool plans = blockIdx.x == gridDim.x - 1;
   if (plans && slot != 0) return;
   find_named(a, ids, bits);
   const Named named = count_named(bits);
   if (plans) {
-    write_plan(a, ids, bits, named, a.hidden / kTileN);
+    write_plan(a, ids, bits, named, a.hidden / kTileN, 16 * CHUNKS);
     return;
   }
   if (slot >= named.total) return;
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
   for (int skip = slot - __shfl(named.before, word_at); skip > 0; --skip) word &= word - 1;
   const int e = __builtin_amdgcn_readfirstlane(32 * word_at + __builtin_ctz(word));
 
-  const int units = a.hidden / kGroup, tile0 = blockIdx.x * TILES + wave / SHARE * WIDE;
+  const int units = a.hidden / kGroup, tile0 = blockIdx.x * WIDE;
   Reader rg[WIDE], ru[WIDE];
 #pragma unroll
   for (int t = 0; t < WIDE; ++t) {
@@ -256,16 +263,12 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
       pu[t] = load_piece<ASYM>(ru[t], unit, a.sets, lane, skip);
     }
   };
-  load(part);
+  load(wave);
 
   const Rows rows = rows_of(a, ids, e);
-  const int count = __popcll(rows.tokens), chunks = (count + 15) / 16;
+  const int all_rows = __popcll(rows.tokens);
   if (wave == 0 && rows.pair >= 0) row_pair[__popcll(rows.tokens & ((uint64_t{1} << lane) - 1))] = rows.pair;
   __syncthreads();
-  // rows past the last repeat it; their results are dropped
-  const uint16_t* x[CHUNKS];
-#pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) x[c] = a.x + row_pair[min(16 * c + r, count - 1)] / a.k * a.x_stride + 32 * p;
   const uint16_t* inv = a.inv_in == nullptr ? nullptr : a.inv_in + e * a.inv_in_stride + 32 * p;
   auto load_x = [&](const uint16_t* from, int unit, half8_t (&f)[4]) {
 #pragma unroll
@@ -274,85 +277,85 @@ __global__ void __launch_bounds__(64 * kUpWaves) moe_up_kernel(MoeArgs a) {
       if (inv != nullptr) f[i] *= load_half8(inv + unit * kGroup + 8 * i);
     }
   };
-  float4_t g[CHUNKS][WIDE], u[CHUNKS][WIDE];
+  for (int row0 = 0; row0 < all_rows; row0 += 16 * CHUNKS) {
+    if (row0 > 0) load(wave);
+    // rows past the last repeat it; their results are dropped
+    const int count = min(all_rows - row0, 16 * CHUNKS), chunks = (count + 15) / 16;
+    const uint16_t* x[CHUNKS];
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c)
+    for (int c = 0; c < CHUNKS; ++c) x[c] = a.x + row_pair[row0 + min(16 * c + r, count - 1)] / a.k * a.x_stride + 32 * p;
+    float4_t g[CHUNKS][WIDE], u[CHUNKS][WIDE];
 #pragma unroll
-    for (int t = 0; t < WIDE; ++t) g[c][t] = u[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+      for (int t = 0; t < WIDE; ++t) g[c][t] = u[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // One unit ahead: four wavefronts on a SIMD hide more than two whose registers hold more units
-  // (one token through two of eight experts, this launch: 25 us, with two units ahead 27, three 32).
-  for (int at = part; at < units; at += SHARE) {
-    half8_t f[CHUNKS][4];
-    load_x(x[0], at, f[0]);
+    // One unit ahead: four wavefronts on a SIMD hide more than two whose registers hold more units
+    // (one token through two of eight experts, this launch: 25 us, with two units ahead 27, three 32).
+    for (int at = wave; at < units; at += kUpWaves) {
+      half8_t f[CHUNKS][4];
+      load_x(x[0], at, f[0]);
 #pragma unroll
-    for (int c = 1; c < CHUNKS; ++c)
-      if (c < chunks) load_x(x[c], at, f[c]);
+      for (int c = 1; c < CHUNKS; ++c)
+        if (c < chunks) load_x(x[c], at, f[c]);
 #pragma unroll
-    for (int t = 0; t < WIDE; ++t) {
-      const Dequant dg = constants<ASYM>(pg[t], lane), du = constants<ASYM>(pu[t], lane);
+      for (int t = 0; t < WIDE; ++t) {
+        const Dequant dg = constants<ASYM>(pg[t], lane), du = constants<ASYM>(pu[t], lane);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const half8_t wg = weights8(pg[t], i, dg), wu = weights8(pu[t], i, du);
-        g[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wg, g[0][t], 0, 0, 0);
-        u[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wu, u[0][t], 0, 0, 0);
+        for (int i = 0; i < 4; ++i) {
+          const half8_t wg = weights8(pg[t], i, dg), wu = weights8(pu[t], i, du);
+          g[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wg, g[0][t], 0, 0, 0);
+          u[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[0][i], wu, u[0][t], 0, 0, 0);
 #pragma unroll
-        for (int c = 1; c < CHUNKS; ++c) {
-          if (c >= chunks) break;
-          g[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wg, g[c][t], 0, 0, 0);
-          u[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wu, u[c][t], 0, 0, 0);
+          for (int c = 1; c < CHUNKS; ++c) {
+            if (c >= chunks) break;
+            g[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wg, g[c][t], 0, 0, 0);
+            u[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f[c][i], wu, u[c][t], 0, 0, 0);
+          }
         }
       }
+      load(at + kUpWaves);
     }
-    load(at + SHARE);
-  }
 #pragma unroll
-  for (int c = 0; c < CHUNKS; ++c) {
-    if (c >= chunks) break;
-    if constexpr (SHARE > 1) {
-      if (c > 0) __syncthreads();  // the sums of the rows before these have been read
+    for (int c = 0; c < CHUNKS; ++c) {
+      if (c >= chunks) break;
+      if (c > 0 || row0 > 0) __syncthreads();  // the sums of the rows before these have been read
 #pragma unroll
       for (int t = 0; t < WIDE; ++t) {
         red[wave][t][0][lane] = g[c][t];
         red[wave][t][1][lane] = u[c][t];
       }
       __syncthreads();
-    }
-    // the wavefronts that share tiles divide them among themselves
+      if (wave < WIDE) {  // a wavefront for each tile
+        const int t = wave;
+        float4_t sg = red[0][t][0][lane], su = red[0][t][1][lane];
 #pragma unroll
-    for (int t = 0; t < WIDE; ++t) {
-      if (t % SHARE != part) continue;
-      float4_t sg = g[c][t], su = u[c][t];
-      if constexpr (SHARE > 1) {
-        const int w0 = wave - part;
-        sg = red[w0][t][0][lane];
-        su = red[w0][t][1][lane];
-#pragma unroll
-        for (int w = 1; w < SHARE; ++w) {
-          sg += red[w0 + w][t][0][lane];
-          su += red[w0 + w][t][1][lane];
+        for (int w = 1; w < kUpWaves; ++w) {
+          sg += red[w][t][0][lane];
+          su += red[w][t][1][lane];
         }
-      }
-      const int out = (tile0 + t) * kTileN + r;
-      const float scale = a.inv_down == nullptr ? 1.0f : f16_to_f32(a.inv_down[e * a.inv_down_stride + out]);
+        const int out = (tile0 + t) * kTileN + r;
+        const float scale = a.inv_down == nullptr ? 1.0f : f16_to_f32(a.inv_down[e * a.inv_down_stride + out]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int m = 16 * c + 4 * p + j;
-        if (m >= count) continue;
-        const float v = activate(sg[j], a.act) * su[j] * scale;
-        a.mid[static_cast<int64_t>(row_pair[m]) * a.ffn + out] = __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+        for (int j = 0; j < 4; ++j) {
+          const int m = 16 * c + 4 * p + j;
+          if (m >= count) continue;
+          const float v = activate(sg[j], a.act) * su[j] * scale;
+          a.mid[static_cast<int64_t>(row_pair[row0 + m]) * a.ffn + out] =
+              __builtin_bit_cast(uint16_t, static_cast<_Float16>(v));
+        }
       }
     }
   }
 }
 
-// Workgroups own WIDE tiles of 16 hidden outputs; a wavefront asks for weights AHEAD_W units ahead and
-// for rows AHEAD_X. grid: the outputs' workgroups, splits of the named experts' units.
+// Workgroups own two tiles of 16 hidden outputs; a wavefront asks for weights two units ahead and for
+// rows one. grid: the outputs' workgroups, splits of the runs' units.
 // Dynamic LDS: [waves][tokens][16 WIDE] float32.
-template <bool ASYM, int WIDE, int WAVES, int CHUNKS, int AHEAD_W, int AHEAD_X>
-__global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
-  constexpr int OUT = 16 * WIDE;
-  __shared__ int experts[kMostExperts], first[kMostExperts + 1];
+template <bool ASYM, int CHUNKS>
+__global__ void __launch_bounds__(64 * kDownWaves) moe_down_kernel(MoeArgs a) {
+  constexpr int WIDE = kDownWide, WAVES = kDownWaves, OUT = 16 * WIDE;
+  __shared__ int experts[kMostRuns], first[kMostRuns + 1];
   __shared__ int row_pair[kMostPairs];
   __shared__ float row_weight[kMostPairs];
   __shared__ int last_one;
@@ -364,9 +367,9 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   for (int i = lane; i < a.tokens * OUT; i += 64) mine[i] = 0.0f;
   const int total = *a.plan.total;
   for (int i = threadIdx.x; i <= pairs; i += 64 * WAVES) {
-    // what lies behind the last named expert (of kMostExperts at most) is not used
-    if (i <= kMostExperts) first[i] = a.plan.first[i];
-    if (i < kMostExperts && i < pairs) experts[i] = a.plan.experts[i];
+    // what lies behind the last run (of kMostRuns at most) is not used
+    if (i <= kMostRuns) first[i] = a.plan.first[i];
+    if (i < kMostRuns && i < pairs) experts[i] = a.plan.experts[i];
     if (i < pairs) {
       row_pair[i] = a.plan.pair[i];
       row_weight[i] = a.plan.weight[i];
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   }
   __syncthreads();
 
-  // this wavefront's run of the named experts' units
+  // this wavefront's share of the runs' units
   const int units = a.ffn / kGroup, all = total * units, waves = WAVES * gridDim.y;
   const int number = blockIdx.y * WAVES + wave;
   const int begin = static_cast<int>(static_cast<int64_t>(all) * number / waves);
@@ -388,8 +391,8 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
       ++c.slot;
     }
   };
-  Piece pw[AHEAD_W][WIDE];
-  half8_t px[AHEAD_X][4];  // of the expert's first 16 rows
+  Piece pw[kAheadW][WIDE];
+  half8_t px[4];  // of a run's first 16 rows
   auto load_w = [&](Piece (&w)[WIDE], const Cursor& c, int at) {
     const bool real = at < end;
     const int e = __builtin_amdgcn_readfirstlane(experts[real ? c.slot : 0]);
@@ -408,23 +411,20 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   if (begin < end) {
     Cursor now = {begin / units, begin % units}, ahead_w = now, ahead_x = now;
 #pragma unroll
-    for (int i = 0; i < AHEAD_W; ++i) {
+    for (int i = 0; i < kAheadW; ++i) {
       load_w(pw[i], ahead_w, begin + i);
       next(ahead_w);
     }
-#pragma unroll
-    for (int i = 0; i < AHEAD_X; ++i) {
-      load_x(px[i], ahead_x, begin + i);
-      next(ahead_x);
-    }
+    load_x(px, ahead_x, begin);
+    next(ahead_x);
     float4_t d[CHUNKS][WIDE];
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
       for (int t = 0; t < WIDE; ++t) d[c][t] = float4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int at0 = begin; at0 < end; at0 += AHEAD_W) {
+    for (int at0 = begin; at0 < end; at0 += kAheadW) {
 #pragma unroll
-      for (int n = 0; n < AHEAD_W; ++n) {
+      for (int n = 0; n < kAheadW; ++n) {
         const int at = at0 + n;
         if (at >= end) break;
         const int row0 = first[now.slot], count = __builtin_amdgcn_readfirstlane(first[now.slot + 1] - row0);
@@ -435,12 +435,12 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             w[t][i] = weights8(pw[n][t], i, dq);
-            d[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[n % AHEAD_X][i], w[t][i], d[0][t], 0, 0, 0);
+            d[0][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(px[i], w[t][i], d[0][t], 0, 0, 0);
           }
         }
-        load_w(pw[n], ahead_w, at + AHEAD_W);
+        load_w(pw[n], ahead_w, at + kAheadW);
         next(ahead_w);
-        load_x(px[n % AHEAD_X], ahead_x, at + AHEAD_X);
+        load_x(px, ahead_x, at + 1);
         next(ahead_x);
 #pragma unroll
         for (int c = 1; c < CHUNKS; ++c) {
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
             for (int t = 0; t < WIDE; ++t) d[c][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, w[t][i], d[c][t], 0, 0, 0);
           }
         }
-        if (now.unit == units - 1 || at + 1 == end) {  // this wavefront's share of the expert is complete
+        if (now.unit == units - 1 || at + 1 == end) {  // this wavefront's share of the run is complete
 #pragma unroll
           for (int c = 0; c < CHUNKS; ++c) {
             if (16 * c >= count) break;
@@ -517,20 +517,12 @@ __global__ void __launch_bounds__(64 * WAVES) moe_down_kernel(MoeArgs a) {
   }
 }
 
-// The second launch. More than 16 tokens: two tiles for each wavefront, whose rows' loads are most
-// of what it does, and eight wavefronts with the registers for that (48 tokens over 64 experts:
-// 76 -> 64 us for its part); else sixteen wavefronts with one and few units ahead (one token through two of
-// eight experts 20 us; eight wavefronts with eight units ahead 24). Workgroups share outputs so that at
-// least one runs on each CU.
-struct Down {
-  int wide, waves, splits;
-};
-Down down_for(int64_t tokens, int hidden) {
-  Down d = {tokens > 16 ? 2 : 1, tokens > 16 ? 8 : 16, 1};
-  const int groups = hidden / (kTileN * d.wide);
-  d.splits = (256 + groups - 1) / groups;
-  if (d.splits > 16) d.splits = 16;
-  return d;
+// Workgroups that share outputs in the second launch, so that at least one runs on each CU. (One
+// token through two of eight experts, that launch: 18.6 us; with one tile 20, with eight wavefronts
+// and eight units ahead 24. 48 tokens over 64 experts: 60, 72 and 76.)
+int down_splits(int hidden) {
+  const int groups = hidden / (kTileN * kDownWide), splits = (256 + groups - 1) / groups;
+  return splits > 16 ? 16 : splits;
 }
 
 Layers make_layers(const void* base, int64_t N, int64_t K, int32_t group, int32_t fmt) {
@@ -556,7 +548,7 @@ size_t lay_out(int64_t tokens, int hidden, int ffn, int k, void* ws, uint16_t** 
   p.pair = reinterpret_cast<int32_t*>(take(4 * pairs));
   p.weight = reinterpret_cast<float*>(take(4 * pairs));
   p.ended = reinterpret_cast<int32_t*>(take(4 * tiles));
-  const int splits = down_for(tokens, hidden).splits;
+  const int splits = down_splits(hidden);
   p.part = reinterpret_cast<float*>(take(splits == 1 ? 0 : 4 * splits * tiles * tokens * 16));
   if (mid != nullptr) *mid = m;
   if (plan != nullptr) *plan = p;
@@ -597,41 +589,30 @@ hipError_t launch_moe(const awq_moe_args& p, hipStream_t st) {
   const int64_t pairs = p.tokens * p.k;
   const int slots = static_cast<int>(pairs < p.experts ? pairs : p.experts);
   const bool asym = p.fmt == AWQ_FMT_ASYM;
-  // As many tiles for a wavefront as leave about 1024 wavefronts; up to four wavefronts share
-  // tiles. More than 16 rows for an expert take twice the registers for each tile.
-  const int tiles = p.ffn / kTileN, all = tiles * slots;
-  auto up = [&](auto kernel, int per_group) {
-    // tiles come in eights
-    hipLaunchKernelGGL(kernel, dim3(tiles / per_group + 1, slots), dim3(64 * kUpWaves), 0, st, a);
+  const int tiles = p.ffn / kTileN;  // a multiple of eight
+  auto up = [&](auto kernel, int wide) {
+    hipLaunchKernelGGL(kernel, dim3(tiles / wide + 1, slots), dim3(64 * kUpWaves), 0, st, a);
   };
   auto up_fmt = [&](auto fmt) {
     constexpr bool ASYM = decltype(fmt)::value;
-    if (a.tokens <= 16) {
-      if (all >= 512) return up(&moe_up_kernel<ASYM, 2, 4, 1>, 2);
-      return up(&moe_up_kernel<ASYM, 1, 4, 1>, 1);
-    }
-    if (all >= 1024) return up(&moe_up_kernel<ASYM, 2, 2, kChunks>, 4);
-    if (all >= 512) return up(&moe_up_kernel<ASYM, 2, 4, kChunks>, 2);
-    return up(&moe_up_kernel<ASYM, 1, 4, kChunks>, 1);
+    const bool two = tiles * slots >= 512;  // one tile where workgroups would not reach all CUs
+    if (a.tokens <= 16) return two ? up(&moe_up_kernel<ASYM, 2, 1>, 2) : up(&moe_up_kernel<ASYM, 1, 1>, 1);
+    return two ? up(&moe_up_kernel<ASYM, 2, kChunks>, 2) : up(&moe_up_kernel<ASYM, 1, kChunks>, 1);
   };
   asym ? up_fmt(std::true_type{}) : up_fmt(std::false_type{});
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const Down d = down_for(p.tokens, p.hidden);
+  constexpr int kSums = 4 * kDownWaves * 16 * kDownWide;  // bytes for each token
   auto down = [&](auto kernel, std::atomic<uint64_t>& done) {
-    const hipError_t limit = ensure_lds_limit(reinterpret_cast<const void*>(kernel),
-                                              4 * d.waves * AWQ_MOE_MAX_TOKENS * 16 * d.wide, done);
+    const hipError_t limit = ensure_lds_limit(reinterpret_cast<const void*>(kernel), kSums * AWQ_MOE_MAX_TOKENS, done);
     if (limit != hipSuccess) return limit;
-    hipLaunchKernelGGL(kernel, dim3(p.hidden / (kTileN * d.wide), d.splits), dim3(64 * d.waves),
-                       static_cast<size_t>(4) * d.waves * a.tokens * 16 * d.wide, st, a);
+    hipLaunchKernelGGL(kernel, dim3(p.hidden / (kTileN * kDownWide), down_splits(p.hidden)), dim3(64 * kDownWaves),
+                       static_cast<size_t>(kSums) * a.tokens, st, a);
     return hipGetLastError();
   };
   static std::atomic<uint64_t> done[4];
-  if (a.tokens <= 16)
-    return asym ? down(&moe_down_kernel<true, 1, 16, 1, 2, 1>, done[0])
-                : down(&moe_down_kernel<false, 1, 16, 1, 2, 1>, done[1]);
-  return asym ? down(&moe_down_kernel<true, 2, 8, kChunks, 4, 2>, done[2])
-              : down(&moe_down_kernel<false, 2, 8, kChunks, 4, 2>, done[3]);
+  if (a.tokens <= 16) return asym ? down(&moe_down_kernel<true, 1>, done[0]) : down(&moe_down_kernel<false, 1>, done[1]);
+  return asym ? down(&moe_down_kernel<true, kChunks>, done[2]) : down(&moe_down_kernel<false, kChunks>, done[3]);
 }
 
 }  // namespace awq
