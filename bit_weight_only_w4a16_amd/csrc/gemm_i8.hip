@@ -3,9 +3,10 @@
 // The sums are whole numbers below 2^31 (K <= 131056), so neither their order nor a split of K
 // changes a result; float32 begins at the scales.
 //
-// Workgroups of eight wavefronts own 16 columns and up to 64 rows, the wavefronts taking units
-// of 64 channels in turn; operands go from memory straight into the matrix instruction's
-// registers, and the wavefronts' sums meet in LDS.
+// Few rows: workgroups of eight wavefronts own 16 columns and up to 64 rows, the wavefronts taking
+// units of 64 channels in turn; operands go from memory straight into the matrix instruction's
+// registers, and the wavefronts' sums meet in LDS. Bound by memory: 4096 -> 14336 of one row 10.8 us
+// (5.4 TB/s), 4096 -> 4096 4.6. More rows: tiles (below).
 #include "ffn_internal.hpp"
 
 #include <math.h>
@@ -117,7 +118,8 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // steps, of which all but one are on their way or have landed ahead of use. The only barrier of a step
 // stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
-// runs of four outputs of one row.
+// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 137-141 us (1.7 POPS): the
+// way from L2 into LDS takes 117 of it by itself, products 78.
 
 typedef int int16_t_ __attribute__((ext_vector_type(16)));
 

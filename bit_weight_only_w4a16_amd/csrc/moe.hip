@@ -7,14 +7,16 @@
 // known on the device alone, so the first launch has workgroups for as many experts as the
 // ids could name (those past the last named one end at once), and each finds its expert as the
 // n-th set bit of the bits that the ids set. One workgroup of that launch writes the plan of the
-// second: the named experts and their tokens in order. There a workgroup owns 16 outputs of all
-// tokens and walks over the named experts' rows, its wavefronts taking equal runs of units, so
+// second: the named experts and their tokens in order. There a workgroup owns 32 outputs of all
+// tokens and walks over the named experts, its wavefronts taking equal shares of their units, so
 // that its load does not depend on how many experts there are; with few outputs, several
 // workgroups share them, and the one that ends last adds their sums.
 //
-// Weights go from memory to registers, 1 KiB per load (awq_repack's units), several units ahead of
-// their use; they are dequantized exactly to binary16 and meet up to 16 tokens' rows in one matrix
-// instruction. Every sum has its place and order: results do not vary.
+// Weights go from memory to registers, 1 KiB per load (awq_repack's units), ahead of their use; they
+// are dequantized exactly to binary16 and meet up to 16 tokens' rows in one matrix instruction. Every
+// sum has its place and order: results do not vary. Measured: one token through two of eight experts
+// of 4096 x 14336 44.5 us (183 MB, 4.1 TB/s), 48 tokens over 64 experts of 4096 x 1536 138 us (628 MB,
+// 4.5 TB/s); beside memory, dequantization issues vector instructions 30 to 50 % of the time.
 #include "ffn_internal.hpp"
 
 #include <type_traits>
