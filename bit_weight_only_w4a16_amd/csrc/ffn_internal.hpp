@@ -32,11 +32,13 @@ inline I8Layout make_i8_layout(int64_t N, int64_t K) {
   return l;
 }
 
-// Rows whose largest value is not above this count as zeros: 127 / max stays finite.
+// Rows whose largest value is not above this count as zeros: their scales' reciprocals stay finite.
 constexpr float kLeastMax = 1e-30f;
 
-// The scale of an 8-bit row and the factor that makes its codes, from the largest bit pattern of
-// the values' magnitudes (patterns of infinities and NaN lie above those of finite values).
+// The scale of an 8-bit row and its reciprocal, from the largest bit pattern of the values'
+// magnitudes (patterns of infinities and NaN lie above those of finite values). The scale is the product
+// with 1 / 127, two roundings where a division has one: so does PyTorch divide by a constant on this
+// device, and codes at halves come out as there.
 struct RowScale {
   float scale, inv;
 };
@@ -44,17 +46,22 @@ __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   const float most = __builtin_bit_cast(float, top);
   if (top >= 0x7F800000u) return {__builtin_nanf(""), 0.0f};
   if (!(most > kLeastMax)) return {0.0f, 0.0f};
-  return {most / 127.0f, 127.0f / most};
+  const float scale = most * (1.0f / 127.0f);
+  return {scale, 1.0f / scale};
 }
-// rint(v * inv), at most 127 in magnitude; 0 where inv is 0, whatever v is
-__device__ __forceinline__ int to_code(float v, float inv) {
-  if (inv == 0.0f) return 0;
-  return static_cast<int>(fminf(fmaxf(__builtin_rintf(v * inv), -127.0f), 127.0f));
+// rint(v / scale), at most 127 in magnitude; 0 where inv is 0, whatever v is. The product with inv is
+// put right by what it leaves of v: products of short fractions are halves more often than chance has
+// it, and there the product alone may fall on either side.
+__device__ __forceinline__ int to_code(float v, const RowScale& s) {
+  if (s.inv == 0.0f) return 0;
+  const float t = v * s.inv;
+  const float q = __builtin_rintf(__builtin_fmaf(__builtin_fmaf(-t, s.scale, v), s.inv, t));
+  return static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
 }
-__device__ __forceinline__ uint32_t pack_codes(const float* v, float inv) {
+__device__ __forceinline__ uint32_t pack_codes(const float* v, const RowScale& s) {
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= (static_cast<uint32_t>(to_code(v[i], inv)) & 0xFFu) << (8 * i);
+  for (int i = 0; i < 4; ++i) w |= (static_cast<uint32_t>(to_code(v[i], s)) & 0xFFu) << (8 * i);
   return w;
 }
 __device__ __forceinline__ uint32_t magnitude(float v) { return __builtin_bit_cast(uint32_t, v) & 0x7FFFFFFFu; }

@@ -7,7 +7,7 @@
 // A row is read once and stays in registers; its sum of squares, and for 8-bit rows max|v| after
 // it, come from reductions over the row's threads, and every output is written from there. Memory
 // is the only bound of long inputs: 16384 x 8192 bfloat16 with a residual 186 us (5.8 TB/s), 2048 x 14336
-// to 8 bits 20 us (4.4 TB/s); one row of 4096 2.9 us, a launch, a trip to memory and a reduction.
+// to 8 bits 21 us (4.2 TB/s); one row of 4096 2.9 us, a launch, a trip to memory and a reduction.
 #include "ffn_internal.hpp"
 
 namespace awq {
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(Row
       if (NORM && a.y != nullptr) *reinterpret_cast<uint4*>(a.y + row * a.y_stride + at) = narrow<T>(v);
       if (a.q != nullptr)
         *reinterpret_cast<uint2*>(a.q + row * a.q_stride + at) =
-            make_uint2(pack_codes(v, s.inv), pack_codes(v + 4, s.inv));
+            make_uint2(pack_codes(v, s), pack_codes(v + 4, s));
     }
   }
 }
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256)
     value(16 * c, v);
     value(16 * c + 8, v + 8);
     *reinterpret_cast<uint4*>(codes + (tile * units + c / 4) * 1024 + 16 * (16 * (c % 4) + r)) = make_uint4(
-        pack_codes(v, s.inv), pack_codes(v + 4, s.inv), pack_codes(v + 8, s.inv), pack_codes(v + 12, s.inv));
+        pack_codes(v, s), pack_codes(v + 4, s), pack_codes(v + 8, s), pack_codes(v + 12, s));
   }
 }
 

@@ -77,6 +77,44 @@ def test_quant(dtype, width):
 
 
 @TYPES
+def test_quant_at_halves(dtype):
+    """Values that lie halfway between two codes: the quotient by the scale decides, to even where the
+    scale is exact."""
+    for top in (127.0, 254.0, 63.5):   # scales 1, 2 and 1/2, as float32's product with 1 / 127 gives them
+        x = torch.zeros(2, 256, dtype=dtype)
+        x[:, 0] = top
+        step = torch.tensor(top) * (torch.tensor(1.0) / 127.0)
+        x[0, 1:128] = (torch.arange(127) + 0.5).to(dtype) * (top / 127)
+        x[1, 1:128] = -x[0, 1:128]
+        q, s = int8.awq_quant_i8(x.to(DEV))
+        assert bool((s.cpu() == step).all())
+        want = torch.round(x.float() / step).clamp(-127, 127)
+        assert torch.equal(q.cpu().float(), want)
+
+
+@TYPES
+def test_quant_of_short_fractions(dtype):
+    """Values of few bits: every code is the float32 quotient by the stored scale, rounded."""
+    gen = torch.Generator().manual_seed(5)
+    x = (torch.randint(-96, 97, (300, 520), generator=gen) * 2.0 ** torch.randint(-6, 3, (300, 1), generator=gen)).to(dtype)
+    q, s = int8.awq_quant_i8(x.to(DEV))
+    want = torch.round(x.float() / s.cpu()[:, None]).clamp(-127, 127)
+    assert torch.equal(q.cpu().float(), want)
+
+
+def test_rms_norm_refuses():
+    x = randn(2, 64, seed=1)
+    for bad, kind in ((dict(y16=False), ValueError), (dict(h=x), ValueError), (dict(weight=x[0].float()), TypeError),
+                      (dict(weight=x), ValueError), (dict(residual=x[:1]), ValueError), (dict(eps=0.0), awq.AwqError),
+                      (dict(q=torch.empty(2, 64, dtype=torch.uint8, device=DEV)), TypeError),
+                      (dict(y=torch.empty(64, 2, dtype=F16, device=DEV).t()), ValueError)):
+        with pytest.raises(kind):
+            int8.awq_rms_norm(x, **bad)
+    with pytest.raises(awq.AwqError):
+        int8.awq_rms_norm(randn(2, 60, seed=1))
+
+
+@TYPES
 def test_rows_with_strides_and_in_place(dtype):
     width = 2064
     wide = randn(7, 3 * width + 24, seed=5, dtype=dtype)
