@@ -114,9 +114,10 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 //
 // Four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of 64 channels; with
 // TEAMS = 2 a workgroup has two such teams, which take turns with the steps and add up their sums
-// at the end (few tiles leave a SIMD one wavefront, whose every step waits for LDS and the barrier). Operands go from memory straight into LDS, into a ring of three or four
-// steps, of which all but one are on their way or have landed ahead of use. The only barrier of a step
-// stands before its second half, whose operands are in registers already.
+// at the end (few tiles leave a SIMD one wavefront, whose every step waits for LDS and the barrier).
+// Operands go from memory straight into LDS, into a ring of three or four steps, of which all but one
+// are on their way or have landed ahead of use. The only barrier of a step stands before its second
+// half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
 // runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 137-141 us (1.7 POPS): the
 // way from L2 into LDS takes 117 of it by itself, products 78.

@@ -22,7 +22,8 @@ constexpr int kSliceWaves = 4, kRouteAhead = 2;
 
 // Slices of the channels, one per workgroup of four wavefronts, so that about four workgroups per
 // CU run; a wavefront has at least 32 channels. (One workgroup per CU left each float64
-// instruction waiting for its operands: 517 tokens x 128 experts x 4096 31 us instead of 19; independent float64 matrix instructions alone would take 12.)
+// instruction waiting for its operands: 517 tokens x 128 experts x 4096 31 us instead of 19;
+// independent float64 matrix instructions alone would take 12.)
 int route_wide(int64_t tokens) { return tokens > 16 ? 2 : 1; }  // tiles of 16 tokens for a wavefront
 int route_slices(int64_t tokens, int hidden, int experts) {
   const int rows = 16 * route_wide(tokens);
