@@ -115,12 +115,13 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // Four wavefronts own BM x BN outputs, a wavefront a quarter of them, in steps of 64 channels; with
 // TEAMS = 2 a workgroup has two such teams, which take turns with the steps and add up their sums
 // at the end (few tiles leave a SIMD one wavefront, whose every step waits for LDS and the barrier).
-// Operands go from memory straight into LDS, into a ring of three or four steps, of which all but one
-// are on their way or have landed ahead of use. The only barrier of a step stands before its second
-// half, whose operands are in registers already.
+// Operands go from memory straight into LDS, W's into a ring of three or four steps, the rows' into one
+// of two or three pairs of steps: a pair is a whole line of 128 bytes of each row (steps of 64 bytes by
+// themselves: 142 us instead of 134 at 2048 x 14336 x 4096, 81 instead of 68 at 1000 x 11000 x 4080).
+// The only barrier of a step stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
-// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 137-141 us (1.7 POPS): the
-// way from L2 into LDS takes 117 of it by itself, products 78.
+// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 133-135 us (1.8 POPS), of
+// which the products alone take 78.
 
 typedef int int16_t_ __attribute__((ext_vector_type(16)));
 
@@ -157,31 +158,20 @@ __device__ __forceinline__ uint4 tail8(const I8Args& a, float8_t v, uint4 f, uin
 }
 
 constexpr int kStep = 64;  // channels of a step
-// Steps in LDS. Three steps of 128 x 256 outputs leave room for two workgroups on a CU, one of
+// W's steps in LDS. Three steps of 128 x 256 outputs leave room for two workgroups on a CU, one of
 // which multiplies while the other stores (four steps: 149 us instead of 135 at 2048 x 14336 x
 // 4096; tiles of 256 x 256, which have a CU to themselves: 155). Smaller tiles have less to do in a
-// step and take four (64 x 128 at 333 x 4096 x 11008: 41 us with three, 32 with four, 33 with six).
+// step and take four (64 x 128 at 333 x 4096 x 11008: 41 us with three, 32 with four, 33 with six),
+// and three of the rows' pairs (there 38 us with two, 32 with three).
 constexpr int ring(int bm, int bn) { return bm * bn > 16384 ? 3 : 4; }
-
-// Waits until at most `ahead` <= MOST steps of PIECES loads each are on their way.
-template <int MOST, int PIECES>
-__device__ __forceinline__ void wait_steps(int ahead) {
-  if constexpr (MOST == 0) {
-    wait_loads<0>();
-  } else {
-    if (ahead >= MOST) {
-      wait_loads<MOST * PIECES>();
-    } else {
-      wait_steps<MOST - 1, PIECES>(ahead);
-    }
-  }
-}
+constexpr int pairs(int bm, int bn) { return bm * bn > 16384 ? 2 : 3; }
+constexpr int stages(int bm, int bn) { return ring(bm, bn) * bn * kStep + pairs(bm, bn) * 2 * bm * kStep; }
 
 template <typename T, int BM, int BN, int TEAMS, bool SPLIT>
 __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   constexpr int TM = BM / 2, TN = BN / 2, FM = TM / 32, FN = TN / 32;
-  constexpr int STAGE = (BM + BN) * kStep, RING = ring(BM, BN);
-  constexpr int PIECES_A = BM / 64, PIECES_W = BN / 64, PIECES = PIECES_A + PIECES_W;  // a wavefront's loads of a step
+  constexpr int RING = ring(BM, BN), PAIRS = pairs(BM, BN), STAGE_W = BN * kStep, PAIR = 2 * BM * kStep;
+  constexpr int PIECES_Q = BM / 32, PIECES_W = BN / 64;  // a wavefront's loads of a pair of steps, and of one
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
   const int number = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wave = number & 3, team = number >> 2;
@@ -199,7 +189,7 @@ __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   const u32x4 rq = rsrc_words(a.q + m0 * a.q_stride, (rows - 1) * stride + a.K);
   const int tiles = static_cast<int>((a.N + 15) / 16);
   const u32x4 rw = rsrc_words(a.codes, static_cast<uint32_t>(tiles) * a.units * 1024u);
-  const unsigned char* mine_lds = lds + team * RING * STAGE;
+  const unsigned char* mine_lds = lds + team * stages(BM, BN);  // W's steps, then the rows' pairs of steps
   const uint32_t base = lds_offset(mine_lds);
 
   // units of this workgroup's share of the channels; a team's last step may lie past them (zeros)
@@ -209,32 +199,36 @@ __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
     end = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.y + 1) / gridDim.y);
   }
   const int steps = (end - first + TEAMS - 1) / TEAMS;
+  first += team * steps;
 
-  // 64 bytes of a row in LDS, their 16-byte pieces exchanged by the row's number (p ^ row / 2 % 4),
-  // so that eight rows' equal pieces lie in different banks; the exchange is made where a lane loads
-  const uint32_t lane_q = (lane >> 2) * stride + 16u * ((lane & 3) ^ ((lane >> 3) & 3));
-  auto issue_piece = [&](int slot, int step, int i) {  // 1 KiB each: 16 rows, or a unit of W
-    const uint32_t dst = base + slot * STAGE;
-    const int unit = first + TEAMS * step + team;
-    if (i < PIECES_A) {
-      const uint32_t piece = wave * PIECES_A + i;
-      load_to_lds(rq, lane_q + piece * 16u * stride + static_cast<uint32_t>(unit) * kStep, dst + piece * 1024u);
-      return;
-    }
-    const int piece = wave * PIECES_W + i - PIECES_A, t = n0 / 16 + piece;
-    const uint32_t at = t < tiles && (TEAMS == 1 || unit < end) ? (static_cast<uint32_t>(t) * a.units + unit) * 1024u : kNoLoad;
-    load_to_lds(rw, at + 16u * lane, dst + BM * kStep + piece * 1024u);
+  // Rows are read two steps at a time, whole lines of 128 bytes; in LDS a line's 16-byte pieces are
+  // exchanged by the row's number (p ^ row / 2 % 8), so that sixteen rows' equal pieces lie in
+  // different banks; the exchange is made where a lane loads.
+  const uint32_t lane_row = (lane >> 3) * stride, lane_col = 16u * ((lane & 7) ^ (lane >> 4));
+  auto issue_rows = [&](int slot, int pair, int i) {  // 1 KiB: eight rows
+    const uint32_t piece = wave * PIECES_Q + i;
+    const uint32_t at = lane_row + piece * 8u * stride + static_cast<uint32_t>(first + 2 * pair) * kStep;
+    load_to_lds(rq, 2 * pair < steps ? at + (lane_col ^ 64u * (i & 1)) : kNoLoad,
+                base + RING * STAGE_W + slot * PAIR + piece * 1024u);
+  };
+  auto issue_w = [&](int slot, int step, int i) {  // 1 KiB: a unit
+    const int piece = wave * PIECES_W + i, t = n0 / 16 + piece, unit = first + step;
+    const uint32_t at = t < tiles && step < steps && (TEAMS == 1 || unit < end)
+                            ? (static_cast<uint32_t>(t) * a.units + unit) * 1024u + 16u * lane
+                            : kNoLoad;
+    load_to_lds(rw, at, base + slot * STAGE_W + piece * 1024u);
   };
   // operands of half s of a step, in the order of their use: W's, then the rows'
   int4_t fq[2][FM], fw[2][FN];
-  auto read_one = [&](int slot, int s, int i) {
-    const unsigned char* stage = mine_lds + slot * STAGE;
+  auto read_one = [&](int step, int s, int i) {  // step: its number modulo UNROLL
     if (i < FN) {
-      const unsigned char* w = stage + BM * kStep + (wn * TN / 16 + (l32 >> 4)) * 1024 + 16 * ((lane & 15) + 16 * (2 * s + half));
+      const unsigned char* w = mine_lds + step % RING * STAGE_W + (wn * TN / 16 + (l32 >> 4)) * 1024 +
+                               16 * ((lane & 15) + 16 * (2 * s + half));
       fw[s][i] = *reinterpret_cast<const int4_t*>(w + i * 2048);
     } else {
-      const unsigned char* q = stage + (wm * TM + l32) * kStep + 16 * ((2 * s + half) ^ ((lane >> 1) & 3));
-      fq[s][i - FN] = *reinterpret_cast<const int4_t*>(q + (i - FN) * 32 * kStep);
+      const unsigned char* q = mine_lds + RING * STAGE_W + step / 2 % PAIRS * PAIR + (wm * TM + l32) * 2 * kStep +
+                               16 * ((4 * (step % 2) + 2 * s + half) ^ ((lane >> 1) & 7));
+      fq[s][i - FN] = *reinterpret_cast<const int4_t*>(q + (i - FN) * 64 * kStep);
     }
   };
   int16_t_ acc[FM][FN];
@@ -247,49 +241,68 @@ __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   // A half's products in runs of FN, and between the runs an equal part of the next half's LDS
   // reads and of the loads of a step to come: a wavefront may have its SIMD to itself, and nothing
   // else would fill the matrix cores' pauses. (Left to the compiler, both stand in front.)
-  auto products = [&](int s, bool reads, int read_slot, bool loads, int load_slot, int load_step) {
+  // A step's loads go out in its second half: W's of step + RING, and from an odd step before them the
+  // rows' of the pair that takes its own pair's place, which it was the last to read.
+  auto products = [&](int s, int read_step, bool loads, int n, int step) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
       for (int j = 0; j < FN; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fw[s][j], fq[s][i], acc[i][j], 0, 0, 0);
-      if (reads) {
 #pragma unroll
-        for (int r = (FM + FN) * i / FM; r < (FM + FN) * (i + 1) / FM; ++r) read_one(read_slot, s ^ 1, r);
-      }
+      for (int r = (FM + FN) * i / FM; r < (FM + FN) * (i + 1) / FM; ++r) read_one(read_step, s ^ 1, r);
       if (loads) {
+        const int rows = n % 2 * PIECES_Q, all = rows + PIECES_W;
 #pragma unroll
-        for (int l = PIECES * i / FM; l < PIECES * (i + 1) / FM; ++l) issue_piece(load_slot, load_step, l);
+        for (int l = 0; l < PIECES_Q + PIECES_W; ++l) {
+          if (l < all * i / FM || l >= all * (i + 1) / FM) continue;
+          if (l < rows) {
+            issue_rows(n / 2 % PAIRS, step / 2 + PAIRS, l);
+          } else {
+            issue_w(n % RING, step + RING, l - rows);
+          }
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   };
 
+  // in front of the first step the same loads in the same order; those past the end write zeros
 #pragma unroll
-  for (int i = 0; i < RING; ++i)
-    if (i < steps) {
+  for (int n = 1 - 2 * PAIRS < -RING ? 1 - 2 * PAIRS : -RING; n < 0; ++n) {
+    if (n % 2 != 0 && n >= 1 - 2 * PAIRS) {
 #pragma unroll
-      for (int l = 0; l < PIECES; ++l) issue_piece(i, i, l);
+      for (int l = 0; l < PIECES_Q; ++l) issue_rows((n + 2 * PAIRS) / 2, (n + 2 * PAIRS) / 2, l);
     }
-  // `ahead` steps behind the one that is waited for may be on their way
-  auto wait_step = [&](int ahead) {
-    wait_steps<RING - 1, PIECES>(ahead);
-    lds_barrier();
-  };
-  wait_step(min(steps, RING) - 1);
+    if (n >= -RING) {
 #pragma unroll
-  for (int r = 0; r < FM + FN; ++r) read_one(0, 0, r);
-  for (int i0 = 0; i0 < steps; i0 += RING) {
-#pragma unroll
-    for (int n = 0; n < RING; ++n) {  // the steps' places in the ring are constants
-      const int i = i0 + n;
-      if (i >= steps) break;
-      products(0, true, n, false, 0, 0);
-      // this step's operands are read, the next step's have landed
-      wait_step(min(steps - i, RING) - 2);
-      products(1, i + 1 < steps, (n + 1) % RING, i + RING < steps, n, i + RING);
+      for (int l = 0; l < PIECES_W; ++l) issue_w(n + RING, n + RING, l);
     }
   }
+  constexpr int AHEAD = (RING - 2) * PIECES_W;
+  wait_loads<AHEAD + PIECES_W + (PAIRS - 1) * PIECES_Q>();
+  lds_barrier();
+#pragma unroll
+  for (int r = 0; r < FM + FN; ++r) read_one(0, 0, r);
+  constexpr int UNROLL = 12;
+  for (int i0 = 0; i0 < steps; i0 += UNROLL) {
+#pragma unroll
+    for (int n = 0; n < UNROLL; ++n) {  // the steps' places in the rings are constants
+      if (i0 + n >= steps) break;
+      products(0, n, false, 0, 0);
+      // This step's operands are read, and the next step's have landed when no more are on their way
+      // than went out behind them: W's of RING - 2 steps and a pair of the rows'. (With two pairs
+      // the rows' themselves are the last but AHEAD where the next step begins a pair.)
+      if (PAIRS > 2 || n % 2 == 0) {
+        wait_loads<AHEAD + PIECES_Q>();
+      } else {
+        wait_loads<AHEAD>();
+      }
+      lds_barrier();
+      products(1, (n + 1) % UNROLL, true, n, i0 + n);
+    }
+  }
+  wait_loads<0>();  // none may land in what follows
 
   constexpr int PITCH = TN + 4;
   if constexpr (TEAMS > 1) {  // behind the place of the output's transposition
@@ -474,7 +487,7 @@ Choice choose(int64_t M, int64_t N, int64_t K) {
 
 template <typename T, int BM, int BN, int TEAMS>
 hipError_t launch_tiles(const I8Args& a, int splits, hipStream_t st) {
-  constexpr int STAGES = TEAMS * ring(BM, BN) * (BM + BN) * kStep;
+  constexpr int STAGES = TEAMS * stages(BM, BN);
   constexpr int TAIL = 4 * 32 * (BN / 2 + 4) * 4 + (TEAMS > 1 ? BM * BN * 4 : 0), LDS = STAGES > TAIL ? STAGES : TAIL;
   static_assert(LDS <= 163840, "a CU's LDS");
   const unsigned blocks = static_cast<unsigned>((a.M + BM - 1) / BM * ((a.N + BN - 1) / BN));
