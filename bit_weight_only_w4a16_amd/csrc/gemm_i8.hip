@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // themselves: 142 us instead of 134 at 2048 x 14336 x 4096, 81 instead of 68 at 1000 x 11000 x 4080).
 // The only barrier of a step stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
-// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 133-135 us (1.8 POPS), of
+// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 132-135 us (1.8 POPS), of
 // which the products alone take 78.
 
 typedef int int16_t_ __attribute__((ext_vector_type(16)));
@@ -204,19 +204,21 @@ __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   // Rows are read two steps at a time, whole lines of 128 bytes; in LDS a line's 16-byte pieces are
   // exchanged by the row's number (p ^ row / 2 % 8), so that sixteen rows' equal pieces lie in
   // different banks; the exchange is made where a lane loads.
-  const uint32_t lane_row = (lane >> 3) * stride, lane_col = 16u * ((lane & 7) ^ (lane >> 4));
+  // All but a lane's own part of an offset is scalar (333 x 4096 x 11008 32.3 us -> 30.5).
+  const uint32_t lane_col = 16u * ((lane & 7) ^ (lane >> 4));
+  const uint32_t lane_q[2] = {(lane >> 3) * stride + lane_col, (lane >> 3) * stride + (lane_col ^ 64u)};
   auto issue_rows = [&](int slot, int pair, int i) {  // 1 KiB: eight rows
     const uint32_t piece = wave * PIECES_Q + i;
-    const uint32_t at = lane_row + piece * 8u * stride + static_cast<uint32_t>(first + 2 * pair) * kStep;
-    load_to_lds(rq, 2 * pair < steps ? at + (lane_col ^ 64u * (i & 1)) : kNoLoad,
-                base + RING * STAGE_W + slot * PAIR + piece * 1024u);
+    const uint32_t unit = first + 2 * pair;
+    const uint32_t at = 2 * pair < steps ? piece * 8u * stride + unit * kStep : kNoLoad;
+    load_to_lds(rq, at + lane_q[i & 1], base + RING * STAGE_W + slot * PAIR + piece * 1024u);
   };
   auto issue_w = [&](int slot, int step, int i) {  // 1 KiB: a unit
     const int piece = wave * PIECES_W + i, t = n0 / 16 + piece, unit = first + step;
     const uint32_t at = t < tiles && step < steps && (TEAMS == 1 || unit < end)
-                            ? (static_cast<uint32_t>(t) * a.units + unit) * 1024u + 16u * lane
+                            ? (static_cast<uint32_t>(t) * a.units + unit) * 1024u
                             : kNoLoad;
-    load_to_lds(rw, at, base + slot * STAGE_W + piece * 1024u);
+    load_to_lds(rw, at + 16u * lane, base + slot * STAGE_W + piece * 1024u);
   };
   // operands of half s of a step, in the order of their use: W's, then the rows'
   int4_t fq[2][FM], fw[2][FN];
