@@ -433,8 +433,9 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
 
 // Which kernel a product takes: the one with the least time by an estimate in microseconds, whose
 // constants were fitted (by least squares of the logarithms, 10 % rms) to 2400 timings of all
-// kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. On
-// those the choice costs 1.6 % more than the best one on average, 26 % at worst (33 x 8192 x 1024).
+// kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. Over
+// those sizes the choice costs 2.6 % more than the best one on average, 33 % at worst (33 x 8192 x
+// 1024: 6.5 us, 4.9); a fit of its own to the 1765 timings that say so would cost 2.5 %.
 // A CU's blocks share its matrix cores (`work` each and step) and pass their steps not faster than
 // memory answers (`wait`, `fit` of them at a time). Two teams win where 64 x 64 tiles leave CUs to
 // spare (200 x 4096 x 4096: 10.9 us, one team 12.9); with larger tiles they gained 2 % at most.
