@@ -153,38 +153,35 @@ __device__ __forceinline__ half8_t load_half8(const uint16_t* p) {
   return __builtin_bit_cast(half8_t, *reinterpret_cast<const uint4*>(p));
 }
 
-// The plan, by one workgroup. Where an expert's tokens stand among each other depends on the
-// order of the atomics, what is computed for each of them does not.
+// The plan, by one workgroup. An expert's tokens stand in their own order: which of more than 16 CHUNKS
+// are a run decides where their sums are cut. (Their LDS leaves room for four workgroups on a CU.)
 __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, const uint32_t* bits, const Named& named,
                                            int tiles, int most_rows) {
+  static_assert(kMostExperts <= 65536 && kMostPairs <= 65536, "16 bits each");
   __shared__ int before[kMostExperts / 32];
-  __shared__ int who[kMostExperts], begin[kMostExperts], taken[kMostExperts];
+  __shared__ uint16_t who[kMostExperts], begin[kMostExperts];
+  __shared__ unsigned long long tokens[kMostExperts];  // those that name the expert, as bits
   const int lane = threadIdx.x & 63, pairs = a.tokens * a.k;
   if (threadIdx.x < kMostExperts / 32) {
     before[lane] = named.before;
     uint32_t word = named.word;
-    for (int at = named.before; word != 0; ++at, word &= word - 1) who[at] = 32 * lane + __builtin_ctz(word);
+    for (int at = named.before; word != 0; ++at, word &= word - 1)
+      who[at] = static_cast<uint16_t>(32 * lane + __builtin_ctz(word));
   }
-  for (int i = threadIdx.x; i < named.total; i += blockDim.x) taken[i] = 0;
+  for (int i = threadIdx.x; i < named.total; i += blockDim.x) tokens[i] = 0;
   for (int i = threadIdx.x; i < tiles; i += blockDim.x) a.plan.ended[i] = 0;
   __syncthreads();
-  // a pair's expert by its place among the named ones, -1 where an earlier j of the token names it
-  auto place = [&](int i) {
-    const int e = ids[i];
-    if (e < 0) return -1;
-    for (int j = i / a.k * a.k; j < i; ++j)
-      if (ids[j] == e) return -1;
+  // an expert's place among the named ones
+  auto place = [&](int e) {
     return before[e >> 5] + static_cast<int>(__popc(bits[e >> 5] & ((1u << (e & 31)) - 1)));
   };
-  for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int at = place(i);
-    if (at >= 0) atomicAdd(&taken[at], 1);
-  }
+  for (int i = threadIdx.x; i < pairs; i += blockDim.x)
+    if (ids[i] >= 0) atomicOr(&tokens[place(ids[i])], 1ull << (i / a.k));
   __syncthreads();
   if (threadIdx.x < 64) {  // sums over the experts before one: of tokens (low half) and of runs
     int base = 0;
     for (int i0 = 0; i0 < named.total; i0 += 64) {
-      const int rows = i0 + lane < named.total ? taken[i0 + lane] : 0;
+      const int rows = i0 + lane < named.total ? __popcll(tokens[i0 + lane]) : 0;
       const int runs = (rows + most_rows - 1) / most_rows, mine = rows | runs << 16;
       int upto = mine;
 #pragma unroll
@@ -194,7 +191,7 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
       }
       const int from = base + upto - mine;
       if (i0 + lane < named.total) {
-        begin[i0 + lane] = from & 0xFFFF;
+        begin[i0 + lane] = static_cast<uint16_t>(from);
         for (int n = 0; n < runs; ++n) {
           a.plan.experts[(from >> 16) + n] = who[i0 + lane];
           a.plan.first[(from >> 16) + n] = (from & 0xFFFF) + n * most_rows;
@@ -208,15 +205,15 @@ __device__ __forceinline__ void write_plan(const MoeArgs& a, const int* ids, con
     }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < named.total; i += blockDim.x) taken[i] = 0;
-  __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int at = place(i);
-    if (at < 0) continue;
-    const int to = begin[at] + atomicAdd(&taken[at], 1);
+    const int e = ids[i], t = i / a.k;
+    bool again = e < 0;  // an earlier j of the token names the expert
+    for (int j = t * a.k; j < i; ++j) again |= ids[j] == e;
+    if (again) continue;
+    const int at = place(e), to = begin[at] + __popcll(tokens[at] & ((1ull << t) - 1));
     float weight = a.weights[i];
-    for (int j = i + 1; j < (i / a.k + 1) * a.k; ++j)
-      if (ids[j] == ids[i]) weight += a.weights[j];
+    for (int j = i + 1; j < (t + 1) * a.k; ++j)
+      if (ids[j] == e) weight += a.weights[j];
     a.plan.pair[to] = i;
     a.plan.weight[to] = weight;
   }

@@ -1,0 +1,34 @@
+"""The feed-forward operators on the GPU where tests of single kernels' sizes do not reach: loops of
+many steps and units in every variant that the rules choose, runs of one expert, extremes."""
+import pytest
+
+import ffn_ref as ref
+
+torch = pytest.importorskip("torch")
+awq = pytest.importorskip("bit_weight_only_w4a16_amd.awq")
+moe = pytest.importorskip("bit_weight_only_w4a16_amd.moe")
+
+from test_gpu_ffn import DEV, experts4, randn, same  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def test_moe_runs_of_one_expert_give_the_same_bits():
+    """Experts of more than 32 tokens, whose units are cut at different places for their first and their
+    second 32: which token is among which is the ids' alone. Experts 0 and 1 are the same and
+    their shares cancel, so that an output is what the sums' order leaves."""
+    tokens, hidden, ffn, experts = 64, 512, 1408, 4
+    packed, _ = experts4(experts, hidden, ffn, 128, 0, seed=41)
+    for p in packed:
+        p[1] = p[0]
+    x = randn(tokens, hidden, seed=42, gain=4.0)
+    ids = torch.tensor([0, 1, -1, 4], dtype=torch.int32).repeat(tokens, 1)
+    ids[::5, 2] = 2   # a run between, of few tokens
+    ids[1::3, 3] = 3
+    weights = torch.tensor([1e3, -1e3, 0.0, 0.0]).repeat(tokens, 1)
+    ids, weights = ids.to(DEV), weights.to(DEV)
+    first = moe.awq_moe(x, ids, weights, *packed, ffn)
+    assert bool((first != 0).any())   # the sums' roundings show
+    for i in range(40):
+        randn(64, 64, seed=i) @ randn(64, 64, seed=i)   # other work between
+        assert same(first, moe.awq_moe(x, ids, weights, *packed, ffn)), i
