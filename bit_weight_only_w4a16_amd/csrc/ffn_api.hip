@@ -150,6 +150,10 @@ int awq_moe_route(const awq_moe_route_args* a, hipStream_t stream) {
 
 size_t awq_moe_workspace_bytes(int64_t tokens, int32_t hidden, int32_t ffn, int32_t k) {
   if (tokens == 0 || check_moe_sizes(tokens, hidden, ffn, k) != AWQ_OK) return 0;
+  // the limits of a layer that hold for all groups and formats, both ways round
+  if (hidden % 128 != 0 || ffn % 128 != 0 || awq_repacked_bytes(ffn, hidden, 128, AWQ_FMT_SYM8) == 0 ||
+      awq_repacked_bytes(hidden, ffn, 128, AWQ_FMT_SYM8) == 0)
+    return 0;
   return awq::moe_workspace_bytes(tokens, hidden, ffn, k);
 }
 

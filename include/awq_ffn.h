@@ -154,6 +154,7 @@ typedef struct awq_moe_route_args {
   int32_t reserved;
 } awq_moe_route_args;
 
+/* Workspace of an awq_moe_route call; 0 where none is used, and for sizes it would refuse. */
 size_t awq_moe_route_workspace_bytes(int64_t tokens, int32_t hidden, int32_t experts);
 
 /* Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, HIP. tokens == 0 launches nothing. */
@@ -198,6 +199,7 @@ typedef struct awq_moe_args {
   int32_t reserved;
 } awq_moe_args;
 
+/* Workspace of an awq_moe call; 0 for sizes it would refuse. */
 size_t awq_moe_workspace_bytes(int64_t tokens, int32_t hidden, int32_t ffn, int32_t k);
 
 /* Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, HIP. tokens == 0 launches nothing. */
