@@ -106,13 +106,13 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(Row
         hide_all();
         return row_reduce<THREADS>(sum, sums, [](float a, float b) { return a + b; });
       };
-      float sum = squares(), eps = a.eps;
-      if (sum == __builtin_inff()) {
+      const float width = static_cast<float>(a.width);
+      float mean = squares() / width + a.eps;
+      if (mean == __builtin_inff()) {
         down = kDown;
-        eps *= kDown * kDown;
-        sum = squares();
+        mean = squares() / width + a.eps * kDown * kDown;  // 2^-152 itself is no float32
       }
-      r = 1.0f / sqrtf(sum / static_cast<float>(a.width) + eps);
+      r = 1.0f / sqrtf(mean);
     }
     auto values = [&](int i, float* v) {
       float f[8];

@@ -6,9 +6,10 @@ import ffn_ref as ref
 
 torch = pytest.importorskip("torch")
 awq = pytest.importorskip("bit_weight_only_w4a16_amd.awq")
+int8 = pytest.importorskip("bit_weight_only_w4a16_amd.int8")
 moe = pytest.importorskip("bit_weight_only_w4a16_amd.moe")
 
-from test_gpu_ffn import DEV, experts4, randn, same  # noqa: E402
+from test_gpu_ffn import BF16, DEV, experts4, randn, same  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +33,16 @@ def test_moe_runs_of_one_expert_give_the_same_bits():
     for i in range(40):
         randn(64, 64, seed=i) @ randn(64, 64, seed=i)   # other work between
         assert same(first, moe.awq_moe(x, ids, weights, *packed, ffn)), i
+
+
+@pytest.mark.parametrize("width", [8, 4096])
+@pytest.mark.parametrize("eps", [1e30, 1e36, 3e38, 3.4e38])
+def test_rms_norm_large_eps_beside_squares_past_float32(eps, width):
+    """Rows whose squares' sum passes float32 are summed scaled down, and eps counts as much as it does
+    in other rows; the mean and eps may each be in range and their sum not."""
+    x = randn(4, width, seed=51, dtype=BF16) * torch.tensor([[59], [61], [62], [90]], device=DEV).exp2().to(BF16)
+    w = randn(width, seed=52, dtype=BF16)
+    _, v, off = ref.norm(x, w, eps)
+    got = int8.awq_rms_norm(x, w, eps, i8=True)
+    ref.check(got.y, v, off + ref.U[BF16] * v.abs() + ref.TINY[BF16])
+    ref.check_rows8(got.q, got.scale, v, off)
