@@ -66,10 +66,12 @@ class MoeLayer:
     """Experts with their router: y = residual + sum of the k best experts' outputs."""
 
     def __init__(self, router, gate, up, down, ffn, k, group=awq.GROUP, fmt=awq.FMT_ASYM, *, bias=None,
-                 score="softmax", act="silu", inv_in=None, inv_down=None):
+                 score="softmax", renormalize=True, scale=1.0, act="silu", inv_in=None, inv_down=None):
+        """bias, score, renormalize and scale are awq_moe_route's, the others awq_moe's."""
         self.router, self.gate, self.up, self.down = router, gate, up, down
         self.ffn, self.k, self.group, self.fmt = ffn, k, group, fmt
-        self.bias, self.score, self.act, self.inv_in, self.inv_down = bias, score, act, inv_in, inv_down
+        self.bias, self.score, self.renormalize, self.scale = bias, score, renormalize, scale
+        self.act, self.inv_in, self.inv_down = act, inv_in, inv_down
 
     @classmethod
     def from_weights(cls, router, gate, up, down, k, group=awq.GROUP, fmt=awq.FMT_ASYM, **kw):
@@ -82,7 +84,8 @@ class MoeLayer:
 
     def __call__(self, x, residual=None):
         """x fp16 [tokens, hidden]; more tokens than one call takes go in several."""
-        ids, weights = awq_moe_route(x, self.router, self.k, self.bias, score=self.score)
+        ids, weights = awq_moe_route(x, self.router, self.k, self.bias, score=self.score,
+                                     renormalize=self.renormalize, scale=self.scale)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         for at in range(0, x.shape[0], MAX_TOKENS):
             part = slice(at, at + MAX_TOKENS)

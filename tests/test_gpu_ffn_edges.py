@@ -46,3 +46,20 @@ def test_rms_norm_large_eps_beside_squares_past_float32(eps, width):
     got = int8.awq_rms_norm(x, w, eps, i8=True)
     ref.check(got.y, v, off + ref.U[BF16] * v.abs() + ref.TINY[BF16])
     ref.check_rows8(got.q, got.scale, v, off)
+
+
+def moe_weights(hidden=128, ffn=256, experts=4):
+    return [randn(experts, *shape, seed=91 + i, gain=0.1)
+            for i, shape in enumerate([(hidden,), (ffn, hidden), (ffn, hidden), (hidden, ffn)])]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize,scale", [(True, 1.0), (False, 1.0), (False, 2.5), (True, 0.5)])
+def test_moe_layer_reaches_the_routers_forms(score, renormalize, scale):
+    layer = moe.MoeLayer.from_weights(*moe_weights(), 2, score=score, renormalize=renormalize, scale=scale)
+    x, r = randn(70, 128, seed=95), randn(70, 128, seed=96)
+    ids, weights = moe.awq_moe_route(x, layer.router, 2, score=score, renormalize=renormalize, scale=scale)
+    y = layer(x, r)
+    for part in (slice(0, 64), slice(64, 70)):
+        assert same(y[part], moe.awq_moe(x[part], ids[part], weights[part], layer.gate, layer.up, layer.down, 256,
+                                         residual=r[part]))
