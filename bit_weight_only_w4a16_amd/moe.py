@@ -74,13 +74,18 @@ class MoeLayer:
         self.act, self.inv_in, self.inv_down = act, inv_in, inv_down
 
     @classmethod
-    def from_weights(cls, router, gate, up, down, k, group=awq.GROUP, fmt=awq.FMT_ASYM, **kw):
+    def from_weights(cls, router, gate, up, down, k, group=awq.GROUP, fmt=awq.FMT_ASYM, *, s_in=None, s_down=None, **kw):
         """router fp16 [experts, hidden]; gate and up fp16 [experts, ffn, hidden], down fp16
-        [experts, hidden, ffn], quantized and packed here."""
-        def stack(w):
+        [experts, hidden, ffn], quantized and packed here. s_in ([experts, hidden] or [hidden]) and
+        s_down ([experts, ffn] or [ffn]) are channel scales folded into gate and up, and into down;
+        their inverses (awq.awq_channel_scale forms both) go with them as inv_in and inv_down.
+        inv_in or inv_down without its scale belongs to weights that carry the scale already."""
+        def stack(w, s):
             n, kk = w.shape[1:]
-            return torch.stack([awq.awq_repack(*awq.awq_pack(e, None, group, fmt), n, kk, group, fmt) for e in w])
-        return cls(router, stack(gate), stack(up), stack(down), gate.shape[1], k, group, fmt, **kw)
+            scales = [None if s is None else s if s.dim() == 1 else s[e] for e in range(w.shape[0])]
+            return torch.stack([awq.awq_repack(*awq.awq_pack(e, s_c, group, fmt), n, kk, group, fmt)
+                                for e, s_c in zip(w, scales)])
+        return cls(router, stack(gate, s_in), stack(up, s_in), stack(down, s_down), gate.shape[1], k, group, fmt, **kw)
 
     def __call__(self, x, residual=None):
         """x fp16 [tokens, hidden]; more tokens than one call takes go in several."""

@@ -63,3 +63,28 @@ def test_moe_layer_reaches_the_routers_forms(score, renormalize, scale):
     for part in (slice(0, 64), slice(64, 70)):
         assert same(y[part], moe.awq_moe(x[part], ids[part], weights[part], layer.gate, layer.up, layer.down, 256,
                                          residual=r[part]))
+
+
+@pytest.mark.parametrize("each", [False, True], ids=["one scale", "a scale for each expert"])
+def test_moe_layer_folds_channel_scales(each):
+    """The scales that x and the intermediate are divided by are in the weights: stacks packed by hand
+    have the same bits, and the layer is the product of what they stand for."""
+    router, gate, up, down = moe_weights(hidden=256)
+    scale = lambda width, at: awq.awq_channel_scale(  # noqa: E731
+        randn(32, width, seed=at) * (1.0 + 7.0 * (torch.arange(width, device=DEV) % 16 == 3)).half())
+    pairs = [[scale(width, 10 * at + e) for e in range(4)] for at, width in enumerate((256, 256))]
+    (s_in, inv_in), (s_down, inv_down) = (
+        [torch.stack(t) for t in zip(*p)] if each else list(p[0]) for p in pairs)
+    layer = moe.MoeLayer.from_weights(router, gate, up, down, 2, s_in=s_in, s_down=s_down, inv_in=inv_in,
+                                      inv_down=inv_down)
+    assert layer.inv_in is inv_in and layer.inv_down is inv_down
+    for packed, w, s in ((layer.gate, gate, s_in), (layer.up, up, s_in), (layer.down, down, s_down)):
+        for e in range(4):
+            hand = awq.awq_repack(*awq.awq_pack(w[e], s[e] if each else s), *w.shape[1:])
+            assert same(packed[e], hand)
+    x = randn(9, 256, seed=97)
+    ids, weights = moe.awq_moe_route(x, router, 2)
+    dense = [torch.stack([awq.awq_dequant(p, None, None, awq.LAYOUT_GFX950, *w.shape[1:]) for p in packed])
+             for packed, w in ((layer.gate, gate), (layer.up, up), (layer.down, down))]
+    want, bound = ref.moe(x, ids, weights, *dense, inv_in=inv_in, inv_down=inv_down)
+    ref.check(layer(x), want, bound)
