@@ -9,7 +9,7 @@ awq = pytest.importorskip("bit_weight_only_w4a16_amd.awq")
 int8 = pytest.importorskip("bit_weight_only_w4a16_amd.int8")
 moe = pytest.importorskip("bit_weight_only_w4a16_amd.moe")
 
-from test_gpu_ffn import BF16, DEV, experts4, randn, same  # noqa: E402
+from test_gpu_ffn import BF16, DEV, TYPES, experts4, randn, same  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +88,85 @@ def test_moe_layer_folds_channel_scales(each):
              for packed, w in ((layer.gate, gate), (layer.up, up), (layer.down, down))]
     want, bound = ref.moe(x, ids, weights, *dense, inv_in=inv_in, inv_down=inv_down)
     ref.check(layer(x), want, bound)
+
+
+# ------------------------------------------------------------ tiles of the 8-bit product
+
+# a product for each kernel of tiles that the rule chooses, alone and with the channels split
+# (test_ffn_choice.py holds that it is so): more steps than the loop has in a turn, not a multiple of
+# them, ragged in every direction
+TILES = {  # (tile, teams, split): M, N, K
+    ("64x64", 1, False): (639, 3248, 1776), ("64x64", 1, True): (66, 2296, 2864),
+    ("64x64", 2, False): (193, 1048, 3152), ("64x64", 2, True): (68, 1632, 12512),
+    ("64x128", 1, False): (69, 8424, 1696), ("64x128", 1, True): (65, 2728, 7456),
+    ("128x128", 1, False): (134, 11336, 1568), ("128x128", 1, True): (65, 8792, 4752),
+    ("128x256", 1, False): (279, 13160, 1616), ("128x256", 1, True): (69, 11024, 11440),
+}
+EACH_TILE = pytest.mark.parametrize("kind", TILES, ids=lambda k: f"{k[0]}_{k[1]}_{'split' if k[2] else 'whole'}")
+
+
+def codes(*shape, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randint(-127, 128, shape, generator=g, device=DEV, dtype=torch.int8)
+
+
+def layer_of(w, s_w):
+    """w int8 [N, K] and s_w [N] in the layout of awq_pack_i8."""
+    n, k = w.shape
+    rows, cols = -(-n // 16) * 16, -(-k // 64) * 64
+    full = torch.zeros(rows, cols, dtype=torch.int8, device=DEV)
+    full[:n, :k] = w
+    units = full.view(rows // 16, 16, cols // 64, 4, 16).permute(0, 2, 3, 1, 4).reshape(-1)
+    scales = torch.zeros(rows, device=DEV)
+    scales[:n] = s_w
+    raw = torch.cat([units.view(torch.uint8), scales.view(torch.uint8)])
+    return torch.nn.functional.pad(raw, (0, -raw.numel() % 256))
+
+
+def product_of(kind, dtype):
+    m, n, k = TILES[kind]
+    assert (int8.awq_gemm_i8_workspace_bytes(m, n, k) > 0) == kind[2]
+    g = torch.Generator().manual_seed(n)
+    q, w = codes(m, k, seed=m), codes(n, k, seed=k)
+    scale = ((0.5 + torch.rand(m, generator=g)) / 1024).to(DEV)
+    s_w = ((0.5 + torch.rand(n, generator=g)) / (5.0 * k ** 0.5)).to(DEV)
+    operands = dict(bias=randn(n, seed=1, dtype=dtype), mul=randn(m, n, seed=2, dtype=dtype),
+                    residual=randn(m, n, seed=3, dtype=dtype))
+    return (m, n, k), q, scale, w, s_w, layer_of(w, s_w), operands
+
+
+@TYPES
+@EACH_TILE
+def test_gemm_i8_every_output_of_each_tile(kind, dtype):
+    (m, n, k), q, scale, w, s_w, packed, operands = product_of(kind, dtype)
+    sums = torch.mm(q.double(), w.double().t().contiguous())   # whole numbers, exact
+    v = (sums * scale.double()[:, None] * s_w.double()).cpu()
+    for act, names in (("none", ()), ("gelu", ("bias", "mul", "residual")), ("silu", ("mul",)), ("relu", ("bias",)),
+                       ("gelu_tanh", ("residual",))):
+        some = {name: operands[name] for name in names}
+        y = int8.awq_gemm_i8(q, scale, packed, n, k, act=act, dtype=dtype, **some)
+        want, bound = ref.tail(v, dtype, act, some.get("bias"), some.get("mul"), some.get("residual"), 4 * ref.E * v.abs())
+        ref.check(y, want, bound, f"{m}x{n}x{k} {act}")
+
+
+@TYPES
+@EACH_TILE
+def test_gemm_i8_strides_in_place_and_neighbours_of_each_tile(kind, dtype):
+    (m, n, k), q, scale, _, _, packed, operands = product_of(kind, dtype)
+    r = operands["mul"]
+    wide = codes(m, k + 80, seed=9)
+    wide[:, 32:32 + k] = q
+    # nothing past the output's end is written, and what lies between the rows of codes is not used
+    buf = torch.full((m * n + 8192,), 7.0, dtype=dtype, device=DEV)
+    want = int8.awq_gemm_i8(q, scale, packed, n, k, bias=operands["bias"], residual=r, dtype=dtype,
+                            y=buf[4096:4096 + m * n].view(m, n)).clone()
+    assert bool((buf[:4096] == 7).all()) and bool((buf[4096 + m * n:] == 7).all())
+    got = int8.awq_gemm_i8(wide[:, 32:32 + k], scale, packed, n, k, bias=operands["bias"], residual=r, dtype=dtype)
+    assert same(got, want)
+    inside = r.clone()
+    int8.awq_gemm_i8(q, scale, packed, n, k, bias=operands["bias"], residual=inside, y=inside, dtype=dtype)
+    assert same(inside, want)
+    gated = int8.awq_gemm_i8(q, scale, packed, n, k, act="silu", mul=r, dtype=dtype)
+    inside = r.clone()
+    int8.awq_gemm_i8(q, scale, packed, n, k, act="silu", mul=inside, y=inside, dtype=dtype)
+    assert same(inside, gated)
