@@ -9,7 +9,7 @@ awq = pytest.importorskip("bit_weight_only_w4a16_amd.awq")
 int8 = pytest.importorskip("bit_weight_only_w4a16_amd.int8")
 moe = pytest.importorskip("bit_weight_only_w4a16_amd.moe")
 
-from test_gpu_ffn import BF16, DEV, TYPES, experts4, randn, same  # noqa: E402
+from test_gpu_ffn import BF16, DEV, F16, TYPES, choices, experts4, randn, same  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,74 @@ def test_gemm_i8_strides_in_place_and_neighbours_of_each_tile(kind, dtype):
     inside = r.clone()
     int8.awq_gemm_i8(q, scale, packed, n, k, act="silu", mul=inside, y=inside, dtype=dtype)
     assert same(inside, gated)
+
+
+# ----------------------------------------------------------------- loops of the experts' launches
+
+def moe_by_expert(x, ids, weights, gate, up, down, act, inv_in=None, inv_down=None, residual=None):
+    """ffn_ref.moe, all tokens of an expert at a time."""
+    u, tiny, big_e = ref.U[F16], ref.TINY[F16], ref.E
+    (tokens, hidden), ffn = x.shape, down.shape[2]
+    y = torch.zeros(tokens, hidden, dtype=torch.float64)
+    err, big = torch.zeros_like(y), torch.zeros_like(y)
+    share = ref.cpu64(weights)
+    for e in range(gate.shape[0]):
+        t, j = torch.nonzero(ids.cpu() == e, as_tuple=True)
+        if not len(t):
+            continue
+        xs = ref.cpu64(x)[t]
+        if inv_in is not None:
+            xs = (xs * ref.cpu64(inv_in if inv_in.dim() == 1 else inv_in[e])).half().double()
+        wg, wu, wd = (ref.cpu64(w[e]).t().contiguous() for w in (gate, up, down))
+        g, v = xs @ wg, xs @ wu
+        dg, dv = ((hidden + 64) * big_e * (xs.abs() @ w.abs()) for w in (wg, wu))
+        a = ref.ACTS[act](g)
+        da = 1.13 * dg + 2e-6 * g.abs()
+        m, dm = a * v, da * v.abs() + (a.abs() + da) * dv
+        if inv_down is not None:
+            f = ref.cpu64(inv_down if inv_down.dim() == 1 else inv_down[e])
+            m, dm = m * f, dm * f.abs()
+        dm = dm + 4 * big_e * m.abs()
+        r = m.half().double()
+        dm = torch.where(dm > 0, dm + 2 * u * m.abs() + 2 * tiny, dm)
+        wt = share[t, j][:, None]
+        terms = r.abs() @ wd.abs()
+        y.index_add_(0, t, wt * (r @ wd))
+        err.index_add_(0, t, wt.abs() * (dm @ wd.abs() + (ffn + 64) * big_e * terms))
+        big.index_add_(0, t, wt.abs() * terms)
+    if residual is not None:
+        y = y + ref.cpu64(residual)
+    return y, err + 64 * big_e * big + (u + 2 * big_e) * y.abs() + tiny
+
+
+# A wavefront of the first launch has a quarter of hidden / 128 units, and two tiles where ffn / 16
+# times the experts that may be named is 512 or more; one of the second has a share of the runs' units
+# (runs times ffn / 128), among 16 wavefronts for each of ceil(256 / (hidden / 32)) workgroups, at most
+# 16. Here they have several, but for the last, and a run's units of one wavefront are several too.
+@pytest.mark.parametrize("tokens,hidden,ffn,experts,k,group,fmt", [
+    (5, 4096, 1408, 6, 2, 128, 0),    # two tiles, 8 units each; 32 wavefronts share 66 units of 6 runs
+    (14, 1408, 1408, 8, 3, 64, 1),    # two tiles, 3 or 2 units; 96 wavefronts, 88 units
+    (64, 1408, 2944, 6, 4, 128, 0),   # 32 rows at a time, experts of more than 32 tokens, two tiles
+    (40, 8192, 640, 7, 2, 128, 1),    # one workgroup for 32 outputs: no sums are shared
+    (3, 8320, 768, 5, 2, 32, 0),      # the same with up to 16 rows, hidden past 256 groups of outputs
+    (20, 2048, 4224, 3, 2, 128, 0),   # 64 wavefronts, 99 units: runs cut anywhere
+    (2, 128, 8448, 3, 2, 128, 0),     # one unit of hidden; 256 wavefronts, 198 units: some have none
+])
+def test_moe_loops(tokens, hidden, ffn, experts, k, group, fmt):
+    packed, dense = experts4(experts, hidden, ffn, group, fmt, seed=tokens + 70)
+    x, (ids, weights) = randn(tokens, hidden, seed=71), choices(tokens, k, experts, seed=72)
+    ids[:, 0] = torch.where((ids == 0).any(1), ids[:, 0], 0)   # expert 0 has all tokens
+    more = dict(inv_in=randn(hidden, seed=73).abs() + 0.25, inv_down=randn(experts, ffn, seed=74).abs() + 0.25,
+                residual=randn(tokens, hidden, seed=75))
+    for act, some in (("silu", {}), ("gelu", more)):
+        y = moe.awq_moe(x, ids, weights, *packed, ffn, group, fmt, act=act, **some)
+        want, bound = moe_by_expert(x, ids, weights, *dense, act=act, **some)
+        ref.check(y, want, bound)
+        assert same(y, moe.awq_moe(x, ids, weights, *packed, ffn, group, fmt, act=act, **some))
+
+
+def test_moe_form_by_expert_is_the_other():
+    packed, dense = experts4(5, 256, 384, 128, 0, seed=81)
+    x, (ids, weights) = randn(9, 256, seed=82), choices(9, 3, 5, seed=83)
+    a, b = ref.moe(x, ids, weights, *dense), moe_by_expert(x, ids, weights, *dense, act="silu")
+    assert bool(((a[0] - b[0]).abs() <= 1e-9).all()) and bool(((a[1] - b[1]).abs() <= 1e-9).all())
