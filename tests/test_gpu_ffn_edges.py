@@ -241,3 +241,21 @@ def test_moe_form_by_expert_is_the_other():
     x, (ids, weights) = randn(9, 256, seed=82), choices(9, 3, 5, seed=83)
     a, b = ref.moe(x, ids, weights, *dense), moe_by_expert(x, ids, weights, *dense, act="silu")
     assert bool(((a[0] - b[0]).abs() <= 1e-9).all()) and bool(((a[1] - b[1]).abs() <= 1e-9).all())
+
+
+def test_moe_token_whose_ids_are_all_outside():
+    """It gets its residual, or zeros, whatever the ids and the weights are."""
+    hidden, ffn, experts = 256, 384, 6
+    packed, _ = experts4(experts, hidden, ffn, 128, 0, seed=61)
+    x, r = randn(5, hidden, seed=62), randn(5, hidden, seed=63)
+    ids, weights = choices(5, 4, experts, seed=64)
+    ids[1] = torch.tensor([6, -5, 2 ** 31 - 1, -2 ** 31], dtype=torch.int32)
+    ids[3] = -1
+    weights[3] = float("nan")
+    y = moe.awq_moe(x, ids, weights, *packed, ffn)
+    for t in (1, 3):
+        assert same(y[t], torch.zeros_like(y[t]))
+    assert bool((y[[0, 2, 4]] != 0).any(1).all())
+    y = moe.awq_moe(x, ids, weights, *packed, ffn, residual=r)
+    for t in (1, 3):
+        assert same(y[t], r[t])
