@@ -11,7 +11,7 @@ pytest.importorskip("torch")
 B = pytest.importorskip("bit_weight_only_w4a16_amd.build")
 pytest.importorskip("bit_weight_only_w4a16_amd.int8")
 
-from test_gpu_ffn_edges import TILES  # noqa: E402
+from test_gpu_ffn_edges import ROWS, TILES  # noqa: E402
 
 pytestmark = pytest.mark.skipif(shutil.which("g++") is None, reason="g++ not available")
 
@@ -31,7 +31,7 @@ int main() {
 
 @pytest.fixture(scope="module")
 def rule(tmp_path_factory):
-    """(the tiles there are, what the rule chooses for TILES in their order)"""
+    """(the tiles there are, what the rule chooses for TILES and then ROWS in their order)"""
     text = open(os.path.join(B.CSRC, "gemm_i8.hip")).read()
     begin, end = text.index("struct Tile {"), text.index("hipError_t launch_tiles(")
     body = text[begin:text.rindex("template <", begin, end)]
@@ -40,7 +40,7 @@ def rule(tmp_path_factory):
     source.write_text("#include <math.h>\n#include <stdint.h>\n#include <stdio.h>\n#include <initializer_list>\n"
                       "constexpr int kI8Unit = 64;\nconst char* tuning_env(const char*) { return nullptr; }\n" + body + MAIN)
     subprocess.run(["g++", "-O2", "-std=c++17", str(source), "-o", str(exe)], check=True)
-    out = subprocess.run([str(exe)], input="\n".join("%d %d %d" % s for s in TILES.values()), capture_output=True,
+    out = subprocess.run([str(exe)], input="\n".join("%d %d %d" % s for s in [*TILES.values(), *ROWS]), capture_output=True,
                          text=True, check=True).stdout
     kinds, chosen = out.split("--\n")
     return kinds.splitlines(), chosen.splitlines()
@@ -60,3 +60,7 @@ def test_sizes_are_ragged_and_longer_than_a_turn_of_the_loop(rule):
     for ((tile, teams, _), (m, n, k)), got in zip(TILES.items(), rule[1]):
         steps = -(-k // 64) // (teams * int(got.split()[-1]))
         assert steps > 12 and m % 32 and n % 64 and k % 64, (tile, m, n, k)
+
+
+def test_few_rows_take_the_kernel_for_them(rule):
+    assert rule[1][len(TILES):] == ["rows"] * len(ROWS)

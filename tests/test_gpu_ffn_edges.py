@@ -259,3 +259,68 @@ def test_moe_token_whose_ids_are_all_outside():
     y = moe.awq_moe(x, ids, weights, *packed, ffn, residual=r)
     for t in (1, 3):
         assert same(y[t], r[t])
+
+
+# --------------------------------------------------------------- loops of the other kernels
+
+# few rows, a workgroup's wavefronts with several turns of units each (one, two and four blocks of 16)
+ROWS = [(5, 520, 7280), (14, 4232, 7280), (29, 4712, 4432), (34, 3240, 4304)]
+
+
+@TYPES
+@pytest.mark.parametrize("m,n,k", ROWS)
+def test_gemm_i8_few_rows_of_many_channels(m, n, k, dtype):
+    assert int8.awq_gemm_i8_workspace_bytes(m, n, k) == 0
+    q, w, g = codes(m, k, seed=m), codes(n, k, seed=k), torch.Generator().manual_seed(n)
+    scale, s_w = ((0.5 + torch.rand(s, generator=g)).to(DEV) / 1024 for s in (m, n))
+    operands = dict(bias=randn(n, seed=1, dtype=dtype), mul=randn(m, n, seed=2, dtype=dtype),
+                    residual=randn(m, n, seed=3, dtype=dtype))
+    v = (torch.mm(q.double(), w.double().t().contiguous()) * scale.double()[:, None] * s_w.double()).cpu()
+    y = int8.awq_gemm_i8(q, scale, layer_of(w, s_w), n, k, act="gelu", dtype=dtype, **operands)
+    want, bound = ref.tail(v, dtype, "gelu", *operands.values(), 4 * ref.E * v.abs())
+    ref.check(y, want, bound)
+
+
+def test_gemm_i8_more_rows_than_a_launch_has():
+    """65535 blocks of rows go in one launch of the kernel that takes so little work a row, the others in
+    another."""
+    m, n, k = 65535 * 64 + 134, 8, 16
+    q, w = codes(m, k, seed=1), codes(n, k, seed=2)
+    scale, s_w = torch.rand(m, device=DEV) / 64, torch.rand(n, device=DEV) / 64
+    g = torch.Generator(device=DEV).manual_seed(3)
+    mul, residual = (torch.randn(m, n, generator=g, device=DEV).half() for _ in range(2))
+    y = int8.awq_gemm_i8(q, scale, layer_of(w, s_w), n, k, mul=mul, residual=residual)
+    for part in (slice(0, 70), slice(65535 * 64 - 70, m)):
+        want, bound = ref.gemm_i8(q[part], scale[part], w, s_w, F16, mul=mul[part], residual=residual[part])
+        ref.check(y[part], want, bound)
+
+
+@TYPES
+@pytest.mark.parametrize("tokens,hidden,experts,k", [(70, 8200, 1024, 8), (16, 16392, 1000, 4), (517, 4104, 130, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_of_many_channels(dtype, tokens, hidden, experts, k, score):
+    """Wavefronts that take several turns of the channels, with one tile of tokens and with two."""
+    x = randn(tokens, hidden, seed=tokens, dtype=dtype)
+    w = randn(experts, hidden, seed=experts, dtype=dtype, gain=2.0 * hidden ** -0.5)
+    ids, weights = moe.awq_moe_route(x, w, k, score=score)
+    want_ids, want = ref.route(x, w, k, score=score)
+    assert torch.equal(ids.cpu(), want_ids)
+    ref.check(weights, want, 2 * ref.E * want.abs() + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("width,first", [(8, 4 << 20), (1032, 1 << 20)])
+def test_more_rows_than_a_launch_has(width, first):
+    """Rows past the workgroups of a launch go in its workgroups' second turn."""
+    tokens = first + 5
+    g = torch.Generator(device=DEV).manual_seed(width)
+    x = torch.randn(tokens, width, generator=g, device=DEV, dtype=F16)
+    w = randn(width, seed=1)
+    got = int8.awq_rms_norm(x, w, i8=True)
+    q, s = int8.awq_quant_i8(x, w)
+    for part in (slice(0, 9), slice(first - 3, tokens)):
+        alone = int8.awq_rms_norm(x[part], w, i8=True)
+        assert all(same(a[part], b) for a, b in zip(got[:3], alone[:3]))
+        q1, s1 = int8.awq_quant_i8(x[part], w)
+        assert same(q[part], q1) and same(s[part], s1)
+        _, v, off = ref.norm(x[part], w, 1e-5)
+        ref.check(alone.y, v, off + ref.U[F16] * v.abs() + ref.TINY[F16])
