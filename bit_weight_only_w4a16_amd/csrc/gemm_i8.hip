@@ -27,11 +27,18 @@ struct I8Args {
   int K, units, act;
 };
 
+// A sum times both scales, in range wherever the result is: rows' scales reach 2^121 (bfloat16's largest
+// by 127) and sums 2^31, so the row's scale goes first with 2^-24 and the channel's with 2^24 after it.
+// (Powers of two: ordinary values have the bits that they have without them.)
+__device__ __forceinline__ float row_factor(float s) { return s * 0x1p-24f; }
+__device__ __forceinline__ float channel_factor(float s) { return s * 0x1p24f; }
+
 // outputs n, n + 1 of row m from their sums
 template <typename T>
 __device__ __forceinline__ void store2(const I8Args& a, int64_t m, int n, int s0, int s1) {
-  const float sx = a.scale[m];
-  float v[2] = {static_cast<float>(s0) * sx * a.scales[n], static_cast<float>(s1) * sx * a.scales[n + 1]};
+  const float sx = row_factor(a.scale[m]);
+  float v[2] = {static_cast<float>(s0) * sx * channel_factor(a.scales[n]),
+                static_cast<float>(s1) * sx * channel_factor(a.scales[n + 1])};
   const int64_t o = m * a.N + n;
   auto both = [&](const uint16_t* p, int64_t at, float* f) {
     const uint32_t w = *reinterpret_cast<const uint32_t*>(p + at);
@@ -351,14 +358,14 @@ __global__ void __launch_bounds__(256 * TEAMS, 2) i8_tile_kernel(I8Args a) {
   float8_t sw = {}, bias = {};
   if (in) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sw[e] = a.scales[n + e];
+    for (int e = 0; e < 8; ++e) sw[e] = channel_factor(a.scales[n + e]);
     if (a.bias != nullptr) bias = load8<T>(a.bias + n);
   }
   float sx[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int64_t m = m0 + wm * TM + 32 * i + l32;
-    sx[i] = m < a.M ? a.scale[m] : 0.0f;
+    sx[i] = m < a.M ? row_factor(a.scale[m]) : 0.0f;
   }
   if constexpr (TEAMS == 1) __syncthreads();  // all wavefronts have read their last operands
 #pragma unroll
@@ -416,12 +423,12 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
       }
     }
     const int64_t m = 8 * i / a.N, n = 8 * i - m * a.N;
-    const float sx = a.scale[m];
+    const float sx = row_factor(a.scale[m]);
     float8_t v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      v[e] = static_cast<float>(lo[e]) * sx * a.scales[n + e];
-      v[e + 4] = static_cast<float>(hi[e]) * sx * a.scales[n + 4 + e];
+      v[e] = static_cast<float>(lo[e]) * sx * channel_factor(a.scales[n + e]);
+      v[e + 4] = static_cast<float>(hi[e]) * sx * channel_factor(a.scales[n + 4 + e]);
     }
     if (a.bias != nullptr) v += load8<T>(a.bias + n);
     uint4 f = make_uint4(0, 0, 0, 0), r = f;

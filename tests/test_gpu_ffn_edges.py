@@ -324,3 +324,20 @@ def test_more_rows_than_a_launch_has(width, first):
         assert same(q[part], q1) and same(s[part], s1)
         _, v, off = ref.norm(x[part], w, 1e-5)
         ref.check(alone.y, v, off + ref.U[F16] * v.abs() + ref.TINY[F16])
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 520, 1040), *TILES.values()], ids=lambda v: str(v))
+def test_gemm_i8_of_rows_near_the_types_ends(m, n, k):
+    """Rows whose scale times their sum passes float32 and whose result does not, next to small and to
+    ordinary ones."""
+    q, w = codes(m, k, seed=m), codes(n, k, seed=k)
+    at = torch.arange(m, device=DEV) % 3
+    scale = torch.tensor([2.0 ** 118, 2.0 ** -100, 2.0 ** -7], device=DEV)[at] * 1.25
+    s_w = 2.0 ** -12 * (1.0 + torch.arange(n, device=DEV) % 5)
+    y = int8.awq_gemm_i8(q, scale, layer_of(w, s_w), n, k, dtype=BF16)
+    want = torch.mm(q.double(), w.double().t().contiguous()) * scale.double()[:, None] * s_w.double()
+    most = torch.finfo(BF16).max
+    over = want.abs() >= most * (1 - 2 * ref.U[BF16])
+    assert float(over.double().mean()) < 0.5
+    off = (ref.U[BF16] + 4 * ref.E) * want.abs() + ref.TINY[BF16]
+    assert bool(((y.double() - want).abs() <= off)[~over].all())
