@@ -112,14 +112,14 @@ __global__ void __launch_bounds__(THREADS < 256 ? 256 : THREADS) rows_kernel(Row
         down = kDown;
         mean = squares() / width + a.eps * kDown * kDown;  // 2^-152 itself is no float32
       }
-      r = 1.0f / sqrtf(mean);
+      r = down / sqrtf(mean);
     }
     auto values = [&](int i, float* v) {
       float f[8];
       widen<T>(h[i], v);
       widen<T>(w[i], f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = (NORM ? v[e] * down * r : v[e]) * f[e];
+      for (int e = 0; e < 8; ++e) v[e] = (NORM ? v[e] * r : v[e]) * f[e];
     };
     RowScale s = {0.0f, 0.0f};
     if (a.q != nullptr) {

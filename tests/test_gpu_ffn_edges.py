@@ -48,6 +48,17 @@ def test_rms_norm_large_eps_beside_squares_past_float32(eps, width):
     ref.check_rows8(got.q, got.scale, v, off)
 
 
+@pytest.mark.parametrize("width", [512, 4104])
+def test_rms_norm_small_values_beside_one_past_float32(width):
+    """A value whose square passes float32 does not cost the small ones of its row their bits, which a
+    large weight brings back."""
+    x = randn(2, width, seed=53, dtype=BF16) * 2.0 ** -66
+    x[0, 7], x[1, 11], x[1, 12] = 2.0 ** 64, -2.0 ** 66, 2.0 ** 63
+    w = randn(width, seed=54, dtype=BF16) * 2.0 ** 20
+    _, v, off = ref.norm(x, w, 1e-5)
+    ref.check(int8.awq_rms_norm(x, w).y, v, off + ref.U[BF16] * v.abs() + ref.TINY[BF16])
+
+
 def moe_weights(hidden=128, ffn=256, experts=4):
     return [randn(experts, *shape, seed=91 + i, gain=0.1)
             for i, shape in enumerate([(hidden,), (ffn, hidden), (ffn, hidden), (hidden, ffn)])]
