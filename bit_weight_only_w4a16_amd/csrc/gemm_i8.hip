@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // themselves: 142 us instead of 134 at 2048 x 14336 x 4096, 81 instead of 68 at 1000 x 11000 x 4080).
 // The only barrier of a step stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
-// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 132-135 us (1.8 POPS), of
-// which the products alone take 78.
+// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 129-140 us by the box (1.7 to
+// 1.9 POPS), of which the products alone take 64, the loads alone 61.
 
 typedef int int16_t_ __attribute__((ext_vector_type(16)));
 
@@ -440,7 +440,9 @@ __global__ void __launch_bounds__(256) i8_sum_kernel(I8Args a, int splits) {
 
 // Which kernel a product takes: the one with the least time by an estimate in microseconds, whose
 // constants were fitted (by least squares of the logarithms, 10 % rms) to 2400 timings of all
-// kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. Over
+// kernels and splits at M = 17 .. 4096 and seven layers from 512 x 2048 to 14336 x 4096. Only the order of
+// its times matters: they lie 3 to 26 % below what the kernels take now (2048 x 14336 x 4096 104 us for 122
+// to 130, 4096 x 4096 x 14336 164 for 207, 64 x 14336 x 4096 10.1 for 13.7, 333 x 4096 x 11008 30.2 for 31.2). Over
 // those sizes the choice costs 2.6 % more than the best one on average, 33 % at worst (33 x 8192 x
 // 1024: 6.5 us, 4.9); a fit of its own to the 1765 timings that say so would cost 2.5 %.
 // A CU's blocks share its matrix cores (`work` each and step) and pass their steps not faster than

@@ -6,15 +6,17 @@
 //
 // A row is read once and stays in registers; its sum of squares, and for 8-bit rows max|v| after
 // it, come from reductions over the row's threads, and every output is written from there. Memory
-// is the only bound of long inputs: 16384 x 8192 bfloat16 with a residual 186 us (5.8 TB/s), 2048 x 14336
-// to 8 bits 21 us (4.2 TB/s); one row of 4096 2.9 us, a launch, a trip to memory and a reduction.
+// is the only bound of long inputs: 16384 x 8192 bfloat16 with a residual 187 us (5.7 TB/s), 2048 x 14336
+// to 8 bits 20.5 us one call behind the other and 23.2 by itself (4.3 and 3.8 TB/s); one row of 4096 2.9
+// us, a launch, a trip to memory and a reduction.
 #include "ffn_internal.hpp"
 
 namespace awq {
 namespace {
 
 // Squares of rows past 2^63 overflow float32: such a row is summed times 2^-76 (the largest
-// bfloat16 2^128 squared times 2^15 elements stays below 2^120), and eps times 2^-152 with it.
+// bfloat16 2^128 squared times 2^15 elements stays below 2^120), and eps times 2^-152 with it; so is one
+// whose mean and eps pass it together.
 constexpr float kDown = 0x1p-76f;
 
 struct RowsArgs {
@@ -173,7 +175,8 @@ hipError_t launch_rows(const RowsArgs& a, hipStream_t st) {
 }
 
 // 16 rows of a packed 8-bit layer: 16 threads of a row find its largest value, then write its
-// units' 16-byte pieces.
+// units' 16-byte pieces, for which they read it again: once for a layer's life, 14336 x 4096 in 61 us and
+// 4096 x 14336, with a quarter of the workgroups, in 132 (read once, written once: 34).
 template <typename T>
 __global__ void __launch_bounds__(256)
     pack_i8_kernel(const uint16_t* w, const uint16_t* s_c, int64_t N, int64_t K, int64_t units, uint8_t* codes,

@@ -83,7 +83,8 @@ def awq_gemm_i8(q, scale, packed, n: int, k: int, *, bias=None, act: str = "none
 
 class Int8Linear:
     """A linear layer in 8 bits: rows are quantized as they come (or come quantized, from
-    awq_rms_norm), y = x . w^T."""
+    awq_rms_norm), y = x . w^T. It keeps a byte for each weight; beside an awq.QuantLinear of the same
+    weights, which single tokens take, that is about three times the 4-bit layer's bytes in all."""
 
     def __init__(self, packed, n: int, k: int, inv_s_c=None):
         self.packed, self.n, self.k, self.inv_s_c = packed, n, k, inv_s_c

@@ -30,8 +30,10 @@ extern "C" {
  * Rows: strides of x, residual, h_out and y in elements, of q in bytes; at least width,
  * multiples of 8. width is a multiple of 8, 8 <= width <= 32768. eps is at least 1e-30.
  * Sums are float32; rows whose squares pass its range are summed scaled down.
- * 8-bit rows: a row with no |v| above 1e-30 gets scale 0 and codes 0; one that holds a v that is
- * not finite gets scale NaN and codes 0 (the row of a product with it is NaN).
+ * 8-bit rows: s is formed as the float32 product of max|v| with float32's 1 / 127 (a unit in the
+ * last place beside the quotient at times), and q from the quotient by that s. A row with no |v|
+ * above 1e-30 gets scale 0 and codes 0; one that holds a v that is not finite gets scale NaN and
+ * codes 0 (the row of a product with it is NaN).
  */
 typedef struct awq_rms_norm_args {
   const void* x;        /* [tokens][width] */
@@ -95,7 +97,8 @@ int awq_pack_i8(const void* w, const void* s_c, int64_t N, int64_t K, int32_t dt
  *   y[m][n] = act(scale[m] * s[n] * sum over k of q[m][k] w[n][k] + bias[n]) * mul[m][n]
  *             + residual[m][n]
  * The sum over k is exact (32-bit integers); the rest is float32, rounded once to `dtype`,
- * which is that of bias, mul and residual too. act is AWQ_ACT_*. Codes may be -128 .. 127.
+ * which is that of bias, mul and residual too. The product of the sum and both scales stays in
+ * range where it is in range itself, for scales of channels below 2^104. act is AWQ_ACT_*. Codes may be -128 .. 127.
  * mul and residual may be y itself. q's rows are q_stride bytes apart (>= K, a multiple of
  * 16); y, mul and residual are contiguous. Limits of N and K are awq_pack_i8's; M < 2^30,
  * (M / 64 + 1) * (N / 16 + 1) <= 2^24 - 2^18.
@@ -134,7 +137,8 @@ int awq_gemm_i8(const awq_gemm_i8_args* args, hipStream_t stream);
  *            NaN stands behind all others
  *   weights[t][j] = scale * p[ids[t][j]], divided by their sum over j where renormalize != 0
  *            (0 where that sum is 0)
- * With a bias the softmax's choice is logit + bias too. k <= E <= 1024, k <= 32, tokens <=
+ * The bias is one for the choice alone, of logits or of sigmoids: not a linear router's bias,
+ * which its weights would show too, and not one that is added to softmax's probabilities. k <= E <= 1024, k <= 32, tokens <=
  * 2^20, hidden a multiple of 8 up to 65536; x's rows x_stride elements apart (a multiple of
  * 8), w contiguous.
  * ws: device, awq_moe_route_workspace_bytes() bytes, overwritten; may be NULL with ws_bytes == 0
@@ -176,7 +180,7 @@ int awq_moe_route(const awq_moe_route_args* args, hipStream_t stream);
  * experts with inv_in_stride == 0; inv_down [E][ffn] or [ffn] likewise; binary16, NULL: ones.
  * An id outside [0, E) takes part in nothing (an expert of another device); a token may name
  * an expert twice. A token without an expert gets its residual, or zeros. y may be x or
- * residual (the same address and stride).
+ * residual (the same address and stride). Values of a past binary16 (65504) are infinities.
  * hidden and ffn are multiples of 128 (and of group), E <= 1024, tokens <= AWQ_MOE_MAX_TOKENS,
  * k <= AWQ_MOE_MAX_K. Rows of x, residual and y are strides (elements, multiples of 8) apart.
  * ws: device, awq_moe_workspace_bytes() bytes, overwritten.
