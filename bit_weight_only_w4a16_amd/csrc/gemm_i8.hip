@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(512) i8_rows_kernel(I8Args a) {
 // themselves: 142 us instead of 134 at 2048 x 14336 x 4096, 81 instead of 68 at 1000 x 11000 x 4080).
 // The only barrier of a step stands before its second half, whose operands are in registers already.
 // v_mfma_i32_32x32x32_i8 takes W's fragment as its first operand, so that a lane's results are
-// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 129-140 us by the box (1.7 to
+// runs of four outputs of one row. 2048 x 14336 x 4096 with silu and a factor 129-140 us by the card (1.7 to
 // 1.9 POPS), of which the products alone take 64, the loads alone 61.
 
 typedef int int16_t_ __attribute__((ext_vector_type(16)));
