@@ -32,8 +32,8 @@ def awq_moe_route(x, w, k: int, bias=None, *, score: str = "softmax", renormaliz
     """(ids int32 [tokens, k], weights float32 [tokens, k]): the k experts of each token with the
     largest logits x . w^T (x [tokens, hidden], w [experts, hidden]; score "softmax"), or with the
     largest sigmoids of them (score "sigmoid"), in that order, ties to the lowest index. bias
-    (float32 [experts]) is added to the logits or sigmoids for the choice alone. weights are scale times the chosen scores,
-    divided by their sum if `renormalize`. Logits are summed in float64."""
+    (float32 [experts]) is added to the logits or sigmoids for the choice alone. weights are
+    scale times the chosen scores, divided by their sum if `renormalize`. Logits are summed in float64."""
     code = SCORES.get(score)
     if code is None:
         raise ValueError(f"score must be one of {tuple(SCORES)}")

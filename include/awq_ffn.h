@@ -98,8 +98,8 @@ int awq_pack_i8(const void* w, const void* s_c, int64_t N, int64_t K, int32_t dt
  *             + residual[m][n]
  * The sum over k is exact (32-bit integers); the rest is float32, rounded once to `dtype`,
  * which is that of bias, mul and residual too. The product of the sum and both scales stays in
- * range where it is in range itself, for scales of channels below 2^104. act is AWQ_ACT_*. Codes may be -128 .. 127.
- * mul and residual may be y itself. q's rows are q_stride bytes apart (>= K, a multiple of
+ * range where it is in range itself, for scales of channels below 2^104. act is AWQ_ACT_*.
+ * Codes may be -128 .. 127. mul and residual may be y itself. q's rows are q_stride bytes apart (>= K, a multiple of
  * 16); y, mul and residual are contiguous. Limits of N and K are awq_pack_i8's; M < 2^30,
  * (M / 64 + 1) * (N / 16 + 1) <= 2^24 - 2^18.
  * ws: device, awq_gemm_i8_workspace_bytes() bytes, overwritten; may be NULL with ws_bytes == 0
@@ -138,9 +138,9 @@ int awq_gemm_i8(const awq_gemm_i8_args* args, hipStream_t stream);
  *   weights[t][j] = scale * p[ids[t][j]], divided by their sum over j where renormalize != 0
  *            (0 where that sum is 0)
  * The bias is one for the choice alone, of logits or of sigmoids: not a linear router's bias,
- * which its weights would show too, and not one that is added to softmax's probabilities. k <= E <= 1024, k <= 32, tokens <=
- * 2^20, hidden a multiple of 8 up to 65536; x's rows x_stride elements apart (a multiple of
- * 8), w contiguous.
+ * which its weights would show too, and not one that is added to softmax's probabilities.
+ * k <= E <= 1024, k <= 32, tokens <= 2^20, hidden a multiple of 8 up to 65536; x's rows x_stride
+ * elements apart (a multiple of 8), w contiguous.
  * ws: device, awq_moe_route_workspace_bytes() bytes, overwritten; may be NULL with ws_bytes == 0
  * where that is 0 (a few tokens with a small router).
  */
